@@ -2,8 +2,8 @@
 
 ``native`` binds ``libseacells_fw.so`` (include/seacells_fw.h for the A and B
 updates, include/seacells_sparse.h for the operand construction,
-include/seacells_debug.h for the test hooks); ``csrc/``
-holds the HIP sources; ``_build`` compiles them in-tree.
+include/seacells_token.h for the token operators, include/seacells_debug.h for
+the test hooks); ``csrc/`` holds the HIP sources; ``_build`` compiles them in-tree.
 """
 from .native import (DeviceCSR, SeacellsError, load, new_status, raise_on_status,  # noqa: F401
                      seacells_fw_a_columns, seacells_fw_a_columns_pruned, seacells_fw_a_columns_noalloc,
@@ -20,4 +20,8 @@ from .native import (DeviceCSR, SeacellsError, load, new_status, raise_on_status
                      seacells_fw_a_to_csr_fill, fw_a_to_csr, outer_iteration, csr_trim,
                      seacells_debug_set_a_options, seacells_debug_b_layout,
                      seacells_debug_b_last_epoch, seacells_debug_b_reduce, status_flags,
-                     seacells_fw_step_size)
+                     seacells_fw_step_size,
+                     seacells_embed, seacells_embed_grad_workspace, seacells_embed_grad,
+                     seacells_layer_norm, seacells_layer_norm_grad_workspace,
+                     seacells_layer_norm_grad, seacells_logprobs_workspace, seacells_logprobs,
+                     seacells_logprobs_grad)

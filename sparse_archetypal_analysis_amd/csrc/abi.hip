@@ -10,13 +10,14 @@
 #include "seacells_debug.h"
 #include "seacells_fw.h"
 #include "seacells_sparse.h"
+#include "seacells_token.h"
 #include "common.hpp"
 
 namespace seacells {
 
 static thread_local char g_last_error[256] = "";
 
-static int hip_fail(hipError_t e, const char *what) {
+int hip_fail(hipError_t e, const char *what) {
   std::snprintf(g_last_error, sizeof g_last_error, "%s: %s", what, hipGetErrorString(e));
   return SEACELLS_E_HIP;
 }
@@ -537,6 +538,8 @@ const char *seacells_status_string(int code) {
       return "an operand exceeds the 32-bit index range";
     case SEACELLS_E_HIP:
       return "a HIP launch or query failed";
+    case SEACELLS_E_TYPE:
+      return "an element type is unknown or unsupported, or a pointer is misaligned";
     default:
       return "unknown status";
   }

@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t readlane_u32(uint32_t x, uint32_t lane) {
 }
 
 // ---------------------------------------------------------------------------
-// internal host interface (implemented in fw_a.hip / fw_b.hip)
+// internal host interface (implemented in abi.hip / fw_a.hip / fw_b.hip)
 // ---------------------------------------------------------------------------
 
 struct DeviceInfo {
@@ -110,6 +110,9 @@ struct DeviceInfo {
   int ok = 0;
 };
 hipError_t device_info(DeviceInfo *out);
+
+// SEACELLS_E_HIP, with the message kept for seacells_last_error().
+int hip_fail(hipError_t e, const char *what);
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

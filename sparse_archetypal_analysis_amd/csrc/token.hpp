@@ -1,0 +1,131 @@
+// Element access and reductions shared by the token operators (embedding,
+// layer norm, log probabilities), and their internal host interface. Nothing
+// here is exported.
+#pragma once
+
+#include "common.hpp"
+
+namespace seacells {
+
+// Device-side element types, same values as SEACELLS_F32 / F16 / BF16.
+enum class Dtype : uint32_t { f32 = 0, f16 = 1, bf16 = 2 };
+
+constexpr uint32_t kVecBytes = 16;  // one lane's load or store
+template <class T>
+constexpr uint32_t kVec = kVecBytes / sizeof(T);
+
+// 16 bytes of elements at any element-aligned address: the global memory path
+// takes dwordx4 accesses at any byte address, so odd widths, strides and
+// offsets need no variant of their own (a row that starts inside a 64-byte
+// line costs the wave one more line, not a narrower access).
+template <class T>
+using Vec = T __attribute__((ext_vector_type(kVec<T>), aligned(sizeof(T))));
+
+template <class T>
+__device__ __forceinline__ Vec<T> load_vec(const T *p) {
+  return *reinterpret_cast<const Vec<T> *>(p);
+}
+
+template <class T>
+__device__ __forceinline__ void store_vec(T *p, Vec<T> v) {
+  *reinterpret_cast<Vec<T> *>(p) = v;
+}
+
+// The elements of [at, end) that a lane's vector at `at` covers; those past
+// the end read as `fill`.
+template <class T>
+__device__ __forceinline__ Vec<T> load_vec_tail(const T *row, uint32_t at, uint32_t end, T fill) {
+  if (at + kVec<T> <= end) return load_vec(row + at);
+  Vec<T> v;
+#pragma unroll
+  for (uint32_t j = 0; j < kVec<T>; ++j) v[j] = at + j < end ? row[at + j] : fill;
+  return v;
+}
+
+template <class T>
+__device__ __forceinline__ void store_vec_tail(T *row, uint32_t at, uint32_t end, Vec<T> v) {
+  if (at + kVec<T> <= end) {
+    store_vec(row + at, v);
+    return;
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < kVec<T>; ++j)
+    if (at + j < end) row[at + j] = v[j];
+}
+
+// IEEE maximum: NaN if either side is (v_maximum3_f32 on gfx950).
+__device__ __forceinline__ float nan_max(float a, float b) {
+  return __builtin_elementwise_maximum(a, b);
+}
+
+// e^x for x <= 0 in one instruction beside the scaling (v_exp_f32, 1 ulp; the
+// product's rounding adds |x| 2^-24 relative).
+__device__ __forceinline__ float exp_neg(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
+}
+
+inline bool dtype_known(uint32_t t) { return t <= 2u; }
+inline uint32_t dtype_size(uint32_t t) { return t == 0u ? 4u : 2u; }
+inline uint32_t div_up(uint64_t a, uint64_t b) { return (uint32_t)((a + b - 1) / b); }
+
+// Calls f(T{}) with the element type of a dtype code.
+template <class F>
+hipError_t with_type(uint32_t t, F &&f) {
+  switch (static_cast<Dtype>(t)) {
+    case Dtype::f32:
+      return f(float{});
+    case Dtype::f16:
+      return f(_Float16{});
+    default:
+      return f(__bf16{});
+  }
+}
+
+// --- host interface ---------------------------------------------------------
+
+hipError_t launch_embed(const void *table, uint32_t dtype, uint32_t v, uint32_t d, uint64_t table_ld,
+                        const int32_t *tokens, uint32_t n, float scale, void *out, uint64_t out_ld,
+                        uint32_t *status, hipStream_t stream);
+
+struct EmbedGradPlan {
+  uint32_t ids;     // table rows per block of the token sort
+  uint32_t blocks;  // blocks of the token sort
+  size_t off_perm, off_start;
+  size_t ws_bytes;
+};
+EmbedGradPlan plan_embed_grad(uint32_t n, uint32_t v, uint32_t d);
+hipError_t launch_embed_grad(const EmbedGradPlan &plan, const int32_t *tokens, uint32_t n,
+                             const void *d_out, uint32_t d_out_type, uint64_t d_out_ld, uint32_t v,
+                             uint32_t d, float scale, const void *add_to, void *d_table,
+                             uint32_t d_table_type, uint64_t d_table_ld, void *ws, uint32_t *status,
+                             hipStream_t stream);
+
+hipError_t launch_layer_norm(const void *x, uint32_t dtype, uint32_t n, uint32_t d, uint64_t x_ld,
+                             const void *weight, const void *bias, uint32_t weight_type, float eps,
+                             void *out, uint64_t out_ld, float *mean, float *rstd,
+                             hipStream_t stream);
+
+struct NormGradPlan {
+  uint32_t parts;  // row parts of the weight's and bias' sums
+  size_t ws_bytes;
+};
+NormGradPlan plan_layer_norm_grad(uint32_t n, uint32_t d);
+hipError_t launch_layer_norm_grad(const NormGradPlan &plan, const void *d_out, uint64_t d_out_ld,
+                                  const void *x, uint32_t dtype, uint32_t n, uint32_t d,
+                                  uint64_t x_ld, const float *mean, const float *rstd,
+                                  const void *weight, uint32_t weight_type, void *d_x,
+                                  uint64_t d_x_ld, void *d_weight, void *d_bias, void *ws,
+                                  hipStream_t stream);
+
+size_t logprobs_workspace(uint32_t n, uint32_t v, uint32_t top_k);
+hipError_t launch_logprobs(const void *logits, uint32_t dtype, uint32_t n, uint32_t v, uint64_t ld,
+                           const int32_t *targets, uint32_t top_k, float *logp, float *entropy,
+                           float *stats, int32_t *top_idx, float *top_logp, void *ws,
+                           uint32_t *status, hipStream_t stream);
+hipError_t launch_logprobs_grad(const void *logits, uint32_t dtype, uint32_t n, uint32_t v,
+                                uint64_t ld, const int32_t *targets, const float *stats,
+                                const float *entropy, const float *d_logp, const float *d_entropy,
+                                void *d_logits, uint64_t d_logits_ld, uint32_t *status,
+                                hipStream_t stream);
+
+}  // namespace seacells

@@ -1,5 +1,5 @@
 """Thin ctypes binding of ``libseacells_fw.so`` (include/seacells_fw.h,
-include/seacells_sparse.h, include/seacells_debug.h).
+include/seacells_sparse.h, include/seacells_token.h, include/seacells_debug.h).
 
 The functions carry the C names and only marshal arguments: device tensors
 become raw pointers, torch's current stream becomes the hipStream_t. Every
@@ -19,7 +19,8 @@ import torch
 from . import _build
 
 SEACELLS_OK = 0
-ERRORS = {-1: "E_NULL", -2: "E_SHAPE", -3: "E_WORKSPACE", -4: "E_TOO_LARGE", -5: "E_HIP"}
+ERRORS = {-1: "E_NULL", -2: "E_SHAPE", -3: "E_WORKSPACE", -4: "E_TOO_LARGE", -5: "E_HIP",
+          -6: "E_TYPE"}
 FLAGS = {0x1: "CAP_OVERFLOW", 0x2: "PARTIALS_INVALID", 0x4: "B_CAP_OVERFLOW", 0x8: "BAD_INDEX",
          0x10: "NONFINITE", 0x20: "BAD_GAMMA", 0x40: "OUTPUT_TOO_LARGE"}
 
@@ -34,6 +35,9 @@ EXPORTS = ("seacells_fw_a_columns_workspace", "seacells_fw_a_columns",
            "seacells_fw_b_vertex_workspace", "seacells_fw_b_vertex",
            "seacells_fw_a_to_csr_workspace", "seacells_fw_a_to_csr_rows",
            "seacells_fw_a_to_csr_fill",
+           "seacells_embed", "seacells_embed_grad_workspace", "seacells_embed_grad",
+           "seacells_layer_norm", "seacells_layer_norm_grad_workspace", "seacells_layer_norm_grad",
+           "seacells_logprobs_workspace", "seacells_logprobs", "seacells_logprobs_grad",
            "seacells_debug_set_a_options", "seacells_debug_b_layout",
            "seacells_debug_b_last_epoch", "seacells_debug_b_reduce",
            "seacells_fw_step_size",
@@ -61,6 +65,9 @@ class seacells_b_layout(ctypes.Structure):
 _CSR_P = ctypes.POINTER(seacells_csr)
 _VP = ctypes.c_void_p
 _U32 = ctypes.c_uint32
+_U64 = ctypes.c_uint64
+_F32 = ctypes.c_float
+_SIZE = ctypes.c_size_t
 _lib = None
 
 
@@ -140,6 +147,29 @@ def load():
     lib.seacells_fw_a_to_csr_fill.restype = ctypes.c_int
     lib.seacells_fw_a_to_csr_fill.argtypes = [_VP, _VP, _VP, _U32, _U32, _U32, _VP, _VP, _VP,
                                               _VP, _VP]
+    lib.seacells_embed.restype = ctypes.c_int
+    lib.seacells_embed.argtypes = [_VP, _U32, _U32, _U32, _U64, _VP, _U32, _F32, _VP, _U64, _VP, _VP]
+    lib.seacells_embed_grad_workspace.restype = _SIZE
+    lib.seacells_embed_grad_workspace.argtypes = [_U32, _U32, _U32]
+    lib.seacells_embed_grad.restype = ctypes.c_int
+    lib.seacells_embed_grad.argtypes = [_VP, _U32, _VP, _U32, _U64, _U32, _U32, _F32, _VP, _VP, _U32,
+                                        _U64, _VP, _SIZE, _VP, _VP]
+    lib.seacells_layer_norm.restype = ctypes.c_int
+    lib.seacells_layer_norm.argtypes = [_VP, _U32, _U32, _U32, _U64, _VP, _VP, _U32, _F32, _VP, _U64,
+                                        _VP, _VP, _VP]
+    lib.seacells_layer_norm_grad_workspace.restype = _SIZE
+    lib.seacells_layer_norm_grad_workspace.argtypes = [_U32, _U32]
+    lib.seacells_layer_norm_grad.restype = ctypes.c_int
+    lib.seacells_layer_norm_grad.argtypes = [_VP, _U64, _VP, _U32, _U32, _U32, _U64, _VP, _VP, _VP,
+                                             _U32, _VP, _U64, _VP, _VP, _VP, _SIZE, _VP]
+    lib.seacells_logprobs_workspace.restype = _SIZE
+    lib.seacells_logprobs_workspace.argtypes = [_U32, _U32, _U32]
+    lib.seacells_logprobs.restype = ctypes.c_int
+    lib.seacells_logprobs.argtypes = [_VP, _U32, _U32, _U32, _U64, _VP, _U32, _VP, _VP, _VP, _VP, _VP,
+                                      _VP, _SIZE, _VP, _VP]
+    lib.seacells_logprobs_grad.restype = ctypes.c_int
+    lib.seacells_logprobs_grad.argtypes = [_VP, _U32, _U32, _U32, _U64, _VP, _VP, _VP, _VP, _VP, _VP,
+                                           _U64, _VP, _VP]
     lib.seacells_debug_set_a_options.restype = ctypes.c_int
     lib.seacells_debug_set_a_options.argtypes = [ctypes.POINTER(seacells_a_options)]
     lib.seacells_debug_b_layout.restype = ctypes.c_int
@@ -878,3 +908,295 @@ def outer_iteration(K: DeviceCSR, b: DeviceCSR, k2b: DeviceCSR, a_t: DeviceCSR, 
     raise_on_status(status)
     return {"b": b2, "k2b": k2b2, "a_t": a_t2, "t1": t1, "aat": aat, "k2at": k2at, "rss": acc,
             "a_trace": tr, "b_picks": picks, "b_mins": mins, "b_gaps": gaps}
+
+
+# --------------------------------------------------------------------------
+# token operators (include/seacells_token.h)
+# --------------------------------------------------------------------------
+#
+# Row operands are [..., d] tensors of float32, float16 or bfloat16 with
+# consecutive elements in a row and one stride between rows. Outputs,
+# workspace and status are allocated on the call's stream when not given.
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+TOP_MAX = 64  # SEACELLS_TOP_MAX
+
+
+def _rows(t, name, dev=None):
+    """(tensor as [n, d], row stride) of a row operand."""
+    if t.dim() != 2:
+        try:
+            t = t.view(-1, t.shape[-1])
+        except (RuntimeError, IndexError):
+            raise SeacellsError("%s: the rows have no common stride" % name) from None
+    if not t.is_cuda or t.dtype not in _DTYPES or (dev is not None and t.get_device() != dev):
+        raise SeacellsError("%s must be a float32, float16 or bfloat16 tensor on the call's GPU"
+                            % name)
+    n, d = t.shape
+    ld, step = t.stride()
+    if d > 1 and step != 1:
+        raise SeacellsError("%s: a row's elements must be consecutive" % name)
+    if n < 2:
+        ld = d
+    elif ld < d:
+        raise SeacellsError("%s: rows overlap (stride %d < %d)" % (name, ld, d))
+    return t, ld
+
+
+def _out_rows(t, name, n, d, dev, dtype):
+    t2, ld = _rows(t, name, dev)
+    if t2.shape[0] != n or t2.shape[1] != d or t2.dtype != dtype:
+        raise SeacellsError("%s must be [%d, %d] of %s" % (name, n, d, dtype))
+    return ld
+
+
+def _vector(t, name, numel, dev, *dtypes):
+    """The pointer of a contiguous vector operand (None: a NULL pointer)."""
+    if t is None:
+        return None
+    if (t.dtype not in dtypes or t.numel() != numel or not t.is_contiguous()
+            or t.get_device() != dev):
+        raise SeacellsError("%s must be contiguous, on the call's GPU, of %d elements of %s"
+                            % (name, numel, " or ".join(map(str, dtypes))))
+    return t.data_ptr()
+
+
+def _new(shape, dtype, dev, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device="cuda:%d" % dev)
+    with torch.cuda.stream(stream):  # the block belongs to the stream that writes it
+        return torch.empty(shape, dtype=dtype, device="cuda:%d" % dev)
+
+
+def _workspace(ws, size, dev, stream):
+    if size == 0:
+        return None, 0, None
+    if ws is None:
+        ws = _new(size, torch.uint8, dev, stream)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise SeacellsError("workspace must be a contiguous tensor on the call's GPU")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def _enqueue(fn, dev, stream, *args):
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != SEACELLS_OK:
+        _check_rc(rc)
+
+
+def seacells_embed(table, tokens, scale=1.0, out=None, status=None, stream=None):
+    """out[i] = scale * table[tokens[i]]; a negative token gives zeros.
+
+    table [v, d]; tokens int32 of any shape. Returns (out [*tokens.shape, d],
+    status).
+    """
+    lib = load()
+    tab, ld = _rows(table, "table")
+    v, d = tab.shape
+    dev, dt, n = tab.get_device(), tab.dtype, tokens.numel()
+    tok = _vector(tokens, "tokens", n, dev, torch.int32)
+    if out is None:
+        out = _new((*tokens.shape, d), dt, dev, stream)
+    out_ld = _out_rows(out, "out", n, d, dev, dt)
+    if status is None:
+        status = _new(1, torch.int32, dev, stream)
+    _enqueue(lib.seacells_embed, dev, stream, tab.data_ptr(), _DTYPES[dt], v, d, ld, tok, n, scale,
+             out.data_ptr(), out_ld, _vector(status, "status", 1, dev, torch.int32))
+    return out, status
+
+
+def seacells_embed_grad_workspace(n, v, d) -> int:
+    return int(load().seacells_embed_grad_workspace(n, v, d))
+
+
+def seacells_embed_grad(tokens, d_out, v: int, scale=1.0, add_to=None, d_table=None,
+                        workspace=None, status=None, stream=None):
+    """Gradient of seacells_embed's table: add_to + scale * the sums of d_out's
+    rows by token. Returns (d_table [v, d], status).
+
+    d_table is of d_out's type or float32 (default: add_to's type, else
+    d_out's). add_to (same type and strides) may be d_table itself.
+    """
+    lib = load()
+    dy, dy_ld = _rows(d_out, "d_out")
+    n, d = dy.shape
+    dev, dt = dy.get_device(), dy.dtype
+    tok = _vector(tokens, "tokens", n, dev, torch.int32)
+    if d_table is None:
+        d_table = _new((v, d), dt if add_to is None else add_to.dtype, dev, stream)
+    ot = d_table.dtype
+    if ot != dt and ot != torch.float32:
+        raise SeacellsError("d_table must be of d_out's type or float32")
+    t_ld = _out_rows(d_table, "d_table", v, d, dev, ot)
+    add = None
+    if add_to is not None:
+        if _out_rows(add_to, "add_to", v, d, dev, ot) != t_ld:
+            raise SeacellsError("add_to and d_table must have the same row stride")
+        add = add_to.data_ptr()
+    if status is None:
+        status = _new(1, torch.int32, dev, stream)
+    ws, ws_bytes, keep = _workspace(workspace, lib.seacells_embed_grad_workspace(n, v, d), dev,
+                                    stream)
+    _enqueue(lib.seacells_embed_grad, dev, stream, tok, n, dy.data_ptr(), _DTYPES[dt], dy_ld, v, d,
+             scale, add, d_table.data_ptr(), _DTYPES[ot], t_ld, ws, ws_bytes,
+             _vector(status, "status", 1, dev, torch.int32))
+    return d_table, status
+
+
+def seacells_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, mean=None, rstd=None,
+                        stream=None):
+    """Layer norm over the last dimension. Returns (out, mean, rstd); mean and
+    rstd are float32 of one entry per row (what the gradient needs).
+
+    weight and bias [d] share a type: x's or float32. out may be x.
+    """
+    lib = load()
+    xr, ld = _rows(x, "x")
+    n, d = xr.shape
+    dev, dt = xr.get_device(), xr.dtype
+    wt = weight.dtype if weight is not None else bias.dtype if bias is not None else dt
+    if wt != dt and wt != torch.float32:
+        raise SeacellsError("weight and bias must be of x's type or float32")
+    w = _vector(weight, "weight", d, dev, wt)
+    b = _vector(bias, "bias", d, dev, wt)
+    if out is None:
+        out = _new(x.shape, dt, dev, stream)
+    out_ld = _out_rows(out, "out", n, d, dev, dt)
+    if mean is None:
+        mean = _new(x.shape[:-1], torch.float32, dev, stream)
+    if rstd is None:
+        rstd = _new(x.shape[:-1], torch.float32, dev, stream)
+    _enqueue(lib.seacells_layer_norm, dev, stream, xr.data_ptr(), _DTYPES[dt], n, d, ld, w, b,
+             _DTYPES[wt], eps, out.data_ptr(), out_ld,
+             _vector(mean, "mean", n, dev, torch.float32),
+             _vector(rstd, "rstd", n, dev, torch.float32))
+    return out, mean, rstd
+
+
+def seacells_layer_norm_grad_workspace(n, d) -> int:
+    return int(load().seacells_layer_norm_grad_workspace(n, d))
+
+
+def seacells_layer_norm_grad(d_out, x, mean, rstd, weight=None, d_x=None, d_weight=None,
+                             d_bias=None, workspace=None, stream=None):
+    """Gradients of seacells_layer_norm. Returns (d_x, d_weight, d_bias), the
+    latter two of weight's type (x's without a weight).
+
+    d_x may be d_out or x. False for d_x, d_weight or d_bias leaves it out
+    (returned as None).
+    """
+    lib = load()
+    xr, ld = _rows(x, "x")
+    n, d = xr.shape
+    dev, dt = xr.get_device(), xr.dtype
+    dy, dy_ld = _rows(d_out, "d_out", dev)
+    if dy.shape != xr.shape or dy.dtype != dt:
+        raise SeacellsError("d_out must have x's shape and type")
+    wt = weight.dtype if weight is not None else dt
+    if wt != dt and wt != torch.float32:
+        raise SeacellsError("weight must be of x's type or float32")
+    w = _vector(weight, "weight", d, dev, wt)
+    dx_ld = d
+    if d_x is False:
+        d_x = None
+    else:
+        if d_x is None:
+            d_x = _new(x.shape, dt, dev, stream)
+        dx_ld = _out_rows(d_x, "d_x", n, d, dev, dt)
+    d_weight = (None if d_weight is False
+                else _new(d, wt, dev, stream) if d_weight is None else d_weight)
+    d_bias = None if d_bias is False else _new(d, wt, dev, stream) if d_bias is None else d_bias
+    ws, ws_bytes, keep = _workspace(workspace, lib.seacells_layer_norm_grad_workspace(n, d), dev,
+                                    stream)
+    _enqueue(lib.seacells_layer_norm_grad, dev, stream, dy.data_ptr(), dy_ld, xr.data_ptr(),
+             _DTYPES[dt], n, d, ld, _vector(mean, "mean", n, dev, torch.float32),
+             _vector(rstd, "rstd", n, dev, torch.float32), w, _DTYPES[wt],
+             None if d_x is None else d_x.data_ptr(), dx_ld,
+             _vector(d_weight, "d_weight", d, dev, wt), _vector(d_bias, "d_bias", d, dev, wt), ws,
+             ws_bytes)
+    return d_x, d_weight, d_bias
+
+
+def seacells_logprobs_workspace(n, v, top_k=0) -> int:
+    return int(load().seacells_logprobs_workspace(n, v, top_k))
+
+
+def seacells_logprobs(logits, targets=None, top_k=0, logp=None, entropy=None, stats=None,
+                      top_idx=None, top_logp=None, workspace=None, status=None, stream=None):
+    """Log probabilities of the target classes, entropies and top alternatives
+    of rows of logits [..., v].
+
+    Returns (logp, entropy, stats, top_idx, top_logp, status): logp (None
+    without targets) and entropy of one float32 per row, stats [..., 2] (row
+    maximum, log sum exp(x - maximum)), top_idx int32 and top_logp [...,
+    top_k] (None for top_k = 0). targets int32, negative: ignored (logp 0).
+    """
+    lib = load()
+    x, ld = _rows(logits, "logits")
+    n, v = x.shape
+    dev, lead = x.get_device(), logits.shape[:-1]
+    tgt = _vector(targets, "targets", n, dev, torch.int32)
+    if not 0 <= top_k <= TOP_MAX:
+        raise SeacellsError("top_k must be 0 to %d" % TOP_MAX)
+    if targets is None:
+        logp = None
+    elif logp is None:
+        logp = _new(lead, torch.float32, dev, stream)
+    if entropy is None:
+        entropy = _new(lead, torch.float32, dev, stream)
+    if stats is None:
+        stats = _new((*lead, 2), torch.float32, dev, stream)
+    if top_k == 0:
+        top_idx = top_logp = None
+    else:
+        if top_idx is None:
+            top_idx = _new((*lead, top_k), torch.int32, dev, stream)
+        if top_logp is None:
+            top_logp = _new((*lead, top_k), torch.float32, dev, stream)
+    if status is None:
+        status = _new(1, torch.int32, dev, stream)
+    ws, ws_bytes, keep = _workspace(workspace, lib.seacells_logprobs_workspace(n, v, top_k), dev,
+                                    stream)
+    _enqueue(lib.seacells_logprobs, dev, stream, x.data_ptr(), _DTYPES[x.dtype], n, v, ld, tgt,
+             top_k, _vector(logp, "logp", n, dev, torch.float32),
+             _vector(entropy, "entropy", n, dev, torch.float32),
+             _vector(stats, "stats", 2 * n, dev, torch.float32),
+             _vector(top_idx, "top_idx", n * top_k, dev, torch.int32),
+             _vector(top_logp, "top_logp", n * top_k, dev, torch.float32), ws, ws_bytes,
+             _vector(status, "status", 1, dev, torch.int32))
+    return logp, entropy, stats, top_idx, top_logp, status
+
+
+def seacells_logprobs_grad(logits, targets, stats, entropy=None, d_logp=None, d_entropy=None,
+                           d_logits=None, status=None, stream=None):
+    """Gradient of sum(d_logp * logp + d_entropy * entropy) to the logits.
+    Returns (d_logits, status). d_logits may be logits.
+
+    stats and entropy as seacells_logprobs returned them (entropy only with
+    d_entropy); targets may be None (no part of d_logp).
+    """
+    lib = load()
+    x, ld = _rows(logits, "logits")
+    n, v = x.shape
+    dev, dt = x.get_device(), x.dtype
+    if d_logits is None:
+        d_logits = _new(logits.shape, dt, dev, stream)
+    d_ld = _out_rows(d_logits, "d_logits", n, v, dev, dt)
+    if d_entropy is not None and entropy is None:
+        raise SeacellsError("d_entropy needs the entropies")
+    if status is None:
+        status = _new(1, torch.int32, dev, stream)
+    _enqueue(lib.seacells_logprobs_grad, dev, stream, x.data_ptr(), _DTYPES[dt], n, v, ld,
+             _vector(targets, "targets", n, dev, torch.int32),
+             _vector(stats, "stats", 2 * n, dev, torch.float32),
+             _vector(entropy, "entropy", n, dev, torch.float32),
+             _vector(d_logp, "d_logp", n, dev, torch.float32),
+             _vector(d_entropy, "d_entropy", n, dev, torch.float32), d_logits.data_ptr(), d_ld,
+             _vector(status, "status", 1, dev, torch.int32))
+    return d_logits, status
