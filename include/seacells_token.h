@@ -49,6 +49,10 @@ extern "C" {
  * to its element (return value). */
 #define SEACELLS_E_TYPE (-6)
 
+/* Longest row (elements of an embedding, a norm or a row of logits); row
+ * counts and table rows may go to 2^31 - 1. SEACELLS_E_TOO_LARGE above. */
+#define SEACELLS_MAX_WIDTH (1u << 23)
+
 /* Most alternatives that seacells_logprobs returns per row. */
 #define SEACELLS_TOP_MAX 64u
 

@@ -11,6 +11,7 @@ using namespace seacells;
 namespace {
 
 constexpr uint32_t kTooLarge = 0x80000000u;
+constexpr uint32_t kMaxWidth = SEACELLS_MAX_WIDTH;
 
 bool aligned(const void *p, uint32_t dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (dtype_size(dtype) - 1u)) == 0;
@@ -19,7 +20,7 @@ bool aligned(const void *p, uint32_t dtype) {
 // Rows of d elements: sizes in range, the stride at least the row's length.
 int check_rows(uint32_t n, uint32_t d, uint64_t ld) {
   if (d == 0 || ld < d) return SEACELLS_E_SHAPE;
-  if (n >= kTooLarge || d >= kTooLarge || ld >= (1ull << 40)) return SEACELLS_E_TOO_LARGE;
+  if (n >= kTooLarge || d > kMaxWidth || ld >= (1ull << 40)) return SEACELLS_E_TOO_LARGE;
   return SEACELLS_OK;
 }
 
@@ -57,7 +58,7 @@ int seacells_embed(const void *table, uint32_t dtype, uint32_t v, uint32_t d, ui
 }
 
 size_t seacells_embed_grad_workspace(uint32_t n, uint32_t v, uint32_t d) {
-  if (v == 0 || d == 0 || n >= kTooLarge || v >= kTooLarge || d >= kTooLarge) return 0;
+  if (v == 0 || d == 0 || n >= kTooLarge || v >= kTooLarge || d > kMaxWidth) return 0;
   return plan_embed_grad(n, v, d).ws_bytes;
 }
 
@@ -107,7 +108,7 @@ int seacells_layer_norm(const void *x, uint32_t dtype, uint32_t n, uint32_t d, u
 }
 
 size_t seacells_layer_norm_grad_workspace(uint32_t n, uint32_t d) {
-  if (d == 0 || n >= kTooLarge || d >= kTooLarge) return 0;
+  if (d == 0 || n >= kTooLarge || d > kMaxWidth) return 0;
   return plan_layer_norm_grad(n, d).ws_bytes;
 }
 
@@ -138,7 +139,7 @@ int seacells_layer_norm_grad(const void *d_out, uint64_t d_out_ld, const void *x
 }
 
 size_t seacells_logprobs_workspace(uint32_t n, uint32_t v, uint32_t top_k) {
-  if (v == 0 || n >= kTooLarge || v >= kTooLarge || top_k > SEACELLS_TOP_MAX) return 0;
+  if (v == 0 || n >= kTooLarge || v > kMaxWidth || top_k > SEACELLS_TOP_MAX) return 0;
   return logprobs_workspace(n, v, top_k);
 }
 

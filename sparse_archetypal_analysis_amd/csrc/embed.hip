@@ -162,31 +162,188 @@ __global__ void __launch_bounds__(kSortThreads)
 
 // --- table gradient ---------------------------------------------------------
 
-template <class T, class O>
-__global__ void __launch_bounds__(kThreads)
-    embed_grad_rows_kernel(const uint32_t *__restrict__ perm, const uint32_t *__restrict__ start,
-                           const T *__restrict__ d_out, uint64_t d_out_ld, uint32_t v, uint32_t d,
-                           float scale, const O *add_to, O *d_table, uint64_t d_table_ld) {
-  constexpr uint32_t kV = kVec<T> < kVec<O> ? kVec<T> : kVec<O>;
-  const uint32_t lane = lane_id();
-  const uint32_t waves = gridDim.x * (kThreads / kWave);
-  for (uint64_t t = blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave; t < v; t += waves) {
-    const uint32_t p0 = start[t], p1 = start[t + 1];
-    if (p0 == p1 && add_to == d_table) continue;
-    for (uint32_t c = lane * kV; c < d; c += kWave * kV) {
-      float acc[kV] = {};
-      for (uint32_t p = p0; p < p1; ++p) {
-        const T *row = d_out + (uint64_t)perm[p] * d_out_ld;
+// Ids with more tokens than this ("heavy") are summed in parts, one part per
+// window of kHeavy sorted positions, so that a token that fills a third of
+// the batch does not leave its row to one wave.
+constexpr uint32_t kHeavy = 32;
+constexpr uint32_t kRowUnroll = 8;  // rows of d_y in flight per lane
+
+// How the lanes cover the columns: `lanes` (a power of two, at most a wave)
+// side by side with `chunks` vectors each, then further slabs (grid y).
+struct Cover {
+  uint32_t lanes, chunks, slabs;
+};
+
+template <uint32_t kV>
+Cover cover(uint32_t d) {
+  Cover c{};
+  const uint32_t vecs = div_up(d, kV);
+  c.lanes = 1;
+  while (c.lanes < kWave && c.lanes < vecs) c.lanes *= 2;
+  const uint32_t per = div_up(vecs, c.lanes);
+  c.chunks = per <= 1 ? 1 : per <= 2 ? 2 : 4;
+  c.slabs = div_up(vecs, c.lanes * c.chunks);
+  return c;
+}
+
+// acc += the rows perm[p0 .. p1) of d_y in order, columns c0 + chunk * step.
+template <class T, uint32_t kC>
+__device__ __forceinline__ void sum_rows(const uint32_t *__restrict__ perm, uint32_t p0, uint32_t p1,
+                                         const T *__restrict__ d_out, uint64_t ld, uint32_t c0,
+                                         uint32_t step, uint32_t d, float (&acc)[kC][kVec<T>]) {
+  constexpr uint32_t kU = kRowUnroll / kC > 1 ? kRowUnroll / kC : 2;
+  for (uint32_t p = p0; p < p1; p += kU) {
+    Vec<T> x[kU][kC];
 #pragma unroll
-        for (uint32_t j = 0; j < kV; ++j) acc[j] += c + j < d ? (float)row[c + j] : 0.0f;
-      }
+    for (uint32_t u = 0; u < kU; ++u) {
+      const T *row = d_out + (uint64_t)perm[p + u < p1 ? p + u : p] * ld;
 #pragma unroll
-      for (uint32_t j = 0; j < kV; ++j) {
-        if (c + j >= d) continue;
-        const float so_far = add_to != nullptr ? (float)add_to[t * d_table_ld + c + j] : 0.0f;
-        d_table[t * d_table_ld + c + j] = (O)(so_far + scale * acc[j]);
+      for (uint32_t k = 0; k < kC; ++k) {
+        const uint32_t c = c0 + k * step;
+        x[u][k] = p + u < p1 && c < d ? load_vec_tail(row, c, d, (T)0.0f) : Vec<T>{};
       }
     }
+#pragma unroll
+    for (uint32_t u = 0; u < kU; ++u)
+#pragma unroll
+      for (uint32_t k = 0; k < kC; ++k)
+#pragma unroll
+        for (uint32_t j = 0; j < kVec<T>; ++j) acc[k][j] += (float)x[u][k][j];
+  }
+}
+
+template <class O, uint32_t kV>
+using Out = O __attribute__((ext_vector_type(kV), aligned(sizeof(O))));
+
+// d_table[t, c ..] = so_far + scale * acc
+template <class O, uint32_t kV>
+__device__ __forceinline__ void write_row(const O *so_far, O *to, uint32_t c, uint32_t d,
+                                          float scale, const float (&acc)[kV]) {
+  if (c + kV <= d) {
+    Out<O, kV> y;
+    if (so_far != nullptr) {
+      const Out<O, kV> a = *reinterpret_cast<const Out<O, kV> *>(so_far + c);
+#pragma unroll
+      for (uint32_t j = 0; j < kV; ++j) y[j] = (O)((float)a[j] + scale * acc[j]);
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < kV; ++j) y[j] = (O)(scale * acc[j]);
+    }
+    *reinterpret_cast<Out<O, kV> *>(to + c) = y;
+    return;
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < kV; ++j)
+    if (c + j < d) to[c + j] = (O)((so_far != nullptr ? (float)so_far[c + j] : 0.0f) + scale * acc[j]);
+}
+
+// One group of lanes per unit: first the windows of sorted positions (parts
+// of heavy ids), then the table rows. A window meets at most two heavy ids,
+// one at each end; part[2 w] holds the sum of the one that covers its first
+// position, part[2 w + 1] of one that starts inside it.
+template <class T, class O, uint32_t kC>
+__global__ void __launch_bounds__(kThreads)
+    embed_grad_rows_kernel(const uint32_t *__restrict__ perm, const uint32_t *__restrict__ start,
+                           const int32_t *__restrict__ tokens, uint32_t windows, uint32_t lanes,
+                           const T *__restrict__ d_out, uint64_t d_out_ld, uint32_t v, uint32_t d,
+                           float scale, const O *add_to, O *d_table, uint64_t d_table_ld,
+                           float *__restrict__ part) {
+  constexpr uint32_t kV = kVec<T>;
+  const uint32_t step = lanes * kV;
+  const uint32_t c0 = blockIdx.y * step * kC + (threadIdx.x & (lanes - 1)) * kV;
+  const uint32_t per_block = kThreads / lanes;
+  const uint64_t units = (uint64_t)windows + v;
+  for (uint64_t unit = (uint64_t)blockIdx.x * per_block + threadIdx.x / lanes; unit < units;
+       unit += (uint64_t)gridDim.x * per_block) {
+    if (unit < windows) {
+      const uint32_t a = (uint32_t)unit * kHeavy;
+      const uint32_t kept = start[v];
+      if (a >= kept) continue;
+      const uint32_t b = a + kHeavy < kept ? a + kHeavy : kept;
+      const uint32_t first = (uint32_t)tokens[perm[a]], last = (uint32_t)tokens[perm[b - 1]];
+      for (uint32_t k = 0; k < 2; ++k) {
+        const uint32_t id = k == 0 ? first : last;
+        if (k == 1 && last == first) break;
+        const uint32_t s0 = start[id], s1 = start[id + 1];
+        if (s1 - s0 <= kHeavy) continue;
+        float acc[kC][kV] = {};
+        sum_rows<T, kC>(perm, s0 > a ? s0 : a, s1 < b ? s1 : b, d_out, d_out_ld, c0, step, d, acc);
+        float *to = part + (2 * unit + (s0 > a ? 1 : 0)) * d;
+#pragma unroll
+        for (uint32_t q = 0; q < kC; ++q) {
+          const uint32_t c = c0 + q * step;
+          if (c < d) write_row<float, kV>(nullptr, to, c, d, 1.0f, acc[q]);
+        }
+      }
+      continue;
+    }
+    const uint64_t t = unit - windows;
+    const uint32_t p0 = start[t], p1 = start[t + 1];
+    if (p1 - p0 > kHeavy || (p0 == p1 && add_to == d_table)) continue;
+    float acc[kC][kV] = {};
+    sum_rows<T, kC>(perm, p0, p1, d_out, d_out_ld, c0, step, d, acc);
+#pragma unroll
+    for (uint32_t q = 0; q < kC; ++q) {
+      const uint32_t c = c0 + q * step;
+      if (c < d)
+        write_row<O, kV>(add_to != nullptr ? add_to + t * d_table_ld : nullptr,
+                         d_table + t * d_table_ld, c, d, scale, acc[q]);
+    }
+  }
+}
+
+// Joins the parts of the heavy id that starts in the block's window, if one
+// does (it then covers the window's last position, and no other heavy id
+// starts there): the waves take equal runs of its windows, then their sums
+// are added in order.
+constexpr uint32_t kJoinThreads = 1024;
+constexpr uint32_t kJoinWaves = kJoinThreads / kWave;
+
+template <class O>
+__global__ void __launch_bounds__(kJoinThreads)
+    embed_grad_join_kernel(const uint32_t *__restrict__ perm, const uint32_t *__restrict__ start,
+                           const int32_t *__restrict__ tokens, uint32_t windows, uint32_t v,
+                           uint32_t d, float scale, const O *add_to, O *d_table,
+                           uint64_t d_table_ld, const float *__restrict__ part) {
+  constexpr uint32_t kV = 4;
+  __shared__ float sums[kJoinWaves][kWave * kV];
+  const uint32_t lane = lane_id(), wave = threadIdx.x / kWave;
+  const uint32_t c = (blockIdx.y * kWave + lane) * kV;
+  const uint32_t kept = start[v];
+  for (uint32_t w = blockIdx.x; w < windows; w += gridDim.x) {
+    const uint32_t a = w * kHeavy;
+    if (a + kHeavy >= kept) return;  // a heavy id that starts here ends past the window
+    const uint32_t id = (uint32_t)tokens[perm[a + kHeavy - 1]];
+    const uint32_t s0 = start[id], s1 = start[id + 1];
+    if (s0 < a || s1 - s0 <= kHeavy) continue;
+    const uint32_t count = (s1 - 1) / kHeavy - w + 1;  // windows it meets
+    const uint32_t run = (count + kJoinWaves - 1) / kJoinWaves;
+    const uint32_t k0 = wave * run, k1 = k0 + run < count ? k0 + run : count;
+    float acc[kV] = {};
+    if (c < d) {
+      for (uint32_t k = k0; k < k1; k += kRowUnroll) {
+        Vec<float> x[kRowUnroll];
+#pragma unroll
+        for (uint32_t u = 0; u < kRowUnroll; ++u) {
+          const uint64_t slot = 2 * ((uint64_t)w + k + u) + (k + u == 0 && s0 > a ? 1 : 0);
+          x[u] = k + u < k1 ? load_vec_tail(part + slot * d, c, d, 0.0f) : Vec<float>{};
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < kRowUnroll; ++u)
+#pragma unroll
+          for (uint32_t j = 0; j < kV; ++j) acc[j] += x[u][j];
+      }
+    }
+    __syncthreads();  // the sums of an earlier id have been read
+#pragma unroll
+    for (uint32_t j = 0; j < kV; ++j) sums[wave][lane * kV + j] = acc[j];
+    __syncthreads();
+    if (wave != 0 || c >= d) continue;
+    for (uint32_t q = 1; q < kJoinWaves; ++q)
+#pragma unroll
+      for (uint32_t j = 0; j < kV; ++j) acc[j] += sums[q][lane * kV + j];
+    write_row<O, kV>(add_to != nullptr ? add_to + (uint64_t)id * d_table_ld : nullptr,
+                     d_table + (uint64_t)id * d_table_ld, c, d, scale, acc);
   }
 }
 
@@ -212,16 +369,17 @@ hipError_t launch_embed(const void *table, uint32_t dtype, uint32_t v, uint32_t 
 }
 
 EmbedGradPlan plan_embed_grad(uint32_t n, uint32_t v, uint32_t d) {
-  (void)d;
   EmbedGradPlan p{};
   // blocks for every compute unit where the ids allow it
   uint32_t ids = div_up(v, 256);
   ids = ids < kSortMaxIds ? ids : kSortMaxIds;
   p.ids = ids > 0 ? ids : 1;
   p.blocks = div_up(v, p.ids);
+  p.windows = n > kHeavy ? div_up(n, kHeavy) : 0;  // heavy ids are possible
   p.off_perm = 0;
   p.off_start = align_up((size_t)n * sizeof(uint32_t), 256);
-  p.ws_bytes = p.off_start + align_up(((size_t)v + 1) * sizeof(uint32_t), 256);
+  p.off_part = p.off_start + align_up(((size_t)v + 1) * sizeof(uint32_t), 256);
+  p.ws_bytes = p.off_part + (size_t)p.windows * 2 * d * sizeof(float);
   return p;
 }
 
@@ -238,16 +396,34 @@ hipError_t launch_embed_grad(const EmbedGradPlan &plan, const int32_t *tokens, u
                      start, status);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  float *part = reinterpret_cast<float *>(base + plan.off_part);
   return with_type(d_out_type, [&](auto x) {
     using T = decltype(x);
-    auto rows = [&](auto y) {
+    const Cover cv = cover<kVec<T>>(d);
+    const uint64_t groups = kThreads / cv.lanes;
+    const uint64_t want = ((uint64_t)plan.windows + v + groups - 1) / groups;
+    const dim3 grid((uint32_t)(want < kMaxBlocks ? want : kMaxBlocks), cv.slabs);
+    auto go = [&](auto y) {
       using O = decltype(y);
-      hipLaunchKernelGGL((embed_grad_rows_kernel<T, O>), dim3(wave_blocks(v)), dim3(kThreads), 0,
-                         stream, perm, start, static_cast<const T *>(d_out), d_out_ld, v, d, scale,
-                         static_cast<const O *>(add_to), static_cast<O *>(d_table), d_table_ld);
+      const O *add = static_cast<const O *>(add_to);
+      O *to = static_cast<O *>(d_table);
+      auto rows = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, perm, start, tokens,
+                           plan.windows, cv.lanes, static_cast<const T *>(d_out), d_out_ld, v, d,
+                           scale, add, to, d_table_ld, part);
+      };
+      if (cv.chunks == 1) rows(embed_grad_rows_kernel<T, O, 1>);
+      else if (cv.chunks == 2) rows(embed_grad_rows_kernel<T, O, 2>);
+      else rows(embed_grad_rows_kernel<T, O, 4>);
+      hipError_t err = hipGetLastError();
+      if (err != hipSuccess || plan.windows == 0) return err;
+      hipLaunchKernelGGL((embed_grad_join_kernel<O>), dim3(plan.windows < kMaxBlocks ? plan.windows : kMaxBlocks,
+                              div_up(d, kWave * 4)),
+                         dim3(kJoinThreads), 0, stream, perm, start, tokens, plan.windows, v, d, scale, add, to,
+                         d_table_ld, part);
       return hipGetLastError();
     };
-    return d_table_type == (uint32_t)Dtype::f32 ? rows(float{}) : rows(x);
+    return d_table_type == (uint32_t)Dtype::f32 ? go(float{}) : go(x);
   });
 }
 

@@ -90,7 +90,8 @@ hipError_t launch_embed(const void *table, uint32_t dtype, uint32_t v, uint32_t 
 struct EmbedGradPlan {
   uint32_t ids;     // table rows per block of the token sort
   uint32_t blocks;  // blocks of the token sort
-  size_t off_perm, off_start;
+  uint32_t windows; // windows of sorted positions, 0 if no id can be heavy
+  size_t off_perm, off_start, off_part;
   size_t ws_bytes;
 };
 EmbedGradPlan plan_embed_grad(uint32_t n, uint32_t v, uint32_t d);

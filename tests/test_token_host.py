@@ -43,7 +43,8 @@ REFUSALS = [
         (TYPE, dict(out=Q + 1)), (TYPE, dict(tokens=P + 2)), (SHAPE, dict(v=0)),
         (SHAPE, dict(d=0)), (SHAPE, dict(table_ld=7)), (SHAPE, dict(out_ld=7)),
         (TOO_LARGE, dict(v=2 ** 31)), (TOO_LARGE, dict(n=2 ** 31)),
-        (TOO_LARGE, dict(out_ld=2 ** 40))]),
+        (TOO_LARGE, dict(out_ld=2 ** 40)),
+        (TOO_LARGE, dict(d=2 ** 23 + 1, table_ld=2 ** 24, out_ld=2 ** 24))]),
     ("seacells_embed_grad", EMBED_GRAD, [
         (NULL, dict(tokens=None)), (NULL, dict(d_out=None)), (NULL, dict(d_table=None)),
         (NULL, dict(status=None)), (TYPE, dict(d_out_type=9)), (TYPE, dict(d_table_type=1)),
@@ -69,7 +70,7 @@ REFUSALS = [
         (NULL, dict(top_logp=None)), (NULL, dict(status=None)), (TYPE, dict(dtype=3)),
         (TYPE, dict(logits=P + 1)), (TYPE, dict(stats=Q + 2)), (SHAPE, dict(v=0)),
         (SHAPE, dict(ld=7)), (SHAPE, dict(top_k=65)), (TOO_LARGE, dict(n=2 ** 31)),
-        (TOO_LARGE, dict(v=2 ** 31, ld=2 ** 31))]),
+        (TOO_LARGE, dict(v=2 ** 23 + 1, ld=2 ** 24))]),
     ("seacells_logprobs_grad", LOGP_GRAD, [
         (NULL, dict(logits=None)), (NULL, dict(stats=None)), (NULL, dict(d_logits=None)),
         (NULL, dict(entropy=None)), (NULL, dict(status=None)), (TYPE, dict(dtype=3)),
