@@ -212,24 +212,21 @@ __device__ __forceinline__ void sum_rows(const uint32_t *__restrict__ perm, uint
   }
 }
 
-template <class O, uint32_t kV>
-using Out = O __attribute__((ext_vector_type(kV), aligned(sizeof(O))));
-
 // d_table[t, c ..] = so_far + scale * acc
 template <class O, uint32_t kV>
 __device__ __forceinline__ void write_row(const O *so_far, O *to, uint32_t c, uint32_t d,
                                           float scale, const float (&acc)[kV]) {
   if (c + kV <= d) {
-    Out<O, kV> y;
+    Pack<O, kV> y;
     if (so_far != nullptr) {
-      const Out<O, kV> a = *reinterpret_cast<const Out<O, kV> *>(so_far + c);
+      const Pack<O, kV> a = *reinterpret_cast<const Pack<O, kV> *>(so_far + c);
 #pragma unroll
       for (uint32_t j = 0; j < kV; ++j) y[j] = (O)((float)a[j] + scale * acc[j]);
     } else {
 #pragma unroll
       for (uint32_t j = 0; j < kV; ++j) y[j] = (O)(scale * acc[j]);
     }
-    *reinterpret_cast<Out<O, kV> *>(to + c) = y;
+    *reinterpret_cast<Pack<O, kV> *>(to + c) = y;
     return;
   }
 #pragma unroll

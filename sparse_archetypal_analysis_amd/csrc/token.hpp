@@ -53,6 +53,60 @@ __device__ __forceinline__ void store_vec_tail(T *row, uint32_t at, uint32_t end
     if (at + j < end) row[at + j] = v[j];
 }
 
+// kN elements of any type at any element-aligned address (dwordx4 accesses,
+// as many as they need).
+template <class T, uint32_t kN>
+using Pack = T __attribute__((ext_vector_type(kN), aligned(sizeof(T))));
+
+template <class T, uint32_t kN>
+__device__ __forceinline__ Pack<T, kN> load_pack_tail(const T *row, uint32_t at, uint32_t end) {
+  if (at + kN <= end) return *reinterpret_cast<const Pack<T, kN> *>(row + at);
+  Pack<T, kN> v = {};
+#pragma unroll
+  for (uint32_t j = 0; j < kN; ++j)
+    if (at + j < end) v[j] = row[at + j];
+  return v;
+}
+
+template <class T, uint32_t kN>
+__device__ __forceinline__ void store_pack_tail(T *row, uint32_t at, uint32_t end, Pack<T, kN> v) {
+  if (at + kN <= end) {
+    *reinterpret_cast<Pack<T, kN> *>(row + at) = v;
+    return;
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < kN; ++j)
+    if (at + j < end) row[at + j] = v[j];
+}
+
+// One DPP step: the value of another lane (0 where it has none or its row is
+// masked off).
+template <int kCtrl, int kRows = 0xF>
+__device__ __forceinline__ float dpp_f32(float x) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+      0, (int)__float_as_uint(x), kCtrl, kRows, 0xF, false));
+}
+
+// Sum over each group of kLanes neighbouring lanes (8, 16, 32 or 64) in a
+// fixed order, the result in every lane of the group. Called with every lane
+// active. quad_perm, half-row and row mirrors as in wave_min_u32; over the
+// whole wave two row broadcasts and a lane read replace the last exchanges.
+template <uint32_t kLanes>
+__device__ __forceinline__ float group_sum(float x) {
+  static_assert(kLanes == 8 || kLanes == 16 || kLanes == 32 || kLanes == 64, "group size");
+  x += dpp_f32<0xB1>(x);
+  x += dpp_f32<0x4E>(x);
+  x += dpp_f32<0x141>(x);
+  if (kLanes >= 16) x += dpp_f32<0x140>(x);
+  if (kLanes == 32) x += __shfl_xor(x, 16, kWave);
+  if (kLanes == 64) {
+    x += dpp_f32<0x142, 0xA>(x);
+    x += dpp_f32<0x143, 0xC>(x);
+    x = readlane_f32(x, 63);
+  }
+  return x;
+}
+
 // IEEE maximum: NaN if either side is (v_maximum3_f32 on gfx950).
 __device__ __forceinline__ float nan_max(float a, float b) {
   return __builtin_elementwise_maximum(a, b);
@@ -107,7 +161,7 @@ hipError_t launch_layer_norm(const void *x, uint32_t dtype, uint32_t n, uint32_t
                              hipStream_t stream);
 
 struct NormGradPlan {
-  uint32_t parts;  // row parts of the weight's and bias' sums
+  uint32_t parts;  // row parts of the weight's and bias' sums (1: no join)
   size_t ws_bytes;
 };
 NormGradPlan plan_layer_norm_grad(uint32_t n, uint32_t d);
