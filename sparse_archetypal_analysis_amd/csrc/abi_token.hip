@@ -140,7 +140,10 @@ int seacells_layer_norm_grad(const void *d_out, uint64_t d_out_ld, const void *x
 
 size_t seacells_logprobs_workspace(uint32_t n, uint32_t v, uint32_t top_k) {
   if (v == 0 || n >= kTooLarge || v > kMaxWidth || top_k > SEACELLS_TOP_MAX) return 0;
-  return logprobs_workspace(n, v, top_k);
+  // one size covers every element type
+  const size_t wide = plan_logprobs(SEACELLS_F32, n, v, top_k).ws_bytes;
+  const size_t half = plan_logprobs(SEACELLS_BF16, n, v, top_k).ws_bytes;
+  return wide > half ? wide : half;
 }
 
 int seacells_logprobs(const void *logits, uint32_t dtype, uint32_t n, uint32_t v, uint64_t ld,
@@ -156,10 +159,9 @@ int seacells_logprobs(const void *logits, uint32_t dtype, uint32_t n, uint32_t v
   if (top_k > SEACELLS_TOP_MAX) return SEACELLS_E_SHAPE;
   int rc;
   if ((rc = check_rows(n, v, ld)) != SEACELLS_OK) return rc;
-  if ((rc = check_workspace(workspace, workspace_bytes, logprobs_workspace(n, v, top_k))) !=
-      SEACELLS_OK)
-    return rc;
-  return done(launch_logprobs(logits, dtype, n, v, ld, targets, top_k, logp, entropy, stats,
+  const LogprobsPlan plan = plan_logprobs(dtype, n, v, top_k);
+  if ((rc = check_workspace(workspace, workspace_bytes, plan.ws_bytes)) != SEACELLS_OK) return rc;
+  return done(launch_logprobs(plan, logits, dtype, n, v, ld, targets, top_k, logp, entropy, stats,
                               top_idx, top_logp, workspace, status, hip_stream(stream)),
               "logprobs launch");
 }

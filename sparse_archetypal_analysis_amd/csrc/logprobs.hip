@@ -7,7 +7,17 @@
 //
 // -inf logits are masked: their p is an exact 0 and the product with their
 // logarithm is taken as 0. NaN and +inf leave a row without a distribution.
-// Both directions are bound by memory.
+//
+// Both directions are bound by memory: forward reads the logits once, with a
+// running (maximum, sum exp, sum t exp) that is rescaled once per 64 bytes; the
+// gradient reads and writes each element once.
+//
+// Alternatives cost no second pass: every lane (or thread) already has the
+// maximum of its own elements, the top_k-th largest of those maxima bounds the
+// top_k-th largest element from below, and only the few lanes whose maximum
+// reaches that bound look for the elements that do. Those candidates - hardly
+// more than top_k - are ordered by counting, with (value, lowest column first)
+// as one 64-bit key.
 #include "token.hpp"
 
 namespace seacells {
@@ -17,107 +27,427 @@ namespace {
 constexpr uint32_t kThreads = 256;
 constexpr uint32_t kWaves = kThreads / kWave;
 constexpr uint32_t kMaxBlocks = 1u << 20;
+constexpr uint32_t kMaxParts = kWave;  // a lane of the join per part
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLowest = -3.4028234663852886e38f;
 // exp of anything below is 0 in f32 (log of the least denormal: -103.3);
 // products with a probability of 0 stay finite
 constexpr float kFloor = -200.0f;
 
 __device__ __forceinline__ uint64_t u64max(uint64_t x, uint64_t y) { return x > y ? x : y; }
 
-// Descending (value, lowest column first) as one ascending number; 0 for
-// masked entries (-inf orders to the least key of all values).
+// Descending (value, lowest column first) as one ascending number; never 0.
 __device__ __forceinline__ uint64_t top_key(float x, uint32_t c) {
-  return x > kNegInf ? ((uint64_t)f32_order(x) << 32) | (0xffffffffu - c) : 0ull;
+  return ((uint64_t)f32_order(x) << 32) | (0xffffffffu - c);
 }
 
-__device__ __forceinline__ float block_max(float x, float *lds) {
-  for (int off = 32; off >= 1; off >>= 1) x = nan_max(x, __shfl_xor(x, off, kWave));
-  __syncthreads();
-  if (lane_id() == 0) lds[threadIdx.x / kWave] = x;
-  __syncthreads();
-  float m = lds[0];
-  for (uint32_t w = 1; w < kWaves; ++w) m = nan_max(m, lds[w]);
-  return m;
+// The sums of a set of logits against its maximum: s = sum e^t, u = sum t e^t,
+// t = x - max(best, lowest finite). The lowest finite value stands in for the
+// maximum of nothing, so masked entries get t = -inf and add an exact 0; a
+// NaN or +inf makes s NaN. s = 0 says that nothing is left.
+struct Sums {
+  float best, s, u;
+};
+
+__device__ __forceinline__ float reference(float best) { return fmaxf(best, kLowest); }
+
+// a's sums against the maximum `best` of a larger set.
+__device__ __forceinline__ void rescale(Sums &a, float best) {
+  const float t = nan_max(reference(a.best) - reference(best), kFloor);
+  const float e = exp_neg(t);
+  a.u = e * (a.u + t * a.s);
+  a.s *= e;
+  a.best = best;
 }
 
-__device__ __forceinline__ float block_sum(float x, float *lds) {
-  x = wave_sum_f32(x);
-  __syncthreads();
-  if (lane_id() == 0) lds[threadIdx.x / kWave] = x;
-  __syncthreads();
-  float s = 0.0f;
-  for (uint32_t w = 0; w < kWaves; ++w) s += lds[w];
-  return s;
+template <uint32_t kLanes>
+__device__ __forceinline__ void join_lanes(Sums &a) {
+  rescale(a, group_max<kLanes>(a.best));
+  a.s = group_sum<kLanes>(a.s);
+  a.u = group_sum<kLanes>(a.u);
 }
 
-__device__ __forceinline__ uint64_t block_max_u64(uint64_t x, uint64_t *lds) {
-  for (int off = 32; off >= 1; off >>= 1)
-    x = u64max(x, (uint64_t)__shfl_xor((unsigned long long)x, off, kWave));
-  __syncthreads();
-  if (lane_id() == 0) lds[threadIdx.x / kWave] = x;
-  __syncthreads();
-  uint64_t m = 0;
-  for (uint32_t w = 0; w < kWaves; ++w) m = u64max(m, lds[w]);
-  return m;
-}
-
-template <class T>
-__global__ void __launch_bounds__(kThreads)
-    logprobs_kernel(const T *__restrict__ logits, uint32_t n, uint32_t v, uint64_t ld,
-                    const int32_t *__restrict__ targets, uint32_t top_k, float *__restrict__ logp,
-                    float *__restrict__ entropy, float *__restrict__ stats,
-                    int32_t *__restrict__ top_idx, float *__restrict__ top_logp,
-                    uint32_t *__restrict__ status) {
-  __shared__ float lds[kWaves];
-  __shared__ uint64_t lds64[kWaves];
-  for (uint64_t i = blockIdx.x; i < n; i += gridDim.x) {
-    const T *row = logits + i * ld;
-    float m = kNegInf;
-    for (uint32_t c = threadIdx.x; c < v; c += kThreads) m = nan_max(m, (float)row[c]);
-    m = block_max(m, lds);
-    float s = 0.0f, u = 0.0f;
-    for (uint32_t c = threadIdx.x; c < v; c += kThreads) {
-      const float t = nan_max((float)row[c] - m, kFloor);
+// Adds kN vectors (entries that are not there hold -inf).
+template <class T, uint32_t kN>
+__device__ __forceinline__ void add_vectors(Sums &a, const Vec<T> (&x)[kN]) {
+  float best = a.best;
+#pragma unroll
+  for (uint32_t k = 0; k < kN; ++k)
+#pragma unroll
+    for (uint32_t j = 0; j < kVec<T>; ++j) best = fmaxf(best, (float)x[k][j]);
+  rescale(a, best);
+  const float m = reference(best);
+#pragma unroll
+  for (uint32_t k = 0; k < kN; ++k)
+#pragma unroll
+    for (uint32_t j = 0; j < kVec<T>; ++j) {
+      const float t = nan_max((float)x[k][j] - m, kFloor);
       const float e = exp_neg(t);
-      s += e;
-      u += t * e;
+      a.s += e;
+      a.u += t * e;
     }
-    s = block_sum(s, lds);
-    u = block_sum(u, lds);
-    const bool empty = m == kNegInf;
-    const bool none = !(m <= 3.4028235e38f);  // NaN or +inf
-    const float nan = __builtin_nanf("");
-    const float ls = none ? nan : empty ? 0.0f : logf(s);
-    if (threadIdx.x == 0) {
-      if (stats != nullptr) {
-        stats[2 * i] = none ? nan : m;
-        stats[2 * i + 1] = ls;
-      }
-      if (entropy != nullptr) entropy[i] = none ? nan : empty ? 0.0f : ls - u / s;
-      if (targets != nullptr) {
-        const int32_t t = targets[i];
-        const bool bad = t >= 0 && (uint32_t)t >= v;
-        if (bad) atomicOr(status, kFlagBadIndex);
-        if (logp != nullptr)
-          logp[i] = t < 0 || bad ? 0.0f : none ? nan : empty ? kNegInf : ((float)row[t] - m) - ls;
+}
+
+// What a row's sums say: the logarithm of its sum, and whether it has a
+// distribution at all.
+struct Row {
+  float m, log_sum;
+  bool none, empty;
+  __device__ __forceinline__ explicit Row(const Sums &a) {
+    none = a.s != a.s;
+    empty = a.s == 0.0f;
+    m = a.best;
+    log_sum = none ? a.s : empty ? 0.0f : logf(a.s);
+  }
+  __device__ __forceinline__ float log_p(float x) const {
+    return none ? log_sum : x > kNegInf ? (x - m) - log_sum : kNegInf;
+  }
+};
+
+struct Outputs {
+  const int32_t *targets;
+  float *logp, *entropy, *stats;
+  int32_t *top_idx;
+  float *top_logp;
+  uint32_t top_k;
+  uint32_t *status;
+  bool check;  // flag targets past the row here (else one block looks at all)
+};
+
+// By one lane.
+template <class T>
+__device__ __forceinline__ void write_row(const Outputs &o, const T *row, uint64_t i, uint32_t v,
+                                          const Sums &a, const Row &r) {
+  if (o.stats != nullptr) {
+    o.stats[2 * i] = r.none ? r.log_sum : r.m;
+    o.stats[2 * i + 1] = r.log_sum;
+  }
+  if (o.entropy != nullptr) o.entropy[i] = r.empty ? 0.0f : r.log_sum - a.u / a.s;
+  if (o.targets == nullptr) return;
+  const int32_t t = o.targets[i];
+  const bool bad = t >= 0 && (uint32_t)t >= v;
+  if (bad && o.check) atomicOr(o.status, kFlagBadIndex);
+  if (o.logp != nullptr) o.logp[i] = t < 0 || bad ? 0.0f : r.log_p((float)row[t]);
+}
+
+__device__ __forceinline__ void write_top(const Outputs &o, uint64_t i, uint32_t place,
+                                          uint64_t key, const Row &r) {
+  o.top_idx[i * o.top_k + place] = key != 0 ? (int32_t)(0xffffffffu - (uint32_t)key) : -1;
+  o.top_logp[i * o.top_k + place] = r.log_p(key != 0 ? f32_unorder((uint32_t)(key >> 32)) : kNegInf);
+}
+
+// The k-th largest (k >= 1) of the wave's values, kN per lane, each lane's in
+// descending order: the largest first place is taken out k - 1 times.
+template <uint32_t kN>
+__device__ __forceinline__ float wave_kth(float (&x)[kN], uint32_t k) {
+  float best = group_max<kWave>(x[0]);
+  for (uint32_t q = 1; q < k && best > kNegInf; ++q) {
+    const uint64_t at = __ballot(x[0] == best);
+    const bool mine = lane_id() == (uint32_t)__builtin_ctzll(at);
+#pragma unroll
+    for (uint32_t j = 0; j + 1 < kN; ++j) x[j] = mine ? x[j + 1] : x[j];
+    x[kN - 1] = mine ? kNegInf : x[kN - 1];
+    best = group_max<kWave>(x[0]);
+  }
+  return best;
+}
+
+// --- rows that a wave's registers hold ------------------------------------------
+
+// A row per kLanes lanes, kR vectors per lane.
+template <class T, uint32_t kLanes, uint32_t kR>
+__global__ void __launch_bounds__(kThreads)
+    logprobs_held_kernel(const T *__restrict__ logits, uint32_t n, uint32_t v, uint64_t ld,
+                         Outputs o) {
+  constexpr uint32_t kV = kVec<T>;
+  constexpr uint32_t kGroups = kThreads / kLanes;
+  constexpr uint32_t kRoom = 2 * kWave;  // candidates in LDS, per wave
+  __shared__ uint64_t room[kLanes == kWave ? kWaves : 1][kLanes == kWave ? kRoom : 1];
+  if (blockIdx.x == 0 && o.targets != nullptr && !o.check)
+    report_ids<kThreads>(o.targets, n, v, o.status);
+  const uint32_t at = threadIdx.x % kLanes;
+  const uint64_t step = (uint64_t)gridDim.x * kGroups;
+  for (uint64_t i0 = (uint64_t)blockIdx.x * kGroups; i0 < n; i0 += step) {
+    const uint64_t i = i0 + threadIdx.x / kLanes;
+    const bool live = i < n;
+    const T *row = logits + (live ? i : 0) * ld;
+    Vec<T> x[kR];
+#pragma unroll
+    for (uint32_t k = 0; k < kR; ++k) {
+      const uint32_t c = (k * kLanes + at) * kV;
+      if (live && c < v) x[k] = load_vec_tail(row, c, v, (T)kNegInf);
+      else x[k] = (T)kNegInf;
+    }
+    Sums a{kNegInf, 0.0f, 0.0f};
+    add_vectors<T, kR>(a, x);
+    const float mine = a.best;
+    join_lanes<kLanes>(a);
+    const Row r(a);
+    if (live && at == 0) write_row(o, row, i, v, a, r);
+    if (o.top_k == 0) continue;
+
+    bool rounds = true;
+    if constexpr (kLanes == kWave) {
+      if (live && !r.none) {
+        float best[1] = {mine};
+        const float least = wave_kth<1>(best, o.top_k);
+        uint64_t *keys = room[threadIdx.x / kWave];
+        uint32_t count = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < kR; ++k) {
+          float top = (float)x[k][0];
+#pragma unroll
+          for (uint32_t j = 1; j < kV; ++j) top = fmaxf(top, (float)x[k][j]);
+          if (__ballot(top >= least && top > kNegInf) == 0) continue;
+#pragma unroll
+          for (uint32_t j = 0; j < kV; ++j) {
+            const float y = (float)x[k][j];
+            const bool hit = y >= least && y > kNegInf;
+            const uint64_t hits = __ballot(hit);
+            const uint32_t place = count + (uint32_t)__popcll(hits & ((1ull << at) - 1ull));
+            if (hit && place < kRoom) keys[place] = top_key(y, (k * kWave + at) * kV + j);
+            count += (uint32_t)__popcll(hits);
+          }
+        }
+        wave_lds_sync();
+        if (count <= kRoom) {
+          rounds = false;
+          for (uint32_t q = at; q < (count > o.top_k ? count : o.top_k); q += kWave) {
+            const uint64_t key = q < count ? keys[q] : 0ull;
+            uint32_t place = 0;
+            for (uint32_t p = 0; p < count; ++p) place += keys[p] > key ? 1u : 0u;
+            place = q < count ? place : q;
+            if (place < o.top_k) write_top(o, i, place, key, r);
+          }
+          wave_lds_sync();
+        }
       }
     }
-    uint64_t last = ~0ull;
-    for (uint32_t k = 0; k < top_k; ++k) {
-      uint64_t best = 0;
-      for (uint32_t c = threadIdx.x; c < v; c += kThreads) {
-        const uint64_t key = none ? 0ull : top_key((float)row[c], c);
-        if (key < last) best = u64max(best, key);
-      }
-      last = block_max_u64(best, lds64);
-      if (threadIdx.x == 0) {
-        top_idx[i * top_k + k] = last != 0 ? (int32_t)(0xffffffffu - (uint32_t)last) : -1;
-        top_logp[i * top_k + k] =
-            none ? nan : last != 0 ? (f32_unorder((uint32_t)(last >> 32)) - m) - ls : kNegInf;
-      }
+    if (!rounds) continue;
+    // one alternative per round: few lanes per row, or a row of many equals
+    for (uint32_t q = 0; q < o.top_k; ++q) {
+      float best = kNegInf;
+#pragma unroll
+      for (uint32_t k = 0; k < kR; ++k)
+#pragma unroll
+        for (uint32_t j = 0; j < kV; ++j) best = fmaxf(best, (float)x[k][j]);
+      best = group_max<kLanes>(best);
+      uint32_t c = 0xffffffffu;
+#pragma unroll
+      for (uint32_t k = kR; k-- > 0;)
+#pragma unroll
+        for (uint32_t j = kV; j-- > 0;)
+          if ((float)x[k][j] == best) c = (k * kLanes + at) * kV + j;
+      c = group_min_u32<kLanes>(c);
+#pragma unroll
+      for (uint32_t k = 0; k < kR; ++k)
+#pragma unroll
+        for (uint32_t j = 0; j < kV; ++j)
+          if ((k * kLanes + at) * kV + j == c) x[k][j] = (T)kNegInf;
+      if (live && at == 0)
+        write_top(o, i, q, best > kNegInf && !r.none ? top_key(best, c) : 0ull, r);
     }
   }
 }
+
+// --- rows that are streamed -------------------------------------------------------
+
+constexpr uint32_t kUnroll = 4;   // vectors in flight per thread
+constexpr uint32_t kRoom = 1024;  // candidates in LDS
+
+struct Stream {
+  float best[kThreads];
+  Sums wave[kWaves];
+  float least;
+  uint32_t count;
+  uint64_t keys[kRoom];
+  uint64_t wave_key[kWaves];
+};
+
+// The candidates of columns [q0, q1) (in vectors) go to sh.keys, best first at
+// their place; f(place, key) is called by the thread that holds it, for the
+// places below top_k, key 0 where nothing is left. `mine` is the maximum of
+// the thread's own columns.
+template <class T, class F>
+__device__ __forceinline__ void block_top(Stream &sh, const T *row, uint32_t q0, uint32_t q1,
+                                          uint32_t v, uint32_t top_k, float mine, F &&f) {
+  constexpr uint32_t kV = kVec<T>;
+  sh.best[threadIdx.x] = mine;
+  if (threadIdx.x == 0) sh.count = 0;
+  __syncthreads();
+  if (threadIdx.x < kWave) {
+    float x[kWaves];
+#pragma unroll
+    for (uint32_t k = 0; k < kWaves; ++k) x[k] = sh.best[k * kWave + threadIdx.x];
+#pragma unroll
+    for (uint32_t a = 0; a + 1 < kWaves; ++a)
+#pragma unroll
+      for (uint32_t b = 0; b + 1 < kWaves - a; ++b) {
+        const float hi = fmaxf(x[b], x[b + 1]), lo = fminf(x[b], x[b + 1]);
+        x[b] = hi;
+        x[b + 1] = lo;
+      }
+    const float least = wave_kth<kWaves>(x, top_k);
+    if (threadIdx.x == 0) sh.least = least;
+  }
+  __syncthreads();
+  const float least = sh.least;
+  if (mine >= least && mine > kNegInf) {
+    for (uint32_t q = q0 + threadIdx.x; q < q1; q += kThreads * kUnroll) {
+      Vec<T> x[kUnroll];
+#pragma unroll
+      for (uint32_t u = 0; u < kUnroll; ++u) {
+        const uint32_t p = q + u * kThreads;
+        if (p < q1) x[u] = load_vec_tail(row, p * kV, v, (T)kNegInf);
+        else x[u] = (T)kNegInf;
+      }
+#pragma unroll
+      for (uint32_t u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (uint32_t j = 0; j < kV; ++j) {
+          const float y = (float)x[u][j];
+          if (y >= least && y > kNegInf) {
+            const uint32_t place = atomicAdd(&sh.count, 1u);
+            if (place < kRoom) sh.keys[place] = top_key(y, (q + u * kThreads) * kV + j);
+          }
+        }
+    }
+  }
+  __syncthreads();
+  const uint32_t count = sh.count;
+  if (count <= kRoom) {
+    for (uint32_t q = threadIdx.x; q < (count > top_k ? count : top_k); q += kThreads) {
+      const uint64_t key = q < count ? sh.keys[q] : 0ull;
+      uint32_t place = 0;
+      for (uint32_t p = 0; p < count; ++p) place += sh.keys[p] > key ? 1u : 0u;
+      place = q < count ? place : q;
+      if (place < top_k) f(place, key);
+    }
+    __syncthreads();
+    return;
+  }
+  // many equals: one alternative per pass over the row
+  uint64_t last = ~0ull;
+  for (uint32_t k = 0; k < top_k; ++k) {
+    uint64_t key = 0;
+    for (uint32_t q = q0 + threadIdx.x; q < q1; q += kThreads) {
+      const Vec<T> x = load_vec_tail(row, q * kV, v, (T)kNegInf);
+#pragma unroll
+      for (uint32_t j = 0; j < kV; ++j) {
+        const uint64_t y = top_key((float)x[j], q * kV + j);
+        if ((float)x[j] > kNegInf && y < last) key = u64max(key, y);
+      }
+    }
+    for (int off = 32; off >= 1; off >>= 1)
+      key = u64max(key, (uint64_t)__shfl_xor((unsigned long long)key, off, kWave));
+    __syncthreads();
+    if (lane_id() == 0) sh.wave_key[threadIdx.x / kWave] = key;
+    __syncthreads();
+    last = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kWaves; ++w) last = u64max(last, sh.wave_key[w]);
+    if (threadIdx.x == 0) f(k, last);
+  }
+  __syncthreads();
+}
+
+// A block per part of a row (grid x: rows, y: parts). One part writes the
+// row's outputs, several leave their sums and their candidates for the join.
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+    logprobs_stream_kernel(const T *__restrict__ logits, uint32_t n, uint32_t v, uint64_t ld,
+                           Outputs o, Sums *__restrict__ part_sums, uint64_t *__restrict__ part_keys) {
+  constexpr uint32_t kV = kVec<T>;
+  __shared__ Stream sh;
+  const uint32_t parts = gridDim.y, part = blockIdx.y;
+  if (blockIdx.x == 0 && part == 0 && o.targets != nullptr && !o.check)
+    report_ids<kThreads>(o.targets, n, v, o.status);
+  const uint32_t vecs = (v + kV - 1) / kV;
+  const uint32_t q0 = (uint32_t)((uint64_t)vecs * part / parts);
+  const uint32_t q1 = (uint32_t)((uint64_t)vecs * (part + 1) / parts);
+  for (uint64_t i = blockIdx.x; i < n; i += gridDim.x) {
+    const T *row = logits + i * ld;
+    Sums a{kNegInf, 0.0f, 0.0f};
+    for (uint32_t q = q0; q < q1; q += kThreads * kUnroll) {
+      Vec<T> x[kUnroll];
+      if ((uint64_t)(q + kThreads * kUnroll) * kV <= v && q + kThreads * kUnroll <= q1) {
+#pragma unroll
+        for (uint32_t u = 0; u < kUnroll; ++u)
+          x[u] = load_vec(row + (size_t)(q + u * kThreads + threadIdx.x) * kV);
+      } else {
+#pragma unroll
+        for (uint32_t u = 0; u < kUnroll; ++u) {
+          const uint32_t p = q + u * kThreads + threadIdx.x;
+          if (p < q1) x[u] = load_vec_tail(row, p * kV, v, (T)kNegInf);
+          else x[u] = (T)kNegInf;
+        }
+      }
+      add_vectors<T, kUnroll>(a, x);
+    }
+    const float mine = a.best;
+    join_lanes<kWave>(a);
+    if (lane_id() == 0) sh.wave[threadIdx.x / kWave] = a;
+    __syncthreads();
+    float best = kNegInf;
+#pragma unroll
+    for (uint32_t w = 0; w < kWaves; ++w) best = fmaxf(best, sh.wave[w].best);
+    a = Sums{best, 0.0f, 0.0f};
+#pragma unroll
+    for (uint32_t w = 0; w < kWaves; ++w) {
+      Sums b = sh.wave[w];
+      rescale(b, best);
+      a.s += b.s;
+      a.u += b.u;
+    }
+    __syncthreads();
+    if (parts == 1) {
+      const Row r(a);
+      if (threadIdx.x == 0) write_row(o, row, i, v, a, r);
+      if (o.top_k == 0) continue;
+      if (r.none) {
+        if (threadIdx.x < o.top_k) write_top(o, i, threadIdx.x, 0ull, r);
+        continue;
+      }
+      block_top<T>(sh, row, q0, q1, v, o.top_k, mine,
+                   [&](uint32_t place, uint64_t key) { write_top(o, i, place, key, r); });
+    } else {
+      if (threadIdx.x == 0) part_sums[i * parts + part] = a;
+      if (o.top_k == 0) continue;
+      uint64_t *to = part_keys + (i * parts + part) * o.top_k;
+      block_top<T>(sh, row, q0, q1, v, o.top_k, mine,
+                   [&](uint32_t place, uint64_t key) { to[place] = key; });
+    }
+  }
+}
+
+// The parts of a row, one per lane, in one wave: their sums joined, their
+// ordered candidates merged.
+template <class T>
+__global__ void __launch_bounds__(kWave)
+    logprobs_join_kernel(const T *__restrict__ logits, uint32_t n, uint32_t v, uint64_t ld,
+                         uint32_t parts, Outputs o, const Sums *__restrict__ part_sums,
+                         const uint64_t *__restrict__ part_keys) {
+  const uint32_t lane = lane_id();
+  for (uint64_t i = blockIdx.x; i < n; i += gridDim.x) {
+    Sums a{kNegInf, 0.0f, 0.0f};
+    if (lane < parts) a = part_sums[i * parts + lane];
+    join_lanes<kWave>(a);
+    const Row r(a);
+    if (lane == 0) write_row(o, logits + i * ld, i, v, a, r);
+    const uint64_t *keys = part_keys + (i * parts + lane) * o.top_k;
+    uint32_t next = 0;
+    uint64_t head = lane < parts && o.top_k > 0 && !r.none ? keys[0] : 0ull;
+    for (uint32_t q = 0; q < o.top_k; ++q) {
+      const uint32_t hi = ~wave_min_u32(~(uint32_t)(head >> 32));
+      const uint32_t lo = ~wave_min_u32((uint32_t)(head >> 32) == hi ? ~(uint32_t)head : ~0u);
+      const uint64_t key = ((uint64_t)hi << 32) | lo;
+      if (lane == 0) write_top(o, i, q, key, r);
+      if (key != 0 && head == key) head = ++next < o.top_k ? keys[next] : 0ull;
+    }
+  }
+}
+
+// --- gradient -----------------------------------------------------------------
 
 template <class T>
 __global__ void __launch_bounds__(kThreads)
@@ -149,29 +479,79 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-uint32_t row_blocks(uint32_t n) { return n < kMaxBlocks ? n : kMaxBlocks; }
+uint32_t capped(uint64_t blocks) { return (uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks); }
+
+// f(lanes, vectors per lane) for rows that a wave's registers hold.
+template <uint32_t kLanes_, uint32_t kR_>
+struct Group {
+  static constexpr uint32_t lanes = kLanes_, vecs = kR_;
+};
+
+template <class F>
+bool held_group(uint32_t vecs, F &&f) {
+  if (vecs <= 8) f(Group<8, 1>{});
+  else if (vecs <= 16) f(Group<16, 1>{});
+  else if (vecs <= 32) f(Group<32, 1>{});
+  else if (vecs <= 64) f(Group<64, 1>{});
+  else if (vecs <= 128) f(Group<64, 2>{});
+  else if (vecs <= 256) f(Group<64, 4>{});
+  else if (vecs <= 512) f(Group<64, 8>{});
+  else return false;
+  return true;
+}
+
+constexpr uint32_t kHeldVecs = 512;
+constexpr uint32_t kFillBlocks = 512;               // two blocks per compute unit
+constexpr uint32_t kPartVecs = kThreads * kUnroll;  // least part of a row
 
 }  // namespace
 
-size_t logprobs_workspace(uint32_t n, uint32_t v, uint32_t top_k) {
-  (void)n;
-  (void)v;
-  (void)top_k;
-  return 0;
+LogprobsPlan plan_logprobs(uint32_t dtype, uint32_t n, uint32_t v, uint32_t top_k) {
+  LogprobsPlan p{};
+  const uint32_t vecs = div_up(v, kVecBytes / dtype_size(dtype));
+  p.parts = 1;
+  if (vecs > kHeldVecs && n > 0 && n < kFillBlocks / 2) {
+    const uint32_t fill = kFillBlocks / n, most = div_up(vecs, kPartVecs);
+    p.parts = fill < most ? fill : most;
+    p.parts = p.parts < kMaxParts ? p.parts : kMaxParts;
+  }
+  if (p.parts > 1) {
+    p.off_keys = align_up((size_t)n * p.parts * sizeof(Sums), 256);
+    p.ws_bytes = p.off_keys + (size_t)n * p.parts * top_k * sizeof(uint64_t);
+  }
+  return p;
 }
 
-hipError_t launch_logprobs(const void *logits, uint32_t dtype, uint32_t n, uint32_t v, uint64_t ld,
-                           const int32_t *targets, uint32_t top_k, float *logp, float *entropy,
-                           float *stats, int32_t *top_idx, float *top_logp, void *ws,
-                           uint32_t *status, hipStream_t stream) {
-  (void)ws;
-  hipError_t e = launch_status_clear(status, stream);
-  if (e != hipSuccess || n == 0) return e;
+hipError_t launch_logprobs(const LogprobsPlan &plan, const void *logits, uint32_t dtype, uint32_t n,
+                           uint32_t v, uint64_t ld, const int32_t *targets, uint32_t top_k,
+                           float *logp, float *entropy, float *stats, int32_t *top_idx,
+                           float *top_logp, void *ws, uint32_t *status, hipStream_t stream) {
+  // a block looks at all targets where it can; else (and without targets) the
+  // status is cleared first
+  const bool one = targets != nullptr && n > 0 && n <= kIdsOfOneBlock;
+  if (!one) {
+    const hipError_t e = launch_status_clear(status, stream);
+    if (e != hipSuccess || n == 0) return e;
+  }
+  const Outputs o{targets, logp, entropy, stats, top_idx, top_logp, top_k, status, !one};
   return with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    hipLaunchKernelGGL((logprobs_kernel<T>), dim3(row_blocks(n)), dim3(kThreads), 0, stream,
-                       static_cast<const T *>(logits), n, v, ld, targets, top_k, logp, entropy,
-                       stats, top_idx, top_logp, status);
+    const T *x = static_cast<const T *>(logits);
+    const bool held = held_group(div_up(v, kVec<T>), [&](auto g) {
+      using G = decltype(g);
+      hipLaunchKernelGGL((logprobs_held_kernel<T, G::lanes, G::vecs>),
+                         dim3(capped(div_up(n, kThreads / G::lanes))), dim3(kThreads), 0, stream, x,
+                         n, v, ld, o);
+    });
+    if (held) return hipGetLastError();
+    Sums *sums = static_cast<Sums *>(ws);
+    uint64_t *keys = reinterpret_cast<uint64_t *>(static_cast<char *>(ws) + plan.off_keys);
+    hipLaunchKernelGGL((logprobs_stream_kernel<T>), dim3(capped(n), plan.parts), dim3(kThreads), 0,
+                       stream, x, n, v, ld, o, sums, keys);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || plan.parts == 1) return e;
+    hipLaunchKernelGGL((logprobs_join_kernel<T>), dim3(n), dim3(kWave), 0, stream, x, n, v, ld,
+                       plan.parts, o, sums, keys);
     return hipGetLastError();
   });
 }
@@ -185,7 +565,7 @@ hipError_t launch_logprobs_grad(const void *logits, uint32_t dtype, uint32_t n, 
   if (e != hipSuccess || n == 0) return e;
   return with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    hipLaunchKernelGGL((logprobs_grad_kernel<T>), dim3(row_blocks(n)), dim3(kThreads), 0, stream,
+    hipLaunchKernelGGL((logprobs_grad_kernel<T>), dim3(capped(n)), dim3(kThreads), 0, stream,
                        static_cast<const T *>(logits), n, v, ld, targets, stats, entropy, d_logp,
                        d_entropy, static_cast<T *>(d_logits), d_logits_ld, status);
     return hipGetLastError();

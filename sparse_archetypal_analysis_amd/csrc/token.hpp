@@ -87,6 +87,13 @@ __device__ __forceinline__ float dpp_f32(float x) {
       0, (int)__float_as_uint(x), kCtrl, kRows, 0xF, false));
 }
 
+// As dpp_f32, but the lane's own value where it has none.
+template <int kCtrl, int kRows = 0xF>
+__device__ __forceinline__ float dpp_same_f32(float x) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+      (int)__float_as_uint(x), (int)__float_as_uint(x), kCtrl, kRows, 0xF, false));
+}
+
 // Sum over each group of kLanes neighbouring lanes (8, 16, 32 or 64) in a
 // fixed order, the result in every lane of the group. Called with every lane
 // active. quad_perm, half-row and row mirrors as in wave_min_u32; over the
@@ -105,6 +112,55 @@ __device__ __forceinline__ float group_sum(float x) {
     x = readlane_f32(x, 63);
   }
   return x;
+}
+
+// Maximum over each group of kLanes neighbouring lanes, in every lane of the
+// group. Called with every lane active; NaN loses against any number.
+template <uint32_t kLanes>
+__device__ __forceinline__ float group_max(float x) {
+  x = fmaxf(x, dpp_same_f32<0xB1>(x));
+  x = fmaxf(x, dpp_same_f32<0x4E>(x));
+  x = fmaxf(x, dpp_same_f32<0x141>(x));
+  if (kLanes >= 16) x = fmaxf(x, dpp_same_f32<0x140>(x));
+  if (kLanes == 32) x = fmaxf(x, __shfl_xor(x, 16, kWave));
+  if (kLanes == 64) {
+    x = fmaxf(x, dpp_same_f32<0x142, 0xA>(x));
+    x = fmaxf(x, dpp_same_f32<0x143, 0xC>(x));
+    x = readlane_f32(x, 63);
+  }
+  return x;
+}
+
+template <uint32_t kLanes>
+__device__ __forceinline__ uint32_t group_min_u32(uint32_t x) {
+  if constexpr (kLanes == kWave) {
+    return wave_min_u32(x);
+  } else {
+#pragma unroll
+    for (uint32_t off = 1; off < kLanes; off *= 2) x = min(x, __shfl_xor(x, (int)off, kWave));
+    return x;
+  }
+}
+
+// Ids (tokens, targets) that one block of threads can look over beside its
+// own work; above that the status word is cleared by a launch of its own.
+constexpr uint32_t kIdsOfOneBlock = 16384;
+
+// *status = BAD_INDEX if any id is v or more, else 0; by one whole block.
+template <uint32_t kBlock>
+__device__ __forceinline__ void report_ids(const int32_t *__restrict__ ids, uint32_t n, uint32_t v,
+                                           uint32_t *__restrict__ status) {
+  typedef int32_t Four __attribute__((ext_vector_type(4), aligned(4)));
+  bool bad = false;
+  const uint32_t fours = n / 4;
+#pragma unroll 4
+  for (uint32_t i = threadIdx.x; i < fours; i += kBlock) {
+    const Four t = *reinterpret_cast<const Four *>(ids + 4 * i);
+    bad |= max(max(t.x, t.y), max(t.z, t.w)) >= (int32_t)v;
+  }
+  if (threadIdx.x < n % 4) bad |= ids[4 * fours + threadIdx.x] >= (int32_t)v;
+  const bool any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *status = any ? kFlagBadIndex : 0u;
 }
 
 // IEEE maximum: NaN if either side is (v_maximum3_f32 on gfx950).
@@ -172,9 +228,14 @@ hipError_t launch_layer_norm_grad(const NormGradPlan &plan, const void *d_out, u
                                   uint64_t d_x_ld, void *d_weight, void *d_bias, void *ws,
                                   hipStream_t stream);
 
-size_t logprobs_workspace(uint32_t n, uint32_t v, uint32_t top_k);
-hipError_t launch_logprobs(const void *logits, uint32_t dtype, uint32_t n, uint32_t v, uint64_t ld,
-                           const int32_t *targets, uint32_t top_k, float *logp, float *entropy,
+struct LogprobsPlan {
+  uint32_t parts;  // parts of a row (1: no join)
+  size_t off_keys;
+  size_t ws_bytes;
+};
+LogprobsPlan plan_logprobs(uint32_t dtype, uint32_t n, uint32_t v, uint32_t top_k);
+hipError_t launch_logprobs(const LogprobsPlan &plan, const void *logits, uint32_t dtype, uint32_t n,
+                           uint32_t v, uint64_t ld, const int32_t *targets, uint32_t top_k, float *logp, float *entropy,
                            float *stats, int32_t *top_idx, float *top_logp, void *ws,
                            uint32_t *status, hipStream_t stream);
 hipError_t launch_logprobs_grad(const void *logits, uint32_t dtype, uint32_t n, uint32_t v,
