@@ -160,7 +160,9 @@ int seacells_logprobs(const void *logits, uint32_t dtype, uint32_t n, uint32_t v
   int rc;
   if ((rc = check_rows(n, v, ld)) != SEACELLS_OK) return rc;
   const LogprobsPlan plan = plan_logprobs(dtype, n, v, top_k);
-  if ((rc = check_workspace(workspace, workspace_bytes, plan.ws_bytes)) != SEACELLS_OK) return rc;
+  if ((rc = check_workspace(workspace, workspace_bytes,
+                            seacells_logprobs_workspace(n, v, top_k))) != SEACELLS_OK)
+    return rc;
   return done(launch_logprobs(plan, logits, dtype, n, v, ld, targets, top_k, logp, entropy, stats,
                               top_idx, top_logp, workspace, status, hip_stream(stream)),
               "logprobs launch");

@@ -91,7 +91,7 @@ def test_entry_points_refuse_on_the_host(fn, base, code, change):
 def test_few_rows_of_logits_need_their_workspace():
     need = saa.seacells_logprobs_workspace(1, 131072, 8)
     if need:
-        go = call("seacells_logprobs", **dict(LOGP, n=1, v=131072, ld=131072))
+        go = call("seacells_logprobs", **dict(LOGP, n=1, v=131072, ld=131072, top_k=8))
         assert go(ws=None) == WORKSPACE and go(ws_bytes=need - 1) == WORKSPACE
 
 
