@@ -167,7 +167,8 @@ int seacells_logprobs(const void *logits, uint32_t dtype, uint32_t n, uint32_t v
  * stats, entropy        as seacells_logprobs wrote them; entropy may be NULL
  *                       with d_entropy NULL.
  * d_logp, d_entropy     device [n] f32; either may be NULL (0).
- * Masked (-inf) logits and rows with nothing left get 0.
+ * Masked (-inf) logits and rows with nothing left get 0 (whatever d_logp and
+ * d_entropy hold there); a row without a distribution (NaN stats) gets NaN.
  */
 int seacells_logprobs_grad(const void *logits, uint32_t dtype, uint32_t n, uint32_t v,
                            uint64_t ld, const int32_t *targets, const float *stats,

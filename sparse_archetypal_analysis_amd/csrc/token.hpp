@@ -31,14 +31,19 @@ __device__ __forceinline__ void store_vec(T *p, Vec<T> v) {
   *reinterpret_cast<Vec<T> *>(p) = v;
 }
 
-// The elements of [at, end) that a lane's vector at `at` covers; those past
-// the end read as `fill`.
+// The elements of [at, end) that a lane's vector at `at` covers, at < end;
+// those past the end read as `fill`. The last vector's elements are loaded at
+// clamped places without a branch, so that the loads do not wait for each
+// other (a branch per element took 8 memory latencies: 10 of 107 us for 4096
+// rows of 50001 bf16).
 template <class T>
 __device__ __forceinline__ Vec<T> load_vec_tail(const T *row, uint32_t at, uint32_t end, T fill) {
   if (at + kVec<T> <= end) return load_vec(row + at);
   Vec<T> v;
 #pragma unroll
-  for (uint32_t j = 0; j < kVec<T>; ++j) v[j] = at + j < end ? row[at + j] : fill;
+  for (uint32_t j = 0; j < kVec<T>; ++j) v[j] = row[at + j < end ? at + j : end - 1];
+#pragma unroll
+  for (uint32_t j = 0; j < kVec<T>; ++j) v[j] = at + j < end ? v[j] : fill;
   return v;
 }
 
@@ -61,10 +66,11 @@ using Pack = T __attribute__((ext_vector_type(kN), aligned(sizeof(T))));
 template <class T, uint32_t kN>
 __device__ __forceinline__ Pack<T, kN> load_pack_tail(const T *row, uint32_t at, uint32_t end) {
   if (at + kN <= end) return *reinterpret_cast<const Pack<T, kN> *>(row + at);
-  Pack<T, kN> v = {};
+  Pack<T, kN> v;
 #pragma unroll
-  for (uint32_t j = 0; j < kN; ++j)
-    if (at + j < end) v[j] = row[at + j];
+  for (uint32_t j = 0; j < kN; ++j) v[j] = row[at + j < end ? at + j : end - 1];
+#pragma unroll
+  for (uint32_t j = 0; j < kN; ++j) v[j] = at + j < end ? v[j] : (T)0.0f;
   return v;
 }
 

@@ -445,6 +445,20 @@ def test_logprobs_grad(n, v, k, dtype, masks):
     assert torch.equal(x, out)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_masked_logits_get_no_gradient_from_infinite_ones(dtype):
+    x = rows(np.random.default_rng(4), 3, 300, dtype)
+    x[:, 7:90] = -INF
+    x[2] = -INF
+    tgt = torch.tensor([3, 8, 5], dtype=torch.int32, device="cuda")  # open, masked, empty row
+    _, H, stats = saa.seacells_logprobs(x, None)[:3]
+    for bad in (INF, float("nan")):
+        gl = torch.full((3,), bad, device="cuda")
+        g, _ = saa.seacells_logprobs_grad(x, tgt, stats, H, gl, gl)
+        assert not g[:, 7:90].any() and not g[2].any()
+        assert bool(g[:2, 100:].isnan().all() if bad != INF else (~g[:2, 100:].isfinite()).all())
+
+
 def test_logprobs_rows_beyond_4_gib():
     far = 2 ** 31 + 7
     base = torch.empty(far + 4096, dtype=torch.bfloat16, device="cuda")
