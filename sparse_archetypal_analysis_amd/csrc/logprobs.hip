@@ -67,9 +67,18 @@ __device__ __forceinline__ void join_lanes(Sums &a) {
   a.u = group_sum<kLanes>(a.u);
 }
 
+// Keeps the compiler from carrying what it computed of a vector past here.
+template <class V>
+__device__ __forceinline__ void hide(V &x) {
+  typedef uint32_t Raw __attribute__((ext_vector_type(4)));
+  Raw r = __builtin_bit_cast(Raw, x);
+  asm volatile("" : "+v"(r));
+  x = __builtin_bit_cast(V, r);
+}
+
 // Adds kN vectors (entries that are not there hold -inf).
 template <class T, uint32_t kN>
-__device__ __forceinline__ void add_vectors(Sums &a, const Vec<T> (&x)[kN]) {
+__device__ __forceinline__ void add_vectors(Sums &a, Vec<T> (&x)[kN]) {
   float best = a.best;
 #pragma unroll
   for (uint32_t k = 0; k < kN; ++k)
@@ -78,7 +87,8 @@ __device__ __forceinline__ void add_vectors(Sums &a, const Vec<T> (&x)[kN]) {
   rescale(a, best);
   const float m = reference(best);
 #pragma unroll
-  for (uint32_t k = 0; k < kN; ++k)
+  for (uint32_t k = 0; k < kN; ++k) {
+    if (sizeof(T) == 2 && kN > 1) hide(x[k]);  // unpacked again rather than held as f32
 #pragma unroll
     for (uint32_t j = 0; j < kVec<T>; ++j) {
       const float t = nan_max((float)x[k][j] - m, kFloor);
@@ -86,6 +96,7 @@ __device__ __forceinline__ void add_vectors(Sums &a, const Vec<T> (&x)[kN]) {
       a.s += e;
       a.u += t * e;
     }
+  }
 }
 
 // What a row's sums say: the logarithm of its sum, and whether it has a
@@ -114,20 +125,31 @@ struct Outputs {
   bool check;  // flag targets past the row here (else one block looks at all)
 };
 
+// A row's target and its logit, fetched before the row's sums so that the two
+// dependent loads do not follow them.
+template <class T>
+struct Target {
+  int32_t id;
+  bool bad;
+  T x;
+  __device__ __forceinline__ Target(const Outputs &o, const T *row, uint64_t i, uint32_t v) {
+    id = o.targets != nullptr ? o.targets[i] : -1;
+    bad = id >= 0 && (uint32_t)id >= v;
+    x = o.logp != nullptr && id >= 0 && !bad ? row[id] : (T)0.0f;
+  }
+};
+
 // By one lane.
 template <class T>
-__device__ __forceinline__ void write_row(const Outputs &o, const T *row, uint64_t i, uint32_t v,
+__device__ __forceinline__ void write_row(const Outputs &o, uint64_t i, const Target<T> &t,
                                           const Sums &a, const Row &r) {
   if (o.stats != nullptr) {
     o.stats[2 * i] = r.none ? r.log_sum : r.m;
     o.stats[2 * i + 1] = r.log_sum;
   }
   if (o.entropy != nullptr) o.entropy[i] = r.empty ? 0.0f : r.log_sum - a.u / a.s;
-  if (o.targets == nullptr) return;
-  const int32_t t = o.targets[i];
-  const bool bad = t >= 0 && (uint32_t)t >= v;
-  if (bad && o.check) atomicOr(o.status, kFlagBadIndex);
-  if (o.logp != nullptr) o.logp[i] = t < 0 || bad ? 0.0f : r.log_p((float)row[t]);
+  if (t.bad && o.check) atomicOr(o.status, kFlagBadIndex);
+  if (o.logp != nullptr) o.logp[i] = t.id < 0 || t.bad ? 0.0f : r.log_p((float)t.x);
 }
 
 __device__ __forceinline__ void write_top(const Outputs &o, uint64_t i, uint32_t place,
@@ -136,23 +158,138 @@ __device__ __forceinline__ void write_top(const Outputs &o, uint64_t i, uint32_t
   o.top_logp[i * o.top_k + place] = r.log_p(key != 0 ? f32_unorder((uint32_t)(key >> 32)) : kNegInf);
 }
 
-// The k-th largest (k >= 1) of the wave's values, kN per lane, each lane's in
-// descending order: the largest first place is taken out k - 1 times.
+// The largest number that k of the wave's values reach, to its order's highest
+// kBits bits and from below (16: 7 bits of the mantissa; 32: the k-th largest
+// value itself), but at least the lowest finite value: what is at or above it
+// holds the k largest ones that are not masked. Found bit by bit, whatever k
+// is; reach(y) counts the values >= y (orders past infinity are NaN: none).
+template <uint32_t kBits, class F>
+__device__ __forceinline__ float wave_bound(uint32_t k, F &&reach) {
+  uint32_t at = 0;
+  for (uint32_t bit = 1u << 31; bit >= 1u << (32 - kBits) && bit != 0; bit >>= 1)
+    at = reach(f32_unorder(at | bit)) >= k ? at | bit : at;
+  return fmaxf(f32_unorder(at), kLowest);
+}
+
+__device__ __forceinline__ uint32_t lanes_of(bool x) { return (uint32_t)__popcll(__ballot(x)); }
+
 template <uint32_t kN>
-__device__ __forceinline__ float wave_kth(float (&x)[kN], uint32_t k) {
-  float best = group_max<kWave>(x[0]);
-  for (uint32_t q = 1; q < k && best > kNegInf; ++q) {
-    const uint64_t at = __ballot(x[0] == best);
-    const bool mine = lane_id() == (uint32_t)__builtin_ctzll(at);
+__device__ __forceinline__ float wave_bound_of(const float (&x)[kN], uint32_t k) {
+  return wave_bound<16>(k, [&](float y) {
+    uint32_t c = 0;
 #pragma unroll
-    for (uint32_t j = 0; j + 1 < kN; ++j) x[j] = mine ? x[j + 1] : x[j];
-    x[kN - 1] = mine ? kNegInf : x[kN - 1];
-    best = group_max<kWave>(x[0]);
-  }
-  return best;
+    for (uint32_t j = 0; j < kN; ++j) c += lanes_of(x[j] >= y);
+    return c;
+  });
 }
 
 // --- rows that a wave's registers hold ------------------------------------------
+
+// The alternatives of a row that a wave holds. A lane's largest element (mine)
+// stands for its others: the bound that top_k of those reach, or of up to 8
+// from each lane where the lanes are too few, leaves hardly more than top_k
+// elements, which go to LDS and are ordered there by counting. Should more
+// than a wave's lanes be left (many equals, or a bound too coarse), the
+// top_k-th largest element itself is looked for, and of those that equal it
+// the first columns are taken.
+template <class T, uint32_t kR>
+__device__ __forceinline__ void wave_top(const Outputs &o, uint64_t i, uint32_t v, Vec<T> (&x)[kR],
+                                         float mine, const Row &r, uint64_t *keys) {
+  constexpr uint32_t kV = kVec<T>;
+  constexpr uint32_t kE = kR * kV;
+  const uint32_t lane = lane_id(), top_k = o.top_k;
+  if (r.none) {
+    if (lane < top_k) write_top(o, i, lane, 0ull, r);
+    return;
+  }
+  // (what was computed of the elements before is not carried this far: it
+  // would take up to 220 registers, 2 waves per SIMD)
+#pragma unroll
+  for (uint32_t k = 0; k < kR; ++k) hide(x[k]);
+  float least;
+  if (2 * top_k <= min((v + kV - 1) / kV, kWave)) {
+    const float sets[1] = {mine};
+    least = wave_bound_of<1>(sets, top_k);
+  } else {
+    constexpr uint32_t kSets = kE < 8 ? kE : 8;
+    float sets[kSets];
+#pragma unroll
+    for (uint32_t e = 0; e < kE; ++e)
+      sets[e % kSets] = e < kSets ? (float)x[e / kV][e % kV]
+                                  : fmaxf(sets[e % kSets], (float)x[e / kV][e % kV]);
+    least = wave_bound_of<kSets>(sets, top_k);
+  }
+  uint32_t first = lane * kV;      // the lane's first column
+  asm volatile("" : "+v"(first));  // (not one register per element's)
+#pragma unroll
+  for (uint32_t k = 0; k < kR; ++k) hide(x[k]);
+  const uint64_t lower = (1ull << lane) - 1ull;
+  uint32_t count = 0;
+#pragma unroll
+  for (uint32_t k = 0; k < kR; ++k)
+#pragma unroll
+    for (uint32_t j = 0; j < kV; ++j) {
+      const float y = (float)x[k][j];
+      const bool hit = y >= least;
+      const uint64_t hits = __ballot(hit);
+      if (hits == 0) continue;
+      const uint32_t place = count + (uint32_t)__popcll(hits & lower);
+      if (hit && place < kWave) keys[place] = top_key(y, first + k * kWave * kV + j);
+      count += (uint32_t)__popcll(hits);
+    }
+  if (count > kWave) {
+#pragma unroll
+    for (uint32_t k = 0; k < kR; ++k) hide(x[k]);
+    const float kth = wave_bound<32>(top_k, [&](float y) {
+      uint32_t c = 0;
+#pragma unroll
+      for (uint32_t k = 0; k < kR; ++k) hide(x[k]);
+#pragma unroll
+      for (uint32_t e = 0; e < kE; ++e) c += lanes_of((float)x[e / kV][e % kV] >= y);
+      return c;
+    });
+    count = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < kR; ++k) hide(x[k]);
+#pragma unroll
+    for (uint32_t e = 0; e < kE; ++e) count += lanes_of((float)x[e / kV][e % kV] > kth);
+    uint32_t above = 0, equal = count;  // places of the larger ones, then of the equal ones
+    // vectors in the order of their columns: by k, then lane, then element
+#pragma unroll
+    for (uint32_t k = 0; k < kR; ++k) {
+      hide(x[k]);
+      uint32_t mine_equal = equal, all_equal = 0;
+#pragma unroll
+      for (uint32_t j = 0; j < kV; ++j) {
+        const uint64_t same = __ballot((float)x[k][j] == kth);
+        mine_equal += (uint32_t)__popcll(same & lower);
+        all_equal += (uint32_t)__popcll(same);
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < kV; ++j) {
+        const float y = (float)x[k][j];
+        const uint64_t hits = __ballot(y > kth);
+        const uint32_t place = y == kth ? mine_equal : above + (uint32_t)__popcll(hits & lower);
+        if (y >= kth && place < kWave) keys[place] = top_key(y, first + k * kWave * kV + j);
+        mine_equal += y == kth ? 1u : 0u;
+        above += (uint32_t)__popcll(hits);
+      }
+      equal += all_equal;
+    }
+    count = equal < kWave ? equal : kWave;
+  }
+  wave_lds_sync();
+  const uint64_t key = lane < count ? keys[lane] : 0ull;
+  const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
+  uint32_t place = 0;
+  for (uint32_t p = 0; p < count; ++p) {
+    const uint64_t other = ((uint64_t)readlane_u32(hi, p) << 32) | readlane_u32(lo, p);
+    place += other > key ? 1u : 0u;
+  }
+  place = lane < count ? place : lane;
+  if (place < top_k) write_top(o, i, place, key, r);
+  wave_lds_sync();
+}
 
 // A row per kLanes lanes, kR vectors per lane.
 template <class T, uint32_t kLanes, uint32_t kR>
@@ -161,14 +298,15 @@ __global__ void __launch_bounds__(kThreads)
                          Outputs o) {
   constexpr uint32_t kV = kVec<T>;
   constexpr uint32_t kGroups = kThreads / kLanes;
-  constexpr uint32_t kRoom = 2 * kWave;  // candidates in LDS, per wave
-  __shared__ uint64_t room[kLanes == kWave ? kWaves : 1][kLanes == kWave ? kRoom : 1];
-  if (blockIdx.x == 0 && o.targets != nullptr && !o.check)
-    report_ids<kThreads>(o.targets, n, v, o.status);
+  constexpr bool kWhole = kLanes == kWave;
+  __shared__ uint64_t room[kWhole ? kWaves : 1][kWhole ? kWave : 1];
   const uint32_t at = threadIdx.x % kLanes;
+  // (a wave's row is the same in all its lanes, which the compiler cannot see)
+  const uint32_t group = kWhole ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave))
+                                : threadIdx.x / kLanes;
   const uint64_t step = (uint64_t)gridDim.x * kGroups;
   for (uint64_t i0 = (uint64_t)blockIdx.x * kGroups; i0 < n; i0 += step) {
-    const uint64_t i = i0 + threadIdx.x / kLanes;
+    const uint64_t i = i0 + group;
     const bool live = i < n;
     const T *row = logits + (live ? i : 0) * ld;
     Vec<T> x[kR];
@@ -178,76 +316,44 @@ __global__ void __launch_bounds__(kThreads)
       if (live && c < v) x[k] = load_vec_tail(row, c, v, (T)kNegInf);
       else x[k] = (T)kNegInf;
     }
+    const Target<T> target(o, row, live ? i : 0, v);
     Sums a{kNegInf, 0.0f, 0.0f};
     add_vectors<T, kR>(a, x);
     const float mine = a.best;
     join_lanes<kLanes>(a);
     const Row r(a);
-    if (live && at == 0) write_row(o, row, i, v, a, r);
+    if (live && at == 0) write_row(o, i, target, a, r);
     if (o.top_k == 0) continue;
 
-    bool rounds = true;
-    if constexpr (kLanes == kWave) {
-      if (live && !r.none) {
-        float best[1] = {mine};
-        const float least = wave_kth<1>(best, o.top_k);
-        uint64_t *keys = room[threadIdx.x / kWave];
-        uint32_t count = 0;
+    if constexpr (kWhole) {
+      if (live) wave_top<T, kR>(o, i, v, x, mine, r, room[group]);
+    } else {
+      // one alternative per round
+      for (uint32_t q = 0; q < o.top_k; ++q) {
+        float best = kNegInf;
 #pragma unroll
-        for (uint32_t k = 0; k < kR; ++k) {
-          float top = (float)x[k][0];
-#pragma unroll
-          for (uint32_t j = 1; j < kV; ++j) top = fmaxf(top, (float)x[k][j]);
-          if (__ballot(top >= least && top > kNegInf) == 0) continue;
-#pragma unroll
-          for (uint32_t j = 0; j < kV; ++j) {
-            const float y = (float)x[k][j];
-            const bool hit = y >= least && y > kNegInf;
-            const uint64_t hits = __ballot(hit);
-            const uint32_t place = count + (uint32_t)__popcll(hits & ((1ull << at) - 1ull));
-            if (hit && place < kRoom) keys[place] = top_key(y, (k * kWave + at) * kV + j);
-            count += (uint32_t)__popcll(hits);
-          }
+        for (uint32_t j = 0; j < kV; ++j) best = fmaxf(best, (float)x[0][j]);
+        best = r.none ? kNegInf : group_max<kLanes>(best);
+        if (__ballot(best > kNegInf) == 0) {  // nothing left in any of the rows
+          for (uint32_t p = q + at; p < o.top_k; p += kLanes)
+            if (live) write_top(o, i, p, 0ull, r);
+          break;
         }
-        wave_lds_sync();
-        if (count <= kRoom) {
-          rounds = false;
-          for (uint32_t q = at; q < (count > o.top_k ? count : o.top_k); q += kWave) {
-            const uint64_t key = q < count ? keys[q] : 0ull;
-            uint32_t place = 0;
-            for (uint32_t p = 0; p < count; ++p) place += keys[p] > key ? 1u : 0u;
-            place = q < count ? place : q;
-            if (place < o.top_k) write_top(o, i, place, key, r);
-          }
-          wave_lds_sync();
-        }
-      }
-    }
-    if (!rounds) continue;
-    // one alternative per round: few lanes per row, or a row of many equals
-    for (uint32_t q = 0; q < o.top_k; ++q) {
-      float best = kNegInf;
-#pragma unroll
-      for (uint32_t k = 0; k < kR; ++k)
-#pragma unroll
-        for (uint32_t j = 0; j < kV; ++j) best = fmaxf(best, (float)x[k][j]);
-      best = group_max<kLanes>(best);
-      uint32_t c = 0xffffffffu;
-#pragma unroll
-      for (uint32_t k = kR; k-- > 0;)
+        uint32_t c = 0xffffffffu;
 #pragma unroll
         for (uint32_t j = kV; j-- > 0;)
-          if ((float)x[k][j] == best) c = (k * kLanes + at) * kV + j;
-      c = group_min_u32<kLanes>(c);
-#pragma unroll
-      for (uint32_t k = 0; k < kR; ++k)
+          if ((float)x[0][j] == best) c = at * kV + j;
+        c = group_min_u32<kLanes>(c);
 #pragma unroll
         for (uint32_t j = 0; j < kV; ++j)
-          if ((k * kLanes + at) * kV + j == c) x[k][j] = (T)kNegInf;
-      if (live && at == 0)
-        write_top(o, i, q, best > kNegInf && !r.none ? top_key(best, c) : 0ull, r);
+          if (at * kV + j == c) x[0][j] = (T)kNegInf;
+        if (live && at == 0) write_top(o, i, q, best > kNegInf ? top_key(best, c) : 0ull, r);
+      }
     }
   }
+  // after the rows: the other blocks' work hides it
+  if (blockIdx.x == 0 && o.targets != nullptr && !o.check)
+    report_ids<kThreads>(o.targets, n, v, o.status);
 }
 
 // --- rows that are streamed -------------------------------------------------------
@@ -258,8 +364,8 @@ constexpr uint32_t kRoom = 1024;  // candidates in LDS
 struct Stream {
   float best[kThreads];
   Sums wave[kWaves];
-  float least;
-  uint32_t count;
+  uint32_t holders, count;
+  uint16_t holder[kThreads];
   uint64_t keys[kRoom];
   uint64_t wave_key[kWaves];
 };
@@ -267,51 +373,47 @@ struct Stream {
 // The candidates of columns [q0, q1) (in vectors) go to sh.keys, best first at
 // their place; f(place, key) is called by the thread that holds it, for the
 // places below top_k, key 0 where nothing is left. `mine` is the maximum of
-// the thread's own columns.
+// the thread's own columns, every kThreads-th vector from q0 + its place. The
+// columns of the threads whose maxima reach the bound ("holders", hardly more
+// than top_k) are read again, by all threads: one latency, not a column's
+// length of them (4096 x 50001 bf16 with 8: 26 us of the whole call against
+// HOLD).
 template <class T, class F>
 __device__ __forceinline__ void block_top(Stream &sh, const T *row, uint32_t q0, uint32_t q1,
                                           uint32_t v, uint32_t top_k, float mine, F &&f) {
   constexpr uint32_t kV = kVec<T>;
   sh.best[threadIdx.x] = mine;
-  if (threadIdx.x == 0) sh.count = 0;
+  if (threadIdx.x == 0) sh.holders = sh.count = 0;
   __syncthreads();
-  if (threadIdx.x < kWave) {
-    float x[kWaves];
+  float sets[kWaves];
 #pragma unroll
-    for (uint32_t k = 0; k < kWaves; ++k) x[k] = sh.best[k * kWave + threadIdx.x];
-#pragma unroll
-    for (uint32_t a = 0; a + 1 < kWaves; ++a)
-#pragma unroll
-      for (uint32_t b = 0; b + 1 < kWaves - a; ++b) {
-        const float hi = fmaxf(x[b], x[b + 1]), lo = fminf(x[b], x[b + 1]);
-        x[b] = hi;
-        x[b + 1] = lo;
-      }
-    const float least = wave_kth<kWaves>(x, top_k);
-    if (threadIdx.x == 0) sh.least = least;
-  }
+  for (uint32_t k = 0; k < kWaves; ++k) sets[k] = sh.best[k * kWave + lane_id()];
+  const float least = wave_bound_of<kWaves>(sets, top_k);
+  if (mine >= least) sh.holder[atomicAdd(&sh.holders, 1u)] = (uint16_t)threadIdx.x;
   __syncthreads();
-  const float least = sh.least;
-  if (mine >= least && mine > kNegInf) {
-    for (uint32_t q = q0 + threadIdx.x; q < q1; q += kThreads * kUnroll) {
-      Vec<T> x[kUnroll];
+  const uint32_t holders = sh.holders;
+  const uint32_t total = holders * ((q1 - q0 + kThreads - 1) / kThreads);
+  for (uint32_t w = threadIdx.x; w < total; w += kThreads * kUnroll) {
+    Vec<T> x[kUnroll];
+    uint32_t at[kUnroll];
 #pragma unroll
-      for (uint32_t u = 0; u < kUnroll; ++u) {
-        const uint32_t p = q + u * kThreads;
-        if (p < q1) x[u] = load_vec_tail(row, p * kV, v, (T)kNegInf);
-        else x[u] = (T)kNegInf;
-      }
-#pragma unroll
-      for (uint32_t u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (uint32_t j = 0; j < kV; ++j) {
-          const float y = (float)x[u][j];
-          if (y >= least && y > kNegInf) {
-            const uint32_t place = atomicAdd(&sh.count, 1u);
-            if (place < kRoom) sh.keys[place] = top_key(y, (q + u * kThreads) * kV + j);
-          }
-        }
+    for (uint32_t u = 0; u < kUnroll; ++u) {
+      const uint32_t z = w + u * kThreads, turn = z / holders;
+      const uint32_t q = z < total ? q0 + turn * kThreads + sh.holder[z - turn * holders] : q1;
+      at[u] = q * kV;
+      if (q < q1) x[u] = load_vec_tail(row, q * kV, v, (T)kNegInf);
+      else x[u] = (T)kNegInf;
     }
+#pragma unroll
+    for (uint32_t u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (uint32_t j = 0; j < kV; ++j) {
+        const float y = (float)x[u][j];
+        if (y >= least) {
+          const uint32_t place = atomicAdd(&sh.count, 1u);
+          if (place < kRoom) sh.keys[place] = top_key(y, at[u] + j);
+        }
+      }
   }
   __syncthreads();
   const uint32_t count = sh.count;
@@ -319,6 +421,7 @@ __device__ __forceinline__ void block_top(Stream &sh, const T *row, uint32_t q0,
     for (uint32_t q = threadIdx.x; q < (count > top_k ? count : top_k); q += kThreads) {
       const uint64_t key = q < count ? sh.keys[q] : 0ull;
       uint32_t place = 0;
+#pragma unroll 8
       for (uint32_t p = 0; p < count; ++p) place += sh.keys[p] > key ? 1u : 0u;
       place = q < count ? place : q;
       if (place < top_k) f(place, key);
@@ -360,13 +463,12 @@ __global__ void __launch_bounds__(kThreads)
   constexpr uint32_t kV = kVec<T>;
   __shared__ Stream sh;
   const uint32_t parts = gridDim.y, part = blockIdx.y;
-  if (blockIdx.x == 0 && part == 0 && o.targets != nullptr && !o.check)
-    report_ids<kThreads>(o.targets, n, v, o.status);
   const uint32_t vecs = (v + kV - 1) / kV;
   const uint32_t q0 = (uint32_t)((uint64_t)vecs * part / parts);
   const uint32_t q1 = (uint32_t)((uint64_t)vecs * (part + 1) / parts);
   for (uint64_t i = blockIdx.x; i < n; i += gridDim.x) {
     const T *row = logits + i * ld;
+    const Target<T> target(o, row, i, v);
     Sums a{kNegInf, 0.0f, 0.0f};
     for (uint32_t q = q0; q < q1; q += kThreads * kUnroll) {
       Vec<T> x[kUnroll];
@@ -402,7 +504,7 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     if (parts == 1) {
       const Row r(a);
-      if (threadIdx.x == 0) write_row(o, row, i, v, a, r);
+      if (threadIdx.x == 0) write_row(o, i, target, a, r);
       if (o.top_k == 0) continue;
       if (r.none) {
         if (threadIdx.x < o.top_k) write_top(o, i, threadIdx.x, 0ull, r);
@@ -418,32 +520,43 @@ __global__ void __launch_bounds__(kThreads)
                    [&](uint32_t place, uint64_t key) { to[place] = key; });
     }
   }
+  // after the rows: the other blocks' work hides it
+  if (blockIdx.x == 0 && part == 0 && o.targets != nullptr && !o.check)
+    report_ids<kThreads>(o.targets, n, v, o.status);
 }
 
 // The parts of a row, one per lane, in one wave: their sums joined, their
-// ordered candidates merged.
+// ordered candidates merged from LDS, lane q keeping the q-th.
 template <class T>
 __global__ void __launch_bounds__(kWave)
     logprobs_join_kernel(const T *__restrict__ logits, uint32_t n, uint32_t v, uint64_t ld,
                          uint32_t parts, Outputs o, const Sums *__restrict__ part_sums,
                          const uint64_t *__restrict__ part_keys) {
-  const uint32_t lane = lane_id();
+  extern __shared__ uint64_t lists[];  // [parts][top_k]
+  const uint32_t lane = lane_id(), top_k = o.top_k;
   for (uint64_t i = blockIdx.x; i < n; i += gridDim.x) {
+    const uint64_t *keys = part_keys + i * parts * top_k;
+#pragma unroll 8
+    for (uint32_t q = lane; q < parts * top_k; q += kWave) lists[q] = keys[q];
+    const Target<T> target(o, logits + i * ld, i, v);
     Sums a{kNegInf, 0.0f, 0.0f};
     if (lane < parts) a = part_sums[i * parts + lane];
     join_lanes<kWave>(a);
     const Row r(a);
-    if (lane == 0) write_row(o, logits + i * ld, i, v, a, r);
-    const uint64_t *keys = part_keys + (i * parts + lane) * o.top_k;
-    uint32_t next = 0;
-    uint64_t head = lane < parts && o.top_k > 0 && !r.none ? keys[0] : 0ull;
-    for (uint32_t q = 0; q < o.top_k; ++q) {
+    if (lane == 0) write_row(o, i, target, a, r);
+    if (top_k == 0) continue;
+    wave_lds_sync();
+    uint32_t next = lane * top_k;
+    uint64_t head = lane < parts && !r.none ? lists[next] : 0ull, mine = 0;
+    for (uint32_t q = 0; q < top_k; ++q) {
       const uint32_t hi = ~wave_min_u32(~(uint32_t)(head >> 32));
       const uint32_t lo = ~wave_min_u32((uint32_t)(head >> 32) == hi ? ~(uint32_t)head : ~0u);
       const uint64_t key = ((uint64_t)hi << 32) | lo;
-      if (lane == 0) write_top(o, i, q, key, r);
-      if (key != 0 && head == key) head = ++next < o.top_k ? keys[next] : 0ull;
+      if (lane == q) mine = key;
+      if (key != 0 && head == key) head = ++next < (lane + 1) * top_k ? lists[next] : 0ull;
     }
+    if (lane < top_k) write_top(o, i, lane, mine, r);
+    wave_lds_sync();
   }
 }
 
@@ -523,14 +636,18 @@ struct Group {
   static constexpr uint32_t lanes = kLanes_, vecs = kR_;
 };
 
+// Rows of more than 8 lanes that are asked for many alternatives get a wave
+// (a round per alternative would cost more than the lanes left idle).
 template <class F>
-bool held_group(uint32_t vecs, F &&f) {
+bool held_group(uint32_t vecs, uint32_t top_k, F &&f) {
   if (vecs <= 8) f(Group<8, 1>{});
   else if (vecs <= 16) f(Group<16, 1>{});
-  else if (vecs <= 32) f(Group<32, 1>{});
+  else if (vecs <= 32 && top_k <= 16) f(Group<32, 1>{});
   else if (vecs <= 64) f(Group<64, 1>{});
   else if (vecs <= 128) f(Group<64, 2>{});
+  else if (vecs <= 192) f(Group<64, 3>{});
   else if (vecs <= 256) f(Group<64, 4>{});
+  else if (vecs <= 384) f(Group<64, 6>{});
   else if (vecs <= 512) f(Group<64, 8>{});
   else return false;
   return true;
@@ -573,7 +690,7 @@ hipError_t launch_logprobs(const LogprobsPlan &plan, const void *logits, uint32_
   return with_type(dtype, [&](auto t) {
     using T = decltype(t);
     const T *x = static_cast<const T *>(logits);
-    const bool held = held_group(div_up(v, kVec<T>), [&](auto g) {
+    const bool held = held_group(div_up(v, kVec<T>), top_k, [&](auto g) {
       using G = decltype(g);
       hipLaunchKernelGGL((logprobs_held_kernel<T, G::lanes, G::vecs>),
                          dim3(capped(div_up(n, kThreads / G::lanes))), dim3(kThreads), 0, stream, x,
@@ -586,8 +703,9 @@ hipError_t launch_logprobs(const LogprobsPlan &plan, const void *logits, uint32_
                        stream, x, n, v, ld, o, sums, keys);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || plan.parts == 1) return e;
-    hipLaunchKernelGGL((logprobs_join_kernel<T>), dim3(n), dim3(kWave), 0, stream, x, n, v, ld,
-                       plan.parts, o, sums, keys);
+    hipLaunchKernelGGL((logprobs_join_kernel<T>), dim3(n), dim3(kWave),
+                       plan.parts * top_k * sizeof(uint64_t), stream, x, n, v, ld, plan.parts, o,
+                       sums, keys);
     return hipGetLastError();
   });
 }

@@ -137,15 +137,21 @@ __device__ __forceinline__ float group_max(float x) {
   return x;
 }
 
+// One DPP step of a minimum: the lane's own value where it has no partner.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_min_u32(uint32_t x) {
+  return min(x, (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, kCtrl, 0xF, 0xF, false));
+}
+
 template <uint32_t kLanes>
 __device__ __forceinline__ uint32_t group_min_u32(uint32_t x) {
-  if constexpr (kLanes == kWave) {
-    return wave_min_u32(x);
-  } else {
-#pragma unroll
-    for (uint32_t off = 1; off < kLanes; off *= 2) x = min(x, __shfl_xor(x, (int)off, kWave));
-    return x;
-  }
+  if constexpr (kLanes == kWave) return wave_min_u32(x);
+  x = dpp_min_u32<0xB1>(x);
+  x = dpp_min_u32<0x4E>(x);
+  x = dpp_min_u32<0x141>(x);
+  if (kLanes >= 16) x = dpp_min_u32<0x140>(x);
+  if (kLanes == 32) x = min(x, (uint32_t)__shfl_xor((int)x, 16, kWave));
+  return x;
 }
 
 // Ids (tokens, targets) that one block of threads can look over beside its
