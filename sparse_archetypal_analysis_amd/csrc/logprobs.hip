@@ -125,16 +125,18 @@ struct Outputs {
   bool check;  // flag targets past the row here (else one block looks at all)
 };
 
-// A row's target and its logit, fetched before the row's sums so that the two
-// dependent loads do not follow them.
+// A row's target and its logit: two dependent loads, each started early enough
+// not to be waited for.
 template <class T>
 struct Target {
   int32_t id;
   bool bad;
   T x;
-  __device__ __forceinline__ Target(const Outputs &o, const T *row, uint64_t i, uint32_t v) {
+  __device__ __forceinline__ Target(const Outputs &o, uint64_t i, uint32_t v) {
     id = o.targets != nullptr ? o.targets[i] : -1;
     bad = id >= 0 && (uint32_t)id >= v;
+  }
+  __device__ __forceinline__ void fetch(const Outputs &o, const T *row) {
     x = o.logp != nullptr && id >= 0 && !bad ? row[id] : (T)0.0f;
   }
 };
@@ -158,38 +160,77 @@ __device__ __forceinline__ void write_top(const Outputs &o, uint64_t i, uint32_t
   o.top_logp[i * o.top_k + place] = r.log_p(key != 0 ? f32_unorder((uint32_t)(key >> 32)) : kNegInf);
 }
 
-// The largest number that k of the wave's values reach, to its order's highest
-// kBits bits and from below (16: 7 bits of the mantissa; 32: the k-th largest
-// value itself), but at least the lowest finite value: what is at or above it
-// holds the k largest ones that are not masked. Found bit by bit, whatever k
-// is; reach(y) counts the values >= y (orders past infinity are NaN: none).
-template <uint32_t kBits, class F>
+// The k-th largest of a wave's values, but at least the lowest finite one (what
+// is below is masked), bit by bit of its order, whatever k is. reach(y) counts
+// the values >= y (orders past infinity are NaN: none).
+template <class F>
 __device__ __forceinline__ float wave_bound(uint32_t k, F &&reach) {
   uint32_t at = 0;
-  for (uint32_t bit = 1u << 31; bit >= 1u << (32 - kBits) && bit != 0; bit >>= 1)
+  for (uint32_t bit = 1u << 31; bit != 0; bit >>= 1)
     at = reach(f32_unorder(at | bit)) >= k ? at | bit : at;
   return fmaxf(f32_unorder(at), kLowest);
 }
 
 __device__ __forceinline__ uint32_t lanes_of(bool x) { return (uint32_t)__popcll(__ballot(x)); }
 
+// A bound of it from below for kN values per lane: 16 bits of its order, that is
+// 7 of the mantissa (orders compared, not numbers: 5 operations a step).
 template <uint32_t kN>
 __device__ __forceinline__ float wave_bound_of(const float (&x)[kN], uint32_t k) {
-  return wave_bound<16>(k, [&](float y) {
-    uint32_t c = 0;
+  uint32_t key[kN];
 #pragma unroll
-    for (uint32_t j = 0; j < kN; ++j) c += lanes_of(x[j] >= y);
-    return c;
-  });
+  for (uint32_t j = 0; j < kN; ++j) key[j] = f32_order(x[j]);
+  uint32_t at = 0;
+#pragma unroll 4
+  for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
+    uint32_t reach = 0;
+#pragma unroll
+    for (uint32_t j = 0; j < kN; ++j) reach += lanes_of(key[j] >= (at | bit));
+    at = reach >= k ? at | bit : at;
+  }
+  return fmaxf(f32_unorder(at), kLowest);
 }
 
 // --- rows that a wave's registers hold ------------------------------------------
 
+// Candidates that a wave orders.
+constexpr uint32_t kTopRoom = 2 * kWave;
+
+// The first top_k of `count` keys in LDS, kK of them per lane, written at
+// their places: a key's place is the count of the larger ones.
+template <uint32_t kK>
+__device__ __forceinline__ void order_top(const Outputs &o, uint64_t i, const Row &r,
+                                          const uint64_t *keys, uint32_t count) {
+  const uint32_t lane = lane_id();
+  uint64_t key[kK];
+  uint32_t place[kK];
+#pragma unroll
+  for (uint32_t m = 0; m < kK; ++m) {
+    key[m] = m * kWave + lane < count ? keys[m * kWave + lane] : 0ull;
+    place[m] = 0;
+  }
+#pragma unroll
+  for (uint32_t m = 0; m < kK; ++m) {
+    const uint32_t hi = (uint32_t)(key[m] >> 32), lo = (uint32_t)key[m];
+    const uint32_t here = min(count - min(count, m * kWave), kWave);
+    for (uint32_t p = 0; p < here; ++p) {
+      const uint64_t other = ((uint64_t)readlane_u32(hi, p) << 32) | readlane_u32(lo, p);
+#pragma unroll
+      for (uint32_t l = 0; l < kK; ++l) place[l] += other > key[l] ? 1u : 0u;
+    }
+  }
+#pragma unroll
+  for (uint32_t m = 0; m < kK; ++m) {
+    const uint32_t q = m * kWave + lane < count ? place[m] : m * kWave + lane;
+    if (q < o.top_k) write_top(o, i, q, key[m], r);
+  }
+}
+
 // The alternatives of a row that a wave holds. A lane's largest element (mine)
 // stands for its others: the bound that top_k of those reach, or of up to 8
 // from each lane where the lanes are too few, leaves hardly more than top_k
-// elements, which go to LDS and are ordered there by counting. Should more
-// than a wave's lanes be left (many equals, or a bound too coarse), the
+// elements, which go to LDS and are ordered by counting. Should more than
+// kTopRoom be left (many equals, or a bound too coarse), the
 // top_k-th largest element itself is looked for, and of those that equal it
 // the first columns are taken.
 template <class T, uint32_t kR>
@@ -234,13 +275,13 @@ __device__ __forceinline__ void wave_top(const Outputs &o, uint64_t i, uint32_t 
       const uint64_t hits = __ballot(hit);
       if (hits == 0) continue;
       const uint32_t place = count + (uint32_t)__popcll(hits & lower);
-      if (hit && place < kWave) keys[place] = top_key(y, first + k * kWave * kV + j);
+      if (hit && place < kTopRoom) keys[place] = top_key(y, first + k * kWave * kV + j);
       count += (uint32_t)__popcll(hits);
     }
-  if (count > kWave) {
+  if (count > kTopRoom) {
 #pragma unroll
     for (uint32_t k = 0; k < kR; ++k) hide(x[k]);
-    const float kth = wave_bound<32>(top_k, [&](float y) {
+    const float kth = wave_bound(top_k, [&](float y) {
       uint32_t c = 0;
 #pragma unroll
       for (uint32_t k = 0; k < kR; ++k) hide(x[k]);
@@ -279,15 +320,8 @@ __device__ __forceinline__ void wave_top(const Outputs &o, uint64_t i, uint32_t 
     count = equal < kWave ? equal : kWave;
   }
   wave_lds_sync();
-  const uint64_t key = lane < count ? keys[lane] : 0ull;
-  const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
-  uint32_t place = 0;
-  for (uint32_t p = 0; p < count; ++p) {
-    const uint64_t other = ((uint64_t)readlane_u32(hi, p) << 32) | readlane_u32(lo, p);
-    place += other > key ? 1u : 0u;
-  }
-  place = lane < count ? place : lane;
-  if (place < top_k) write_top(o, i, place, key, r);
+  if (count <= kWave) order_top<1>(o, i, r, keys, count);
+  else order_top<kTopRoom / kWave>(o, i, r, keys, count);
   wave_lds_sync();
 }
 
@@ -299,7 +333,7 @@ __global__ void __launch_bounds__(kThreads)
   constexpr uint32_t kV = kVec<T>;
   constexpr uint32_t kGroups = kThreads / kLanes;
   constexpr bool kWhole = kLanes == kWave;
-  __shared__ uint64_t room[kWhole ? kWaves : 1][kWhole ? kWave : 1];
+  __shared__ uint64_t room[kWhole ? kWaves : 1][kWhole ? kTopRoom : 1];
   const uint32_t at = threadIdx.x % kLanes;
   // (a wave's row is the same in all its lanes, which the compiler cannot see)
   const uint32_t group = kWhole ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave))
@@ -310,13 +344,9 @@ __global__ void __launch_bounds__(kThreads)
     const bool live = i < n;
     const T *row = logits + (live ? i : 0) * ld;
     Vec<T> x[kR];
-#pragma unroll
-    for (uint32_t k = 0; k < kR; ++k) {
-      const uint32_t c = (k * kLanes + at) * kV;
-      if (live && c < v) x[k] = load_vec_tail(row, c, v, (T)kNegInf);
-      else x[k] = (T)kNegInf;
-    }
-    const Target<T> target(o, row, live ? i : 0, v);
+    load_row<T, kLanes, kR>(row, at, v, live, (T)kNegInf, x);
+    Target<T> target(o, live ? i : 0, v);
+    target.fetch(o, row);
     Sums a{kNegInf, 0.0f, 0.0f};
     add_vectors<T, kR>(a, x);
     const float mine = a.best;
@@ -468,7 +498,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t q1 = (uint32_t)((uint64_t)vecs * (part + 1) / parts);
   for (uint64_t i = blockIdx.x; i < n; i += gridDim.x) {
     const T *row = logits + i * ld;
-    const Target<T> target(o, row, i, v);
+    Target<T> target(o, i, v);
     Sums a{kNegInf, 0.0f, 0.0f};
     for (uint32_t q = q0; q < q1; q += kThreads * kUnroll) {
       Vec<T> x[kUnroll];
@@ -486,6 +516,7 @@ __global__ void __launch_bounds__(kThreads)
       }
       add_vectors<T, kUnroll>(a, x);
     }
+    target.fetch(o, row);
     const float mine = a.best;
     join_lanes<kWave>(a);
     if (lane_id() == 0) sh.wave[threadIdx.x / kWave] = a;
@@ -538,7 +569,8 @@ __global__ void __launch_bounds__(kWave)
     const uint64_t *keys = part_keys + i * parts * top_k;
 #pragma unroll 8
     for (uint32_t q = lane; q < parts * top_k; q += kWave) lists[q] = keys[q];
-    const Target<T> target(o, logits + i * ld, i, v);
+    Target<T> target(o, i, v);
+    target.fetch(o, logits + i * ld);
     Sums a{kNegInf, 0.0f, 0.0f};
     if (lane < parts) a = part_sums[i * parts + lane];
     join_lanes<kWave>(a);

@@ -47,6 +47,29 @@ __device__ __forceinline__ Vec<T> load_vec_tail(const T *row, uint32_t at, uint3
   return v;
 }
 
+// A row of d elements over kStride lanes, kR vectors each: x[k] holds the
+// elements from (k * kStride + at) * kVec<T>, those past the end `fill`. The
+// row's one broken vector has a branch of its own (a branch in each load took
+// up to twice the registers).
+template <class T, uint32_t kStride, uint32_t kR>
+__device__ __forceinline__ void load_row(const T *row, uint32_t at, uint32_t d, bool live, T fill,
+                                         Vec<T> (&x)[kR]) {
+  constexpr uint32_t kV = kVec<T>;
+#pragma unroll
+  for (uint32_t k = 0; k < kR; ++k) {
+    const uint32_t c = (k * kStride + at) * kV;
+    x[k] = fill;
+    if (live && c + kV <= d) x[k] = load_vec(row + c);
+  }
+  const uint32_t last = d / kV;  // the broken vector, if there is one
+  if (d % kV != 0 && live && at == last % kStride) {
+    const Vec<T> y = load_vec_tail(row, last * kV, d, fill);
+#pragma unroll
+    for (uint32_t k = 0; k < kR; ++k)
+      if (k == last / kStride) x[k] = y;
+  }
+}
+
 template <class T>
 __device__ __forceinline__ void store_vec_tail(T *row, uint32_t at, uint32_t end, Vec<T> v) {
   if (at + kVec<T> <= end) {
