@@ -123,6 +123,9 @@ __device__ __forceinline__ float dpp_same_f32(float x) {
       (int)__float_as_uint(x), (int)__float_as_uint(x), kCtrl, kRows, 0xF, false));
 }
 
+// How many lanes of the wave say yes.
+__device__ __forceinline__ uint32_t lanes_of(bool x) { return (uint32_t)__popcll(__ballot(x)); }
+
 // Sum over each group of kLanes neighbouring lanes (8, 16, 32 or 64) in a
 // fixed order, the result in every lane of the group. Called with every lane
 // active. quad_perm, half-row and row mirrors as in wave_min_u32; over the
@@ -233,10 +236,11 @@ hipError_t launch_embed(const void *table, uint32_t dtype, uint32_t v, uint32_t 
                         uint32_t *status, hipStream_t stream);
 
 struct EmbedGradPlan {
-  uint32_t ids;     // table rows per block of the token sort
-  uint32_t blocks;  // blocks of the token sort
-  uint32_t windows; // windows of sorted positions, 0 if no id can be heavy
-  size_t off_perm, off_start, off_part;
+  uint32_t shift;    // table rows per bucket of the token sort: 2^shift
+  uint32_t buckets;
+  uint32_t per;      // tokens of a chunk per thread
+  uint32_t chunks;   // 0: the buckets read the tokens themselves
+  size_t off_perm, off_sorted, off_start, off_open, off_entry_id, off_entry_pos, off_cuts, off_part;
   size_t ws_bytes;
 };
 EmbedGradPlan plan_embed_grad(uint32_t n, uint32_t v, uint32_t d);

@@ -143,6 +143,26 @@ def test_embed_grad(n, v, d, dtype, out_dtype, add):
     untouched(base, out)
 
 
+@pytest.mark.parametrize("n,v,d", [(2047, 900, 5), (2048, 300, 9), (2049, 300, 9), (33000, 513, 2),
+                                   (100000, 5000, 7), (600000, 3000, 1), (600000, 5, 1),
+                                   (40000, 1200000, 1), (30000, 1, 515), (20000, 9, 1031)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_embed_grad_of_many_tokens_and_ids(n, v, d, dtype):
+    """Sizes around the steps of the sort: tokens read by the buckets or by
+    chunks, chunks beyond a block's threads, several ranges of ids per bucket,
+    ids that cross many windows."""
+    rng = np.random.default_rng(n + v + d)
+    tok, d_out = ids(rng, n, v), rows(rng, n, d, dtype, gap=1, start=1)
+    base, out = blank(v, d, "f32", gap=1, start=1)
+    _, st = saa.seacells_embed_grad(tok, d_out, v, d_table=out)
+    assert flags(st) == []
+    want, bound = R.embed_grad(exact(tok), exact(d_out), v, 1.0, None, "f32")
+    within(out, want, bound, "d_table")
+    untouched(base, out)
+    tok[n // 2] = v
+    assert flags(saa.seacells_embed_grad(tok, d_out, v, d_table=out)[1]) == ["BAD_INDEX"]
+
+
 @pytest.mark.parametrize("n,v,d", [(5000, 600, 33), (9000, 3, 130), (70000, 40, 3)])
 def test_embed_grad_is_the_same_every_time(n, v, d):
     rng = np.random.default_rng(1)
