@@ -99,6 +99,8 @@ int seacells_embed_grad(const int32_t *tokens, uint32_t n, const void *d_out, ui
  *               be NULL (1 and 0).
  * mean, rstd    device [n] f32 out, or NULL.
  * eps           finite, >= 0.
+ * A row that holds NaN or an infinity gets NaN in out and rstd, and a mean that
+ * is not finite.
  */
 int seacells_layer_norm(const void *x, uint32_t dtype, uint32_t n, uint32_t d, uint64_t x_ld,
                         const void *weight, const void *bias, uint32_t weight_type, float eps,

@@ -18,32 +18,85 @@ namespace {
 constexpr uint32_t kThreads = 256;
 constexpr uint32_t kMaxBlocks = 1u << 20;
 
+// How the lanes cover the columns: `lanes` (a power of two, at most a wave)
+// side by side with a vector each, then further slabs.
+struct Cover {
+  uint32_t lanes, slabs;
+};
+
+template <uint32_t kV>
+Cover cover(uint32_t d) {
+  Cover c{};
+  const uint32_t vecs = div_up(d, kV);
+  c.lanes = 1;
+  while (c.lanes < kWave && c.lanes < vecs) c.lanes *= 2;
+  c.slabs = div_up(vecs, c.lanes);
+  return c;
+}
+
 // --- lookup -----------------------------------------------------------------
 
-template <class T>
+constexpr uint32_t kRows = 4;  // rows in flight per lane group
+
+// A vector of kRows rows per lane. A row's broken last vector is pulled back
+// to end with the row (its first columns are written twice, the same), and
+// where there is nothing to look up row 0 is loaded: no load has a branch, so
+// they are all in flight together. kWhole: a group is a wave, whose tokens the
+// scalar unit reads.
+template <class T, bool kWhole>
 __global__ void __launch_bounds__(kThreads)
     embed_kernel(const T *__restrict__ table, uint32_t v, uint32_t d, uint64_t table_ld,
                  const int32_t *__restrict__ tokens, uint32_t n, float scale, T *__restrict__ out,
-                 uint64_t out_ld, uint32_t *__restrict__ status) {
-  const uint32_t lane = lane_id();
-  const uint32_t waves = gridDim.x * (kThreads / kWave);
-  for (uint64_t i = blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave; i < n; i += waves) {
-    const int32_t t = tokens[i];
-    const bool bad = t >= 0 && (uint32_t)t >= v;
-    if (bad && lane == 0) atomicOr(status, kFlagBadIndex);
-    const bool have = t >= 0 && !bad;
-    const T *row = table + (have ? (uint64_t)t * table_ld : 0);
-    T *to = out + i * out_ld;
-    for (uint32_t c = lane * kVec<T>; c < d; c += kWave * kVec<T>) {
-      Vec<T> y = {};
-      if (have) {
-        const Vec<T> x = load_vec_tail(row, c, d, (T)0.0f);
+                 uint64_t out_ld, uint32_t lanes_, uint32_t slabs, uint32_t *__restrict__ status,
+                 bool check) {
+  constexpr uint32_t kV = kVec<T>;
+  const uint32_t lanes = kWhole ? kWave : lanes_;
+  const uint32_t groups = kThreads / lanes;
+  const uint32_t group =
+      kWhole ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave))
+             : threadIdx.x / lanes;
+  const uint32_t lane = threadIdx.x & (lanes - 1);
+  const uint32_t slab = blockIdx.x % slabs;
+  const uint32_t col = (slab * lanes + lane) * kV;
+  const uint32_t at = d < kV ? 0u : col < d - kV ? col : d - kV;
+  const uint64_t step = (uint64_t)(gridDim.x / slabs) * groups * kRows;
+  for (uint64_t i0 = (uint64_t)(blockIdx.x / slabs) * groups * kRows + group; i0 < n; i0 += step) {
+    int32_t t[kRows];
+    bool have[kRows];
 #pragma unroll
-        for (uint32_t j = 0; j < kVec<T>; ++j) y[j] = (T)((float)x[j] * scale);
-      }
-      store_vec_tail(to, c, d, y);
+    for (uint32_t u = 0; u < kRows; ++u)
+      t[u] = i0 + u * groups < n ? tokens[i0 + u * groups] : -1;
+#pragma unroll
+    for (uint32_t u = 0; u < kRows; ++u) {
+      have[u] = t[u] >= 0 && t[u] < (int32_t)v;
+      if (check && t[u] >= (int32_t)v && lane == 0) atomicOr(status, kFlagBadIndex);
+    }
+    Vec<T> x[kRows];
+    if (d >= kV) {
+#pragma unroll
+      for (uint32_t u = 0; u < kRows; ++u)
+        x[u] = load_vec(table + (have[u] ? (uint64_t)t[u] * table_ld : 0) + at);
+    } else {
+#pragma unroll
+      for (uint32_t u = 0; u < kRows; ++u)
+#pragma unroll
+        for (uint32_t j = 0; j < kV; ++j)
+          x[u][j] = table[(have[u] ? (uint64_t)t[u] * table_ld : 0) + (j < d ? j : 0u)];
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < kRows; ++u) {
+      if (i0 + u * groups >= n || col >= d) break;
+      T *to = out + (i0 + u * groups) * out_ld + at;
+      Vec<T> y = {};
+      if (have[u])
+#pragma unroll
+        for (uint32_t j = 0; j < kV; ++j) y[j] = (T)((float)x[u][j] * scale);
+      if (d >= kV) store_stream(to, y);
+      else store_vec_tail(to, 0u, d, y);
     }
   }
+  // after the rows: the other blocks' work hides it
+  if (!check && blockIdx.x == 0) report_ids<kThreads>(tokens, n, v, status);
 }
 
 // --- token sort -------------------------------------------------------------
@@ -370,22 +423,6 @@ __global__ void __launch_bounds__(kSortThreads)
 
 // --- table gradient ---------------------------------------------------------
 
-// How the lanes cover the columns: `lanes` (a power of two, at most a wave)
-// side by side with a vector each, then further slabs.
-struct Cover {
-  uint32_t lanes, slabs;
-};
-
-template <uint32_t kV>
-Cover cover(uint32_t d) {
-  Cover c{};
-  const uint32_t vecs = div_up(d, kV);
-  c.lanes = 1;
-  while (c.lanes < kWave && c.lanes < vecs) c.lanes *= 2;
-  c.slabs = div_up(vecs, c.lanes);
-  return c;
-}
-
 // to[at + j] = so_far + scale * acc[j] for the columns at + j in [c, c + kV)
 // and below d (at < c in a row's last vector, where it is pulled back).
 template <class O, uint32_t kV>
@@ -401,7 +438,7 @@ __device__ __forceinline__ void write_row(const O *so_far, O *to, uint32_t at, u
 #pragma unroll
       for (uint32_t j = 0; j < kV; ++j) y[j] = (O)(scale * acc[j]);
     }
-    *reinterpret_cast<Pack<O, kV> *>(to + c) = y;
+    store_stream(to + c, y);
     return;
   }
 #pragma unroll
@@ -450,7 +487,7 @@ __device__ __forceinline__ void fill_rows(const uint32_t *__restrict__ start, ui
       for (uint32_t u = 0; u < kU; ++u)
         if (empty[u])
           for (uint32_t c = c0; c < d; c += lanes * kVec<O>)
-            store_vec_tail(d_table + (uint64_t)(r + u * groups) * ld, c, d, Vec<O>{});
+            store_vec_tail<O, true>(d_table + (uint64_t)(r + u * groups) * ld, c, d, Vec<O>{});
       continue;
     }
     for (uint32_t c = c0; c < d; c += lanes * kVec<O>) {
@@ -461,7 +498,8 @@ __device__ __forceinline__ void fill_rows(const uint32_t *__restrict__ start, ui
           y[u] = load_vec_tail(add_to + (uint64_t)(r + u * groups) * ld, c, d, (O)0.0f);
 #pragma unroll
       for (uint32_t u = 0; u < kU; ++u)
-        if (empty[u]) store_vec_tail(d_table + (uint64_t)(r + u * groups) * ld, c, d, y[u]);
+        if (empty[u])
+          store_vec_tail<O, true>(d_table + (uint64_t)(r + u * groups) * ld, c, d, y[u]);
     }
   }
 }
@@ -675,23 +713,27 @@ __global__ void __launch_bounds__(kJoinThreads)
   finish(all.id);
 }
 
-uint32_t wave_blocks(uint64_t waves) {
-  const uint64_t b = (waves + kThreads / kWave - 1) / (kThreads / kWave);
-  return (uint32_t)(b < kMaxBlocks ? b : kMaxBlocks);
-}
-
 }  // namespace
 
 hipError_t launch_embed(const void *table, uint32_t dtype, uint32_t v, uint32_t d, uint64_t table_ld,
                         const int32_t *tokens, uint32_t n, float scale, void *out, uint64_t out_ld,
                         uint32_t *status, hipStream_t stream) {
-  hipError_t e = launch_status_clear(status, stream);
-  if (e != hipSuccess || n == 0) return e;
+  const bool one = n > 0 && n <= kIdsOfOneBlock;
+  if (!one) {
+    const hipError_t e = launch_status_clear(status, stream);
+    if (e != hipSuccess || n == 0) return e;
+  }
   return with_type(dtype, [&](auto x) {
     using T = decltype(x);
-    hipLaunchKernelGGL((embed_kernel<T>), dim3(wave_blocks(n)), dim3(kThreads), 0, stream,
-                       static_cast<const T *>(table), v, d, table_ld, tokens, n, scale,
-                       static_cast<T *>(out), out_ld, status);
+    const Cover cv = cover<kVec<T>>(d);
+    const uint32_t tiles = div_up(n, kThreads / cv.lanes * kRows), most = kMaxBlocks / cv.slabs;
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((tiles < most ? tiles : most) * cv.slabs), dim3(kThreads), 0, stream,
+                         static_cast<const T *>(table), v, d, table_ld, tokens, n, scale,
+                         static_cast<T *>(out), out_ld, cv.lanes, cv.slabs, status, !one);
+    };
+    if (cv.lanes < kWave) go(embed_kernel<T, false>);
+    else go(embed_kernel<T, true>);
     return hipGetLastError();
   });
 }

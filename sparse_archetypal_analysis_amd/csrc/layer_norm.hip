@@ -5,8 +5,9 @@
 //   g = d_y weight                         d_x = rstd (g - mean(g) - h mean(g h))
 //   d_weight = sum over rows of d_y h      d_bias = sum over rows of d_y
 //
-// All are bound by memory: forward reads x and writes y, the gradient reads
-// d_y and x and writes d_x. A row is read once and stays in registers between
+// All are bound by memory: forward reads x and writes y (16384 x 4096 bf16
+// 49 us, 5.5 TB/s), the gradient reads d_y and x and writes d_x (32768 x 2048
+// bf16 with f32 weights 82 us, 4.9 TB/s). A row is read once and stays in registers between
 // its statistics and its output; the gradient's column sums stay in the
 // registers of the lanes that own the columns, over all rows a block takes.
 #include "token.hpp"
@@ -18,6 +19,37 @@ namespace {
 constexpr uint32_t kThreads = 256;
 constexpr uint32_t kLongThreads = 1024;  // rows that no block can hold
 constexpr uint32_t kMaxBlocks = 1u << 20;
+// Threads of a forward launch at most: two rounds of the card, so that a
+// group's weight and bias serve several rows (60499 x 940 f16 with f32 weights
+// 64 -> 49 us, 131072 x 500 bf16 103 -> 69; 1024 to 4096 blocks within 4 %).
+constexpr uint32_t kFillThreads = 4096 * kThreads;
+
+// A row of d elements over kStride lanes, kR packs of kN each: x[k] holds the
+// elements from (k * kStride + at) * kN, those past the end `fill`. The row's
+// one broken pack has a branch of its own, its elements loaded at clamped
+// places (a branch in each load: 4096 bf16 65 us against 50, 2001 64 against
+// 41).
+template <class T, uint32_t kN, uint32_t kStride, uint32_t kR>
+__device__ __forceinline__ void load_row(const T *row, uint32_t at, uint32_t d, bool live, T fill,
+                                         Pack<T, kN> (&x)[kR]) {
+#pragma unroll
+  for (uint32_t k = 0; k < kR; ++k) {
+    const uint32_t c = (k * kStride + at) * kN;
+    x[k] = fill;
+    if (live && c + kN <= d) x[k] = *reinterpret_cast<const Pack<T, kN> *>(row + c);
+  }
+  const uint32_t last = d / kN;  // the broken pack, if there is one
+  if (d % kN != 0 && live && at == last % kStride) {
+    Pack<T, kN> y;
+#pragma unroll
+    for (uint32_t j = 0; j < kN; ++j) y[j] = row[last * kN + j < d ? last * kN + j : d - 1];
+#pragma unroll
+    for (uint32_t j = 0; j < kN; ++j) y[j] = last * kN + j < d ? y[j] : fill;
+#pragma unroll
+    for (uint32_t k = 0; k < kR; ++k)
+      if (k == last / kStride) x[k] = y;
+  }
+}
 
 // Sums of kN values over the kWaves waves of a row's group in a fixed order,
 // the results in every thread. kWaves > 1: the group is the block; buf holds
@@ -70,14 +102,8 @@ __global__ void __launch_bounds__(kWaves > 1 ? kWaves *kWave : kThreads)
   const uint32_t at = threadIdx.x % kRow;
   const float inv_d = 1.0f / (float)d;
   Pack<W, kV> w[kR], b[kR];
-#pragma unroll
-  for (uint32_t k = 0; k < kR; ++k) {
-    const uint32_t c = (k * kRow + at) * kV;
-    if (weight != nullptr && c < d) w[k] = load_pack_tail<W, kV>(weight, c, d);
-    else w[k] = (W)1.0f;
-    if (bias != nullptr && c < d) b[k] = load_pack_tail<W, kV>(bias, c, d);
-    else b[k] = (W)0.0f;
-  }
+  load_row<W, kV, kRow, kR>(weight, at, d, weight != nullptr, (W)1.0f, w);
+  load_row<W, kV, kRow, kR>(bias, at, d, bias != nullptr, (W)0.0f, b);
   const uint64_t step = (uint64_t)gridDim.x * kGroups;
   // every lane of a wave runs the same rounds: the sums take whole waves
   for (uint64_t i0 = (uint64_t)blockIdx.x * kGroups; i0 < n; i0 += step) {
@@ -85,12 +111,8 @@ __global__ void __launch_bounds__(kWaves > 1 ? kWaves *kWave : kThreads)
     const bool live = i < n;
     const T *row = x + (live ? i : 0) * x_ld;
     Vec<T> v[kR];
+    load_row<T, kV, kRow, kR>(row, at, d, live, (T)0.0f, v);
     float s[1] = {0.0f};
-#pragma unroll
-    for (uint32_t k = 0; k < kR; ++k) {
-      const uint32_t c = (k * kRow + at) * kV;
-      v[k] = live && c < d ? load_vec_tail(row, c, d, (T)0.0f) : Vec<T>{};
-    }
 #pragma unroll
     for (uint32_t k = 0; k < kR; ++k)
 #pragma unroll
@@ -112,7 +134,7 @@ __global__ void __launch_bounds__(kWaves > 1 ? kWaves *kWave : kThreads)
     }
     row_sums<kLanes, kWaves, 2>(q, buf[1]);
     const float shift = q[1] * inv_d;
-    const float var = fmaxf(q[0] * inv_d - shift * shift, 0.0f);
+    const float var = nan_max(q[0] * inv_d - shift * shift, 0.0f);
     mu += shift;
     const float rs = 1.0f / sqrtf(var + eps);
     if (!live) continue;
@@ -124,7 +146,7 @@ __global__ void __launch_bounds__(kWaves > 1 ? kWaves *kWave : kThreads)
 #pragma unroll
       for (uint32_t j = 0; j < kV; ++j)
         y[j] = (T)(((float)v[k][j] - mu) * rs * (float)w[k][j] + (float)b[k][j]);
-      if (c < d) store_vec_tail(to, c, d, y);
+      if (c < d) store_vec_tail<T, true>(to, c, d, y);
     }
     if (at == 0) {
       if (mean != nullptr) mean[i] = mu;
@@ -154,7 +176,7 @@ __global__ void __launch_bounds__(kLongThreads)
       r += t;
     }
     const float shift = block_sum(r, lds) * inv_d;
-    const float var = fmaxf(block_sum(q, lds) * inv_d - shift * shift, 0.0f);
+    const float var = nan_max(block_sum(q, lds) * inv_d - shift * shift, 0.0f);
     mu += shift;
     const float rs = 1.0f / sqrtf(var + eps);
     // out may be x: a thread writes only what it alone reads
@@ -197,12 +219,7 @@ __global__ void __launch_bounds__(kWaves > kGradWaves ? kWaves *kWave : kGradThr
   const float inv_d = 1.0f / (float)d;
   Pack<W, kV> w[kR];
   float sw[kR][kV] = {}, sb[kR][kV] = {};
-#pragma unroll
-  for (uint32_t k = 0; k < kR; ++k) {
-    const uint32_t c = (k * kRow + at) * kV;
-    if (weight != nullptr && c < d) w[k] = load_pack_tail<W, kV>(weight, c, d);
-    else w[k] = (W)1.0f;
-  }
+  load_row<W, kV, kRow, kR>(weight, at, d, weight != nullptr, (W)1.0f, w);
   const uint64_t step = (uint64_t)gridDim.x * kGroups;
   uint32_t round = 0;
   for (uint64_t i0 = (uint64_t)blockIdx.x * kGroups; i0 < n; i0 += step, ++round) {
@@ -210,13 +227,8 @@ __global__ void __launch_bounds__(kWaves > kGradWaves ? kWaves *kWave : kGradThr
     const bool live = i < n;
     const T *row = x + (live ? i : 0) * x_ld, *dy = d_out + (live ? i : 0) * d_out_ld;
     Vec<T> v[kR], g[kR];
-#pragma unroll
-    for (uint32_t k = 0; k < kR; ++k) {
-      const uint32_t c = (k * kRow + at) * kV;
-      const bool in = live && c < d;
-      g[k] = in ? load_vec_tail(dy, c, d, (T)0.0f) : Vec<T>{};
-      v[k] = in ? load_vec_tail(row, c, d, (T)0.0f) : Vec<T>{};
-    }
+    load_row<T, kV, kRow, kR>(dy, at, d, live, (T)0.0f, g);
+    load_row<T, kV, kRow, kR>(row, at, d, live, (T)0.0f, v);
     const float mu = live ? mean[i] : 0.0f, rs = live ? rstd[i] : 0.0f;
     // (columns past the end have d_y = 0 and add nothing to any sum)
     float s[2] = {0.0f, 0.0f};
@@ -263,7 +275,7 @@ __global__ void __launch_bounds__(kWaves > kGradWaves ? kWaves *kWave : kGradThr
         const float h = ((float)v[k][j] - mu) * rs;
         y[j] = (T)(rs * ((float)g[k][j] * (float)w[k][j] - a - h * b));
       }
-      if (c < d) store_vec_tail(to, c, d, y);
+      if (c < d) store_vec_tail<T, true>(to, c, d, y);
     }
   }
   if (part == nullptr && d_weight == nullptr && d_bias == nullptr) return;
@@ -416,15 +428,16 @@ struct Group {
   static constexpr uint32_t holds = kLanes_ * kWaves_ * kR_;  // vectors of 16 bytes
 };
 
-// f(Group) with the smallest group that holds `vecs` vectors: lanes of one
-// wave while they do, then more vectors per lane, then more waves. Forward, a
-// lane holds up to 4 vectors (weight and bias beside them).
+// f(Group) with the smallest group that holds `vecs` vectors: two vectors per
+// lane, then more lanes (a reduction over half the lanes serves twice the
+// rows: 131072 x 500 bf16 69 -> 59 us), then more vectors, then more waves.
+// Forward, a lane holds up to 4 vectors (weight and bias beside them).
 template <class F>
 bool forward_group(uint32_t vecs, F &&f) {
   if (vecs <= 8) f(Group<8, 1, 1>{});
-  else if (vecs <= 16) f(Group<16, 1, 1>{});
-  else if (vecs <= 32) f(Group<32, 1, 1>{});
-  else if (vecs <= 64) f(Group<64, 1, 1>{});
+  else if (vecs <= 16) f(Group<8, 1, 2>{});
+  else if (vecs <= 32) f(Group<16, 1, 2>{});
+  else if (vecs <= 64) f(Group<32, 1, 2>{});
   else if (vecs <= 128) f(Group<64, 1, 2>{});
   else if (vecs <= 256) f(Group<64, 1, 4>{});
   else if (vecs <= 512) f(Group<64, 4, 2>{});
@@ -438,9 +451,9 @@ bool forward_group(uint32_t vecs, F &&f) {
 template <class F>
 bool grad_group(uint32_t vecs, F &&f) {
   if (vecs <= 8) f(Group<8, 1, 1>{});
-  else if (vecs <= 16) f(Group<16, 1, 1>{});
-  else if (vecs <= 32) f(Group<32, 1, 1>{});
-  else if (vecs <= 64) f(Group<64, 1, 1>{});
+  else if (vecs <= 16) f(Group<8, 1, 2>{});
+  else if (vecs <= 32) f(Group<16, 1, 2>{});
+  else if (vecs <= 64) f(Group<32, 1, 2>{});
   else if (vecs <= 128) f(Group<64, 1, 2>{});
   else if (vecs <= 256) f(Group<64, 1, 4>{});
   else if (vecs <= 512) f(Group<64, 2, 4>{});
@@ -451,6 +464,7 @@ bool grad_group(uint32_t vecs, F &&f) {
   return true;
 }
 
+uint32_t least(uint32_t a, uint32_t b) { return a < b ? a : b; }
 uint32_t capped(uint64_t blocks) { return (uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks); }
 
 }  // namespace
@@ -474,7 +488,7 @@ hipError_t launch_layer_norm(const void *x, uint32_t dtype, uint32_t n, uint32_t
         using G = decltype(g);
         constexpr uint32_t threads = G::waves > 1 ? G::waves * kWave : kThreads;
         constexpr uint32_t rows = G::waves > 1 ? 1 : kThreads / G::lanes;
-        launch(layer_norm_kernel<T, W, G::lanes, G::waves, G::vecs>, capped(div_up(n, rows)),
+        launch(layer_norm_kernel<T, W, G::lanes, G::waves, G::vecs>, least(div_up(n, rows), kFillThreads / threads),
                threads);
       });
       if (!held) launch(layer_norm_long_kernel<T, W>, capped(n), kLongThreads);
@@ -484,9 +498,10 @@ hipError_t launch_layer_norm(const void *x, uint32_t dtype, uint32_t n, uint32_t
   });
 }
 
-// Parts: one block per compute unit, each with 8 rows or more where there are
-// that many.
-constexpr uint32_t kMaxParts = 256;
+// Parts: a block of 8 rows or more, up to one per compute unit, or two where a
+// lane holds up to 2 vectors and registers leave room for both (100000 x 130
+// f32 74 -> 52 us; 32768 x 2048 bf16, 4 vectors, 82 -> 90 with two).
+constexpr uint32_t kMaxParts = 512;
 
 NormGradPlan plan_layer_norm_grad(uint32_t n, uint32_t d) {
   NormGradPlan p{};
@@ -518,7 +533,7 @@ hipError_t launch_layer_norm_grad(const NormGradPlan &plan, const void *d_out, u
         constexpr uint32_t waves = G::waves > kGradWaves ? G::waves : kGradWaves;
         constexpr uint32_t rows = waves * kWave / (G::lanes * G::waves);
         const uint32_t all = div_up(n, rows);
-        parts = all < plan.parts ? all : plan.parts;
+        parts = least(all, G::vecs > 2 ? least(plan.parts, kMaxParts / 2) : plan.parts);
         const bool alone = parts == 1;
         hipLaunchKernelGGL((layer_norm_grad_kernel<T, W, G::lanes, G::waves, G::vecs>),
                            dim3(parts), dim3(waves * kWave), 0, stream, dy, d_out_ld, xs, n, d,

@@ -189,6 +189,62 @@ __device__ __forceinline__ float wave_bound_of(const float (&x)[kN], uint32_t k)
   return fmaxf(f32_unorder(at), kLowest);
 }
 
+// A row of v logits over kStride lanes, kR vectors each: x[k] holds the
+// elements from (k * kStride + at) * kVec<T>, -inf past the end. The row's one
+// broken vector has a branch of its own (a branch in each load took up to
+// twice the registers). Many vectors of halves are loaded without a branch,
+// those past the end from the row's beginning, and chosen as whole words: put
+// together from branches, each load was waited for before the next (100k x
+// 2600 bf16 with 5 alternatives 198 us against 156; f32 and fewer vectors lose
+// up to 9 % that way, 1300 f32 107 against 116).
+template <class T, uint32_t kStride, uint32_t kR>
+__device__ __forceinline__ void load_row(const T *row, uint32_t at, uint32_t v, bool live,
+                                         Vec<T> (&x)[kR]) {
+  constexpr uint32_t kV = kVec<T>;
+  constexpr uint32_t kWords = kV * sizeof(T) / 4;
+  typedef uint32_t Words __attribute__((ext_vector_type(kWords), aligned(sizeof(T))));
+  const uint32_t last = v / kV;  // the broken vector, if there is one
+  const bool broken = v % kV != 0 && live && at == last % kStride;
+  if constexpr (sizeof(T) == 2 && kR > 4) {  // (rows this long have a whole vector)
+    Vec<T> none;
+    none = (T)kNegInf;
+    const Words filled = __builtin_bit_cast(Words, none);
+    Words w[kR];
+#pragma unroll
+    for (uint32_t k = 0; k < kR; ++k) {
+      const uint32_t c = (k * kStride + at) * kV;
+      w[k] = *reinterpret_cast<const Words *>(row + (c + kV <= v ? c : 0u));
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < kR; ++k) {
+      const bool in = live && (k * kStride + at) * kV + kV <= v;
+#pragma unroll
+      for (uint32_t j = 0; j < kWords; ++j) w[k][j] = in ? w[k][j] : filled[j];
+    }
+    if (broken) {
+      const Words y = __builtin_bit_cast(Words, load_vec_tail(row, last * kV, v, (T)kNegInf));
+#pragma unroll
+      for (uint32_t k = 0; k < kR; ++k)
+        if (k == last / kStride) w[k] = y;
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < kR; ++k) x[k] = __builtin_bit_cast(Vec<T>, w[k]);
+  } else {
+#pragma unroll
+    for (uint32_t k = 0; k < kR; ++k) {
+      const uint32_t c = (k * kStride + at) * kV;
+      x[k] = (T)kNegInf;
+      if (live && c + kV <= v) x[k] = load_vec(row + c);
+    }
+    if (broken) {
+      const Vec<T> y = load_vec_tail(row, last * kV, v, (T)kNegInf);
+#pragma unroll
+      for (uint32_t k = 0; k < kR; ++k)
+        if (k == last / kStride) x[k] = y;
+    }
+  }
+}
+
 // --- rows that a wave's registers hold ------------------------------------------
 
 // Candidates that a wave orders.
@@ -342,7 +398,7 @@ __global__ void __launch_bounds__(kThreads)
     const bool live = i < n;
     const T *row = logits + (live ? i : 0) * ld;
     Vec<T> x[kR];
-    load_row<T, kLanes, kR>(row, at, v, live, (T)kNegInf, x);
+    load_row<T, kLanes, kR>(row, at, v, live, x);
     Target<T> target(o, live ? i : 0, v);
     target.fetch(o, row);
     Sums a{kNegInf, 0.0f, 0.0f};
@@ -596,7 +652,8 @@ constexpr uint32_t kGradUnroll = 4;  // vectors in flight per lane
 // A row per `lanes` lanes (a power of two), or, few rows, a part of a row per
 // block (grid y). Nothing is exchanged between lanes: an element's gradient
 // needs the row's five numbers and itself, so a lane loads up to 4 vectors,
-// then stores over them (d_logits may be logits). Bound by memory: 8192 x
+// then stores over them (d_logits may be logits; stores that the L2 gives up
+// first gain 2 % here and lose 5 where rows are not aligned). Bound by memory: 8192 x
 // 32768 bf16 204 us (5.3 TB/s; an element per lane and load: 406 us).
 template <class T>
 __global__ void __launch_bounds__(kThreads)

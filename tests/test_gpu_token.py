@@ -286,6 +286,22 @@ def test_layer_norm_of_constant_rows(d):
     within(rstd, np.full(3, want), np.full(3, 4 * R.U * want), "rstd")
 
 
+@pytest.mark.parametrize("d", [5, 64, 700, 5000, 70000])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_layer_norm_of_rows_that_hold_no_numbers(d, dtype):
+    rng = np.random.default_rng(d)
+    x = rows(rng, 4, d, dtype)
+    want = saa.seacells_layer_norm(x)
+    for bad in (float("nan"), INF, -INF):
+        y = x.clone()
+        y[1, d // 2] = bad
+        out, mean, rstd = saa.seacells_layer_norm(y)
+        assert bool(out[1].isnan().all()) and bool(rstd[1].isnan()) and not bool(mean[1].isfinite())
+        keep = [0, 2, 3]
+        for a, b in zip((out, mean, rstd), want):
+            assert torch.equal(a[keep], b[keep])
+
+
 def test_layer_norm_without_rows():
     x, f = torch.empty(0, 9, device="cuda"), torch.empty(0, device="cuda")
     assert saa.seacells_layer_norm(x)[0].shape == (0, 9)
