@@ -923,16 +923,19 @@ TOP_MAX = 64  # SEACELLS_TOP_MAX
 
 
 def _rows(t, name, dev=None):
-    """(tensor as [n, d], row stride) of a row operand."""
-    if t.dim() != 2:
+    """(rows, elements per row, row stride, device) of a row operand."""
+    shape = t.shape
+    if len(shape) != 2:
         try:
-            t = t.view(-1, t.shape[-1])
+            t = t.view(-1, shape[-1])
         except (RuntimeError, IndexError):
             raise SeacellsError("%s: the rows have no common stride" % name) from None
-    if not t.is_cuda or t.dtype not in _DTYPES or (dev is not None and t.get_device() != dev):
+        shape = t.shape
+    at = t.get_device()
+    if at < 0 or t.dtype not in _DTYPES or (dev is not None and at != dev):
         raise SeacellsError("%s must be a float32, float16 or bfloat16 tensor on the call's GPU"
                             % name)
-    n, d = t.shape
+    n, d = shape
     ld, step = t.stride()
     if d > 1 and step != 1:
         raise SeacellsError("%s: a row's elements must be consecutive" % name)
@@ -940,12 +943,14 @@ def _rows(t, name, dev=None):
         ld = d
     elif ld < d:
         raise SeacellsError("%s: rows overlap (stride %d < %d)" % (name, ld, d))
-    return t, ld
+    elif n >= 1 << 31:
+        raise SeacellsError("%s: more than 2^31 - 1 rows" % name)
+    return n, d, ld, at
 
 
 def _out_rows(t, name, n, d, dev, dtype):
-    t2, ld = _rows(t, name, dev)
-    if t2.shape[0] != n or t2.shape[1] != d or t2.dtype != dtype:
+    tn, td, ld, _ = _rows(t, name, dev)
+    if tn != n or td != d or t.dtype != dtype:
         raise SeacellsError("%s must be [%d, %d] of %s" % (name, n, d, dtype))
     return ld
 
@@ -979,15 +984,24 @@ def _workspace(ws, size, dev, stream):
 
 
 def _enqueue(fn, dev, stream, *args):
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if torch.cuda.current_device() == dev:
-        rc = fn(*args, stream.cuda_stream)
+    # torch's own accessors of the stream's handle and the device: the public
+    # ones build objects, 1.2 of a small call's 8.8 us
+    raw = (torch._C._cuda_getCurrentRawStream(dev) if stream is None  # noqa: SLF001
+           else stream.cuda_stream)
+    if torch._C._cuda_getDevice() == dev:  # noqa: SLF001
+        rc = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream.cuda_stream)
+            rc = fn(*args, raw)
     if rc != SEACELLS_OK:
         _check_rc(rc)
+
+
+def _query(fn, n, *sizes):
+    """A workspace query (0 for sizes that no call takes)."""
+    if not 0 <= n < 1 << 31 or any(not 0 <= k < 1 << 31 for k in sizes):
+        return 0
+    return int(fn(n, *sizes))
 
 
 def seacells_embed(table, tokens, scale=1.0, out=None, status=None, stream=None):
@@ -997,22 +1011,21 @@ def seacells_embed(table, tokens, scale=1.0, out=None, status=None, stream=None)
     status).
     """
     lib = load()
-    tab, ld = _rows(table, "table")
-    v, d = tab.shape
-    dev, dt, n = tab.get_device(), tab.dtype, tokens.numel()
+    v, d, ld, dev = _rows(table, "table")
+    dt, n = table.dtype, tokens.numel()
     tok = _vector(tokens, "tokens", n, dev, torch.int32)
     if out is None:
         out = _new((*tokens.shape, d), dt, dev, stream)
     out_ld = _out_rows(out, "out", n, d, dev, dt)
     if status is None:
         status = _new(1, torch.int32, dev, stream)
-    _enqueue(lib.seacells_embed, dev, stream, tab.data_ptr(), _DTYPES[dt], v, d, ld, tok, n, scale,
+    _enqueue(lib.seacells_embed, dev, stream, table.data_ptr(), _DTYPES[dt], v, d, ld, tok, n, scale,
              out.data_ptr(), out_ld, _vector(status, "status", 1, dev, torch.int32))
     return out, status
 
 
 def seacells_embed_grad_workspace(n, v, d) -> int:
-    return int(load().seacells_embed_grad_workspace(n, v, d))
+    return _query(load().seacells_embed_grad_workspace, n, v, d)
 
 
 def seacells_embed_grad(tokens, d_out, v: int, scale=1.0, add_to=None, d_table=None,
@@ -1024,9 +1037,8 @@ def seacells_embed_grad(tokens, d_out, v: int, scale=1.0, add_to=None, d_table=N
     d_out's). add_to (same type and strides) may be d_table itself.
     """
     lib = load()
-    dy, dy_ld = _rows(d_out, "d_out")
-    n, d = dy.shape
-    dev, dt = dy.get_device(), dy.dtype
+    n, d, dy_ld, dev = _rows(d_out, "d_out")
+    dt = d_out.dtype
     tok = _vector(tokens, "tokens", n, dev, torch.int32)
     if d_table is None:
         d_table = _new((v, d), dt if add_to is None else add_to.dtype, dev, stream)
@@ -1043,7 +1055,7 @@ def seacells_embed_grad(tokens, d_out, v: int, scale=1.0, add_to=None, d_table=N
         status = _new(1, torch.int32, dev, stream)
     ws, ws_bytes, keep = _workspace(workspace, lib.seacells_embed_grad_workspace(n, v, d), dev,
                                     stream)
-    _enqueue(lib.seacells_embed_grad, dev, stream, tok, n, dy.data_ptr(), _DTYPES[dt], dy_ld, v, d,
+    _enqueue(lib.seacells_embed_grad, dev, stream, tok, n, d_out.data_ptr(), _DTYPES[dt], dy_ld, v, d,
              scale, add, d_table.data_ptr(), _DTYPES[ot], t_ld, ws, ws_bytes,
              _vector(status, "status", 1, dev, torch.int32))
     return d_table, status
@@ -1057,9 +1069,8 @@ def seacells_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, mean=None
     weight and bias [d] share a type: x's or float32. out may be x.
     """
     lib = load()
-    xr, ld = _rows(x, "x")
-    n, d = xr.shape
-    dev, dt = xr.get_device(), xr.dtype
+    n, d, ld, dev = _rows(x, "x")
+    dt = x.dtype
     wt = weight.dtype if weight is not None else bias.dtype if bias is not None else dt
     if wt != dt and wt != torch.float32:
         raise SeacellsError("weight and bias must be of x's type or float32")
@@ -1072,7 +1083,7 @@ def seacells_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, mean=None
         mean = _new(x.shape[:-1], torch.float32, dev, stream)
     if rstd is None:
         rstd = _new(x.shape[:-1], torch.float32, dev, stream)
-    _enqueue(lib.seacells_layer_norm, dev, stream, xr.data_ptr(), _DTYPES[dt], n, d, ld, w, b,
+    _enqueue(lib.seacells_layer_norm, dev, stream, x.data_ptr(), _DTYPES[dt], n, d, ld, w, b,
              _DTYPES[wt], eps, out.data_ptr(), out_ld,
              _vector(mean, "mean", n, dev, torch.float32),
              _vector(rstd, "rstd", n, dev, torch.float32))
@@ -1080,7 +1091,7 @@ def seacells_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, mean=None
 
 
 def seacells_layer_norm_grad_workspace(n, d) -> int:
-    return int(load().seacells_layer_norm_grad_workspace(n, d))
+    return _query(load().seacells_layer_norm_grad_workspace, n, d)
 
 
 def seacells_layer_norm_grad(d_out, x, mean, rstd, weight=None, d_x=None, d_weight=None,
@@ -1092,11 +1103,10 @@ def seacells_layer_norm_grad(d_out, x, mean, rstd, weight=None, d_x=None, d_weig
     (returned as None).
     """
     lib = load()
-    xr, ld = _rows(x, "x")
-    n, d = xr.shape
-    dev, dt = xr.get_device(), xr.dtype
-    dy, dy_ld = _rows(d_out, "d_out", dev)
-    if dy.shape != xr.shape or dy.dtype != dt:
+    n, d, ld, dev = _rows(x, "x")
+    dt = x.dtype
+    dy_n, dy_d, dy_ld, _ = _rows(d_out, "d_out", dev)
+    if dy_n != n or dy_d != d or d_out.dtype != dt:
         raise SeacellsError("d_out must have x's shape and type")
     wt = weight.dtype if weight is not None else dt
     if wt != dt and wt != torch.float32:
@@ -1114,7 +1124,7 @@ def seacells_layer_norm_grad(d_out, x, mean, rstd, weight=None, d_x=None, d_weig
     d_bias = None if d_bias is False else _new(d, wt, dev, stream) if d_bias is None else d_bias
     ws, ws_bytes, keep = _workspace(workspace, lib.seacells_layer_norm_grad_workspace(n, d), dev,
                                     stream)
-    _enqueue(lib.seacells_layer_norm_grad, dev, stream, dy.data_ptr(), dy_ld, xr.data_ptr(),
+    _enqueue(lib.seacells_layer_norm_grad, dev, stream, d_out.data_ptr(), dy_ld, x.data_ptr(),
              _DTYPES[dt], n, d, ld, _vector(mean, "mean", n, dev, torch.float32),
              _vector(rstd, "rstd", n, dev, torch.float32), w, _DTYPES[wt],
              None if d_x is None else d_x.data_ptr(), dx_ld,
@@ -1124,7 +1134,7 @@ def seacells_layer_norm_grad(d_out, x, mean, rstd, weight=None, d_x=None, d_weig
 
 
 def seacells_logprobs_workspace(n, v, top_k=0) -> int:
-    return int(load().seacells_logprobs_workspace(n, v, top_k))
+    return _query(load().seacells_logprobs_workspace, n, v, top_k)
 
 
 def seacells_logprobs(logits, targets=None, top_k=0, logp=None, entropy=None, stats=None,
@@ -1138,9 +1148,8 @@ def seacells_logprobs(logits, targets=None, top_k=0, logp=None, entropy=None, st
     top_k] (None for top_k = 0). targets int32, negative: ignored (logp 0).
     """
     lib = load()
-    x, ld = _rows(logits, "logits")
-    n, v = x.shape
-    dev, lead = x.get_device(), logits.shape[:-1]
+    n, v, ld, dev = _rows(logits, "logits")
+    lead = logits.shape[:-1]
     tgt = _vector(targets, "targets", n, dev, torch.int32)
     if not 0 <= top_k <= TOP_MAX:
         raise SeacellsError("top_k must be 0 to %d" % TOP_MAX)
@@ -1163,7 +1172,7 @@ def seacells_logprobs(logits, targets=None, top_k=0, logp=None, entropy=None, st
         status = _new(1, torch.int32, dev, stream)
     ws, ws_bytes, keep = _workspace(workspace, lib.seacells_logprobs_workspace(n, v, top_k), dev,
                                     stream)
-    _enqueue(lib.seacells_logprobs, dev, stream, x.data_ptr(), _DTYPES[x.dtype], n, v, ld, tgt,
+    _enqueue(lib.seacells_logprobs, dev, stream, logits.data_ptr(), _DTYPES[logits.dtype], n, v, ld, tgt,
              top_k, _vector(logp, "logp", n, dev, torch.float32),
              _vector(entropy, "entropy", n, dev, torch.float32),
              _vector(stats, "stats", 2 * n, dev, torch.float32),
@@ -1182,9 +1191,8 @@ def seacells_logprobs_grad(logits, targets, stats, entropy=None, d_logp=None, d_
     d_entropy); targets may be None (no part of d_logp).
     """
     lib = load()
-    x, ld = _rows(logits, "logits")
-    n, v = x.shape
-    dev, dt = x.get_device(), x.dtype
+    n, v, ld, dev = _rows(logits, "logits")
+    dt = logits.dtype
     if d_logits is None:
         d_logits = _new(logits.shape, dt, dev, stream)
     d_ld = _out_rows(d_logits, "d_logits", n, v, dev, dt)
@@ -1192,7 +1200,7 @@ def seacells_logprobs_grad(logits, targets, stats, entropy=None, d_logp=None, d_
         raise SeacellsError("d_entropy needs the entropies")
     if status is None:
         status = _new(1, torch.int32, dev, stream)
-    _enqueue(lib.seacells_logprobs_grad, dev, stream, x.data_ptr(), _DTYPES[dt], n, v, ld,
+    _enqueue(lib.seacells_logprobs_grad, dev, stream, logits.data_ptr(), _DTYPES[dt], n, v, ld,
              _vector(targets, "targets", n, dev, torch.int32),
              _vector(stats, "stats", 2 * n, dev, torch.float32),
              _vector(entropy, "entropy", n, dev, torch.float32),

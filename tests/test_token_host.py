@@ -106,6 +106,8 @@ def test_workspace_queries_of_impossible_sizes_are_zero():
     assert saa.seacells_layer_norm_grad_workspace(4, 0) == 0
     assert saa.seacells_logprobs_workspace(4, 0, 0) == 0
     assert saa.seacells_logprobs_workspace(4, 8, 65) == 0
+    assert saa.seacells_embed_grad_workspace(2 ** 32 + 4, 8, 8) == 0
+    assert saa.seacells_layer_norm_grad_workspace(-1, 8) == 0
 
 
 def test_binding_refuses_host_tensors_and_wrong_layouts():
