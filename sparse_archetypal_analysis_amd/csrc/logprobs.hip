@@ -412,26 +412,34 @@ __global__ void __launch_bounds__(kThreads)
     if constexpr (kWhole) {
       if (live) wave_top<T, kR>(o, i, v, x, mine, r, room[group]);
     } else {
-      // one alternative per round
+      // one alternative per round, kept by the lane of its place until all
+      // lanes have one, which they write side by side (131072 x 60 f32 with 8:
+      // written one by one 37 us, so 35; x 250 bf16 with 16, the elements held as
+      // f32 and by the rule below 174 and 125)
+      uint64_t kept = 0;
+      float y[kV];
+#pragma unroll
+      for (uint32_t j = 0; j < kV; ++j) y[j] = (float)x[0][j];
       for (uint32_t q = 0; q < o.top_k; ++q) {
         float best = kNegInf;
 #pragma unroll
-        for (uint32_t j = 0; j < kV; ++j) best = fmaxf(best, (float)x[0][j]);
+        for (uint32_t j = 0; j < kV; ++j) best = fmaxf(best, y[j]);
         best = r.none ? kNegInf : group_max<kLanes>(best);
+        const uint32_t turn = q % kLanes;
         if (__ballot(best > kNegInf) == 0) {  // nothing left in any of the rows
-          for (uint32_t p = q + at; p < o.top_k; p += kLanes)
-            if (live) write_top(o, i, p, 0ull, r);
+          for (uint32_t p = q - turn + at; p < o.top_k; p += kLanes)
+            if (live) write_top(o, i, p, p < q ? kept : 0ull, r);
           break;
         }
         uint32_t c = 0xffffffffu;
 #pragma unroll
-        for (uint32_t j = kV; j-- > 0;)
-          if ((float)x[0][j] == best) c = at * kV + j;
+        for (uint32_t j = kV; j-- > 0;) c = y[j] == best ? at * kV + j : c;
         c = group_min_u32<kLanes>(c);
 #pragma unroll
-        for (uint32_t j = 0; j < kV; ++j)
-          if (at * kV + j == c) x[0][j] = (T)kNegInf;
-        if (live && at == 0) write_top(o, i, q, best > kNegInf ? top_key(best, c) : 0ull, r);
+        for (uint32_t j = 0; j < kV; ++j) y[j] = at * kV + j == c ? kNegInf : y[j];
+        if (at == turn) kept = best > kNegInf ? top_key(best, c) : 0ull;
+        if (turn + 1 == kLanes || q + 1 == o.top_k)
+          if (live && at <= turn) write_top(o, i, q - turn + at, kept, r);
       }
     }
   }
@@ -722,13 +730,15 @@ struct Group {
   static constexpr uint32_t lanes = kLanes_, vecs = kR_;
 };
 
-// Rows of more than 8 lanes that are asked for many alternatives get a wave
-// (a round per alternative would cost more than the lanes left idle).
+// Rows of a few lanes that are asked for many alternatives get a wave: a round
+// per alternative for all rows of the wave would cost more than one row at a
+// time (60000 x 125 f32 with 12: 44 us both ways, with 8 34 against 42, with 32
+// 95 against 63; 60 columns: equal at 48; 30: 30 us against 62 with 64).
 template <class F>
 bool held_group(uint32_t vecs, uint32_t top_k, F &&f) {
   if (vecs <= 8) f(Group<8, 1>{});
-  else if (vecs <= 16) f(Group<16, 1>{});
-  else if (vecs <= 32 && top_k <= 16) f(Group<32, 1>{});
+  else if (vecs <= 16 && top_k <= 48) f(Group<16, 1>{});
+  else if (vecs <= 32 && top_k <= 12) f(Group<32, 1>{});
   else if (vecs <= 64) f(Group<64, 1>{});
   else if (vecs <= 128) f(Group<64, 2>{});
   else if (vecs <= 192) f(Group<64, 3>{});
