@@ -417,13 +417,16 @@ __global__ void __launch_bounds__(kThreads)
       // written one by one 37 us, so 35; x 250 bf16 with 16, the elements held as
       // f32 and by the rule below 174 and 125)
       uint64_t kept = 0;
-      float y[kV];
+      constexpr uint32_t kE = kR * kV;
+      float y[kE];
 #pragma unroll
-      for (uint32_t j = 0; j < kV; ++j) y[j] = (float)x[0][j];
+      for (uint32_t e = 0; e < kE; ++e) y[e] = (float)x[e / kV][e % kV];
+      uint32_t first = at * kV;        // the lane's first column
+      asm volatile("" : "+v"(first));  // (not one register per element's)
       for (uint32_t q = 0; q < o.top_k; ++q) {
         float best = kNegInf;
 #pragma unroll
-        for (uint32_t j = 0; j < kV; ++j) best = fmaxf(best, y[j]);
+        for (uint32_t e = 0; e < kE; ++e) best = fmaxf(best, y[e]);
         best = r.none ? kNegInf : group_max<kLanes>(best);
         const uint32_t turn = q % kLanes;
         if (__ballot(best > kNegInf) == 0) {  // nothing left in any of the rows
@@ -431,12 +434,17 @@ __global__ void __launch_bounds__(kThreads)
             if (live) write_top(o, i, p, p < q ? kept : 0ull, r);
           break;
         }
+        // the lowest column that holds it, as an offset from the lane's first
         uint32_t c = 0xffffffffu;
 #pragma unroll
-        for (uint32_t j = kV; j-- > 0;) c = y[j] == best ? at * kV + j : c;
-        c = group_min_u32<kLanes>(c);
+        for (uint32_t e = kE; e-- > 0;)
+          c = y[e] == best ? e / kV * kLanes * kV + e % kV : c;
+        const uint32_t mine = c;
+        c = group_min_u32<kLanes>(c != 0xffffffffu ? first + c : c);
+        const uint32_t gone = first + mine == c ? mine : 0xffffffffu;
 #pragma unroll
-        for (uint32_t j = 0; j < kV; ++j) y[j] = at * kV + j == c ? kNegInf : y[j];
+        for (uint32_t e = 0; e < kE; ++e)
+          y[e] = gone == e / kV * kLanes * kV + e % kV ? kNegInf : y[e];
         if (at == turn) kept = best > kNegInf ? top_key(best, c) : 0ull;
         if (turn + 1 == kLanes || q + 1 == o.top_k)
           if (live && at <= turn) write_top(o, i, q - turn + at, kept, r);
@@ -725,28 +733,69 @@ __global__ void __launch_bounds__(kThreads)
 
 uint32_t capped(uint64_t blocks) { return (uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks); }
 
-// f(lanes, vectors per lane) for rows that a wave's registers hold.
+// How a row that a wave's registers hold is spread over lanes.
 template <uint32_t kLanes_, uint32_t kR_>
 struct Group {
   static constexpr uint32_t lanes = kLanes_, vecs = kR_;
 };
 
-// Rows of a few lanes that are asked for many alternatives get a wave: a round
-// per alternative for all rows of the wave would cost more than one row at a
-// time (60000 x 125 f32 with 12: 44 us both ways, with 8 34 against 42, with 32
-// 95 against 63; 60 columns: equal at 48; 30: 30 us against 62 with 64).
-template <class F>
-bool held_group(uint32_t vecs, uint32_t top_k, F &&f) {
-  if (vecs <= 8) f(Group<8, 1>{});
-  else if (vecs <= 16 && top_k <= 48) f(Group<16, 1>{});
-  else if (vecs <= 32 && top_k <= 12) f(Group<32, 1>{});
-  else if (vecs <= 64) f(Group<64, 1>{});
-  else if (vecs <= 128) f(Group<64, 2>{});
-  else if (vecs <= 192) f(Group<64, 3>{});
-  else if (vecs <= 256) f(Group<64, 4>{});
-  else if (vecs <= 384) f(Group<64, 6>{});
-  else if (vecs <= 512) f(Group<64, 8>{});
-  else return false;
+constexpr uint32_t kFewRows = 4096;  // four per SIMD
+
+// f(Group) for rows of `vecs` vectors of kV logits, false where a wave's
+// registers do not hold them. Rows this short are bound by the instructions of
+// a wave, so the group with the fewest per row is taken, counted roughly: 10
+// per element and 150 for the sums and the outputs of all rows of the wave;
+// per alternative a round over the elements (few lanes), or a search and the
+// candidates' order (a wave). 60000 rows, a wave per row against what is taken:
+// 200 f32 26 and 15 us, with 8 alternatives 43 and 36, with 16 a wave; 500 bf16
+// 36 and 25, with 4 50 and 43; 1000 bf16 41 and 32, with 1 51 and 42. Few rows
+// leave units idle, and get a wave each (rows of up to 8 vectors 8 lanes).
+template <uint32_t kV, class F>
+bool held_group(uint32_t n, uint32_t vecs, uint32_t top_k, F &&f) {
+  if (vecs > 512) return false;
+  const uint32_t wide = vecs <= 64 ? 1 : vecs <= 128 ? 2 : vecs <= 192 ? 3 : vecs <= 256 ? 4
+                      : vecs <= 384 ? 6 : 8;
+  uint32_t least = 10 * kV * wide + 150 + (top_k != 0 ? 120 + 6 * top_k : 0u);
+  uint32_t lanes = kWave, per = wide;
+  if (n <= kFewRows) {
+    if (vecs <= 8) lanes = 8;
+  } else {
+    for (uint32_t l = 8; l < kWave; l *= 2)
+      for (uint32_t r = 1; r <= 4; r *= 2) {
+        const uint32_t e = kV * r;
+        const uint32_t cost = (10 * e + 150 + top_k * (5 * e + 40)) * l / kWave;
+        if (l * r >= vecs && cost < least) {
+          least = cost;
+          lanes = l;
+          per = r;
+        }
+      }
+  }
+  if (lanes == 8) {
+    if (per == 1) f(Group<8, 1>{});
+    else if (per == 2) f(Group<8, 2>{});
+    else f(Group<8, 4>{});
+  } else if (lanes == 16) {
+    if (per == 1) f(Group<16, 1>{});
+    else if (per == 2) f(Group<16, 2>{});
+    else f(Group<16, 4>{});
+  } else if (lanes == 32) {
+    if (per == 1) f(Group<32, 1>{});
+    else if (per == 2) f(Group<32, 2>{});
+    else f(Group<32, 4>{});
+  } else if (per == 1) {
+    f(Group<64, 1>{});
+  } else if (per == 2) {
+    f(Group<64, 2>{});
+  } else if (per == 3) {
+    f(Group<64, 3>{});
+  } else if (per == 4) {
+    f(Group<64, 4>{});
+  } else if (per == 6) {
+    f(Group<64, 6>{});
+  } else {
+    f(Group<64, 8>{});
+  }
   return true;
 }
 
@@ -788,7 +837,7 @@ hipError_t launch_logprobs(const LogprobsPlan &plan, const void *logits, uint32_
   return with_type(dtype, [&](auto t) {
     using T = decltype(t);
     const T *x = static_cast<const T *>(logits);
-    const bool held = held_group(div_up(v, kVec<T>), top_k, [&](auto g) {
+    const bool held = held_group<kVec<T>>(n, div_up(v, kVec<T>), top_k, [&](auto g) {
       using G = decltype(g);
       hipLaunchKernelGGL((logprobs_held_kernel<T, G::lanes, G::vecs>),
                          dim3(capped(div_up(n, kThreads / G::lanes))), dim3(kThreads), 0, stream, x,

@@ -248,6 +248,19 @@ def test_layer_norm(n, d, dtype, w_dtype):
         assert torch.equal(x, out)
 
 
+@pytest.mark.parametrize("dtype,w_dtype", [("f32", "f32"), ("bf16", "f32")])
+@pytest.mark.parametrize("n,d", [(140001, 9), (20001, 301), (5001, 1500), (1501, 8201)])
+def test_layer_norm_of_more_rows_than_a_launch_holds(n, d, dtype, w_dtype):
+    rng = np.random.default_rng(n + d)
+    x = norm_input(rng, n, d, dtype, gap=1)
+    w, b = (rows(rng, 1, d, w_dtype)[0] for _ in range(2))
+    eps = float(np.float32(1e-5))
+    got = saa.seacells_layer_norm(x, w, b, eps)
+    want, bound = R.layer_norm(exact(x), exact(w), exact(b), eps, dtype)
+    for nm, g, y, e in zip(("out", "mean", "rstd"), got, want, bound):
+        within(g, y, e, nm)
+
+
 @pytest.mark.parametrize("dtype,w_dtype", [("f32", "f32"), ("bf16", "f32"), ("f16", "f16"),
                                            ("bf16", None)])
 @pytest.mark.parametrize("n,d", NORM_SIZES + [(5000, 40), (3001, 333)])
@@ -376,6 +389,21 @@ def test_logprobs(n, v, k, dtype, masks):
     lp2, H2, stats2, idx2, val2, _ = saa.seacells_logprobs(x, tgt, k)
     assert lp is None and torch.equal(H, H2) and torch.equal(stats, stats2)
     assert k == 0 or (torch.equal(idx, idx2) and torch.equal(val, val2))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("v,k", [(3, 2), (30, 40), (33, 0), (60, 3), (61, 30), (125, 5), (130, 0),
+                                 (200, 4), (255, 9), (257, 2), (500, 1), (501, 3), (900, 1),
+                                 (1001, 0)])
+def test_logprobs_of_many_short_rows(v, k, dtype):
+    """More rows than get a wave each: every spread of a row over lanes."""
+    rng = np.random.default_rng(v + k)
+    n, (gap, start) = 4103, ((0, 0) if v % 2 == 0 else (5, 1))
+    x = logit_rows(rng, n, v, dtype, True, gap=gap, start=start)
+    x[5, v // 2] = float("nan")
+    x[6] = 1.0  # all equal
+    x[7, : v // 2] = -INF
+    check_logprobs(x, classes(rng, n, v), k)
 
 
 @pytest.mark.parametrize("v", [6, 64, 1300, 20000, 131072])
