@@ -75,6 +75,14 @@ __device__ __forceinline__ void row_sums(float (&x)[kN], float *buf) {
   }
 }
 
+// A sum's mean, rounded to f32: the residuals' sum corrects exactly this number,
+// so the product may not be fused into what takes or adds it (the mean was off
+// by up to a whole step then).
+__device__ __forceinline__ float mean_of(float sum, float inv_d) {
+#pragma clang fp contract(off)
+  return sum * inv_d;
+}
+
 // Sum over the block in a fixed order, the result in every thread.
 __device__ __forceinline__ float block_sum(float x, float *lds) {
   x = group_sum<kWave>(x);
@@ -118,7 +126,7 @@ __global__ void __launch_bounds__(kWaves > 1 ? kWaves *kWave : kThreads)
 #pragma unroll
       for (uint32_t j = 0; j < kV; ++j) s[0] += (float)v[k][j];
     row_sums<kLanes, kWaves, 1>(s, buf[0]);
-    float mu = s[0] * inv_d;
+    float mu = mean_of(s[0], inv_d);
     // the residuals' sum takes out the rounding of the first one
     float q[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(kLongThreads)
     const T *row = x + i * x_ld;
     float s = 0.0f;
     for (uint32_t c = threadIdx.x; c < d; c += kLongThreads) s += (float)row[c];
-    float mu = block_sum(s, lds) * inv_d;
+    float mu = mean_of(block_sum(s, lds), inv_d);
     float q = 0.0f, r = 0.0f;
     for (uint32_t c = threadIdx.x; c < d; c += kLongThreads) {
       const float t = (float)row[c] - mu;
