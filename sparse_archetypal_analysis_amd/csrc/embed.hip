@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(kThreads)
 // the sum of the places where its pieces begin in their chunks: no block waits
 // for another, and no atomic's order shows. (A block per bucket that reads all
 // tokens costs buckets x n: 79 us for 131072 tokens and 262144 rows against 26
-// in two launches; up to kDirect of them it saves the chunks' launch.)
+// in two launches; up to kDirect of them it saves the chunks' launch: 3500
+// tokens and 20000 ids of 64 columns 20.8 us against 25.8.)
 
 typedef int32_t Four __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -120,7 +121,7 @@ constexpr uint32_t kMaxBuckets = 1024;
 constexpr uint32_t kSortThreads = 512;
 constexpr uint32_t kSortWaves = kSortThreads / kWave;
 constexpr uint32_t kSortIds = 512;    // ids ordered at once, a thread each
-constexpr uint32_t kDirect = 2048;
+constexpr uint32_t kDirect = 4096;
 constexpr uint32_t kSortUnroll = 4;   // of a wave's loads
 constexpr uint32_t kSortBlocks = 128;
 
@@ -228,10 +229,11 @@ __global__ void __launch_bounds__(kChunkThreads)
 }
 
 // Orders a bucket's tokens by id. They come from the chunks (cuts) or, few of
-// them, from the tokens themselves (cuts == nullptr). Each wave takes an equal
-// run of them, in the order of their positions, counts it by counters of its
-// own and then places it: cursors follow the order (id, wave). A bucket of one
-// id is in order as it comes, and several blocks (grid y) may share it.
+// them (kFew), from the tokens themselves. Each wave takes an equal run of
+// them, in the order of their positions, counts it by counters of its own and
+// then places it: cursors follow the order (id, wave). A bucket of one id is in
+// order as it comes, and several blocks (grid y) may share it.
+template <bool kFew>
 __global__ void __launch_bounds__(kSortThreads)
     token_sort_kernel(const int32_t *__restrict__ tokens, uint32_t n, uint32_t v, uint32_t shift,
                       uint32_t buckets, const uint32_t *__restrict__ cuts, uint32_t chunks,
@@ -263,52 +265,87 @@ __global__ void __launch_bounds__(kSortThreads)
     return all;
   };
 
+  // a batch of the wave's tokens: id, position, and whether there is one
+  uint32_t id[kSortUnroll], pos[kSortUnroll];
+  bool has[kSortUnroll];
+  constexpr uint32_t kBatch = kWave * kSortUnroll;
+  auto read_tokens = [&](uint32_t i, uint32_t i1) {
+#pragma unroll
+    for (uint32_t u = 0; u < kSortUnroll; ++u) {
+      pos[u] = i + u * kWave + lane;
+      id[u] = pos[u] < i1 ? (uint32_t)tokens[pos[u]] : ~0u;
+      has[u] = id[u] - lo < mine;  // (a negative token is no id below 2^31)
+    }
+  };
+  // the bucket's tokens from e on, of those before e1, in the chunks from c0
+  // on, before which there are `done`
+  auto read_chunks = [&](uint32_t e, uint32_t e1, uint32_t c0, uint32_t done) {
+#pragma unroll
+    for (uint32_t u = 0; u < kSortUnroll; ++u) {
+      const uint32_t q = e + u * kWave + lane;
+      const uint32_t r = (q < e1 ? q : e) - done;
+      uint32_t c = 0;  // the last chunk that begins at or before it
+#pragma unroll
+      for (uint32_t half = kSortThreads / 2; half >= 1; half /= 2)
+        c = first[c + half] <= r ? c + half : c;
+      const uint64_t from = (uint64_t)(c0 + c) * chunk_len + begin[c] + (r - first[c]);
+      has[u] = q < e1;
+      id[u] = entry_id[from];
+      pos[u] = entry_pos[from];
+    }
+  };
+
   uint32_t base = 0, have = 0;  // where the bucket begins in perm, and its tokens
   bool bad = false;
   uint32_t below = 0;
-  if (cuts == nullptr) {
+  if constexpr (kFew) {
     for (uint32_t i = threadIdx.x; i < n; i += kSortThreads) {
-      const int32_t t = tokens[i];  // (a negative one is no id below 2^31)
+      const int32_t t = tokens[i];
       bad |= t >= (int32_t)v;
       below += (uint32_t)t < lo ? 1u : 0u;
     }
   } else {
-    for (uint32_t c = threadIdx.x; c < chunks; c += kSortThreads) {
-      const uint32_t *cut = cuts + (uint64_t)c * (buckets + 2);
-      below += cut[bucket];
-      have += cut[bucket + 1] - cut[bucket];
-      if (bucket == 0) bad |= cut[buckets + 1] != 0;
+    for (uint32_t c0 = 0; c0 < chunks; c0 += kSortThreads) {
+      have += load_cuts(c0);
+      if (c0 + threadIdx.x < chunks) {
+        below += begin[threadIdx.x];
+        if (bucket == 0)
+          bad |= cuts[(uint64_t)(c0 + threadIdx.x) * (buckets + 2) + buckets + 1] != 0;
+      }
     }
-    uint32_t all;
-    block_prefix<kSortWaves>(have, lds, &all);
-    have = all;
-    load_cuts(0);
+    if (chunks > kSortThreads) load_cuts(0);
   }
   block_prefix<kSortWaves>(below, lds, &base);
   const bool any_bad = __syncthreads_or(bad);
   if (bucket == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = any_bad ? kFlagBadIndex : 0u;
 
+  const uint32_t part = blockIdx.y * kSortWaves + wave, parts = gridDim.y * kSortWaves;
+  const uint32_t w0 = (uint32_t)((uint64_t)have * part / parts);
+  const uint32_t w1 = (uint32_t)((uint64_t)have * (part + 1) / parts);
+  // a run of one batch from the chunks stays in registers (28509 tokens 29.6 us
+  // against 31.1; of tokens read directly it cost 1.3 at 200)
+  const bool once = !kFew && chunks <= kSortThreads && w0 < w1 && w1 - w0 <= kBatch;
+  if (once) read_chunks(w0, w1, 0, 0);
+
   // f(has, id, position, place among the bucket's tokens (from chunks)) for
   // the wave's tokens in order, a wave's worth at a time
   auto every = [&](auto f) {
-    if (cuts == nullptr) {
+    auto each = [&](uint32_t e) {
+#pragma unroll
+      for (uint32_t u = 0; u < kSortUnroll; ++u) f(has[u], id[u], pos[u], e + u * kWave + lane);
+    };
+    if (once) {
+      each(w0);
+      return;
+    }
+    if constexpr (kFew) {
       const uint32_t i0 = n * wave / kSortWaves, i1 = n * (wave + 1) / kSortWaves;
-      for (uint32_t i = i0; i < i1; i += kWave * kSortUnroll) {
-        uint32_t id[kSortUnroll];
-#pragma unroll
-        for (uint32_t u = 0; u < kSortUnroll; ++u) {
-          const uint32_t q = i + u * kWave + lane;
-          id[u] = q < i1 ? (uint32_t)tokens[q] : ~0u;
-        }
-#pragma unroll
-        for (uint32_t u = 0; u < kSortUnroll; ++u)
-          f(id[u] - lo < mine, id[u], i + u * kWave + lane, 0u);
+      for (uint32_t i = i0; i < i1; i += kBatch) {
+        read_tokens(i, i1);
+        each(0);
       }
       return;
     }
-    const uint32_t part = blockIdx.y * kSortWaves + wave, parts = gridDim.y * kSortWaves;
-    const uint32_t w0 = (uint32_t)((uint64_t)have * part / parts);
-    const uint32_t w1 = (uint32_t)((uint64_t)have * (part + 1) / parts);
     uint32_t done = 0;
     for (uint32_t c0 = 0; c0 < chunks; c0 += kSortThreads) {
       uint32_t end = have;
@@ -317,31 +354,15 @@ __global__ void __launch_bounds__(kSortThreads)
         end = done + load_cuts(c0);
       }
       const uint32_t e0 = max(w0, done), e1 = min(w1, end);
-      for (uint32_t e = e0; e < e1; e += kWave * kSortUnroll) {
-        uint32_t id[kSortUnroll], pos[kSortUnroll];
-#pragma unroll
-        for (uint32_t u = 0; u < kSortUnroll; ++u) {
-          const uint32_t q = e + u * kWave + lane;
-          const uint32_t r = (q < e1 ? q : e) - done;
-          uint32_t c = 0;  // the last chunk that begins at or before it
-#pragma unroll
-          for (uint32_t half = kSortThreads / 2; half >= 1; half /= 2)
-            c = first[c + half] <= r ? c + half : c;
-          const uint64_t from = (uint64_t)(c0 + c) * chunk_len + begin[c] + (r - first[c]);
-          id[u] = entry_id[from];
-          pos[u] = entry_pos[from];
-        }
-#pragma unroll
-        for (uint32_t u = 0; u < kSortUnroll; ++u) {
-          const uint32_t q = e + u * kWave + lane;
-          f(q < e1, id[u], pos[u], q);
-        }
+      for (uint32_t e = e0; e < e1; e += kBatch) {
+        read_chunks(e, e1, c0, done);
+        each(e);
       }
       done = end;
     }
   };
 
-  if (shift == 0 && cuts != nullptr) {
+  if (shift == 0 && !kFew) {
     if (threadIdx.x == 0 && blockIdx.y == 0) {
       start[lo] = base;
       if (lo + 1 == v) start[v] = base + have;
@@ -796,10 +817,14 @@ hipError_t launch_embed_grad(const EmbedGradPlan &plan, const int32_t *tokens, u
   // 93 us, shared 6)
   const uint32_t share =
       plan.shift == 0 && plan.chunks != 0 ? div_up(kSortBlocks, plan.buckets) : 1u;
-  hipLaunchKernelGGL(token_sort_kernel, dim3(plan.buckets, share), dim3(kSortThreads),
-                     kSortWaves * at_once * sizeof(uint32_t), stream, tokens, n, v, plan.shift,
-                     plan.buckets, plan.chunks != 0 ? cuts : nullptr, plan.chunks,
-                     plan.per * kChunkThreads, entry_id, entry_pos, perm, sorted, start, status);
+  auto sort = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(plan.buckets, share), dim3(kSortThreads),
+                       kSortWaves * at_once * sizeof(uint32_t), stream, tokens, n, v, plan.shift,
+                       plan.buckets, cuts, plan.chunks, plan.per * kChunkThreads, entry_id,
+                       entry_pos, perm, sorted, start, status);
+  };
+  if (plan.chunks != 0) sort(token_sort_kernel<false>);
+  else sort(token_sort_kernel<true>);
   const hipError_t sorting = hipGetLastError();
   if (sorting != hipSuccess) return sorting;
   return with_type(d_out_type, [&](auto x) {

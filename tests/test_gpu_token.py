@@ -163,6 +163,21 @@ def test_embed_grad_of_many_tokens_and_ids(n, v, d, dtype):
     assert flags(saa.seacells_embed_grad(tok, d_out, v, d_table=out)[1]) == ["BAD_INDEX"]
 
 
+@pytest.mark.parametrize("n", [4095, 4096, 4097, 131071, 131500])
+@pytest.mark.parametrize("v,d", [(1, 9), (31, 3), (3000, 17), (70001, 2)])
+def test_embed_grad_around_the_steps_of_its_sort(n, v, d):
+    """The last direct size and the first by chunks; runs of one batch per wave
+    and longer ones; a bucket that holds nearly all the tokens."""
+    rng = np.random.default_rng(3 * n + v)
+    tok, d_out = ids(rng, n, v), rows(rng, n, d, "f32")
+    tok[rng.permutation(n)[:n - n // 8]] = v // 2
+    got, st = saa.seacells_embed_grad(tok, d_out, v)
+    assert flags(st) == []
+    want, bound = R.embed_grad(exact(tok), exact(d_out), v, 1.0, None, "f32")
+    within(got, want, bound, "d_table")
+    assert torch.equal(saa.seacells_embed_grad(tok, d_out, v)[0], got)
+
+
 @pytest.mark.parametrize("n,v,d", [(5000, 600, 33), (9000, 3, 130), (70000, 40, 3)])
 def test_embed_grad_is_the_same_every_time(n, v, d):
     rng = np.random.default_rng(1)
