@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 hipError_t launch_embed(const void *table, uint32_t dtype, uint32_t v, uint32_t d, uint64_t table_ld,
                         const int32_t *tokens, uint32_t n, float scale, void *out, uint64_t out_ld,
                         uint32_t *status, hipStream_t stream) {
-  const bool one = n > 0 && n <= kIdsOfOneBlock;
+  const bool one = one_block_reports(n, d, dtype_size(dtype));
   if (!one) {
     const hipError_t e = launch_status_clear(status, stream);
     if (e != hipSuccess || n == 0) return e;

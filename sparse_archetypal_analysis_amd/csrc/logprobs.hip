@@ -452,8 +452,8 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   // after the rows: the other blocks' work hides it
-  if (blockIdx.x == 0 && o.targets != nullptr && !o.check)
-    report_ids<kThreads>(o.targets, n, v, o.status);
+  if (blockIdx.x == 0 && !o.check)
+    report_ids<kThreads>(o.targets, o.targets != nullptr ? n : 0u, v, o.status);
 }
 
 // --- rows that are streamed -------------------------------------------------------
@@ -622,8 +622,8 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   // after the rows: the other blocks' work hides it
-  if (blockIdx.x == 0 && part == 0 && o.targets != nullptr && !o.check)
-    report_ids<kThreads>(o.targets, n, v, o.status);
+  if (blockIdx.x == 0 && part == 0 && !o.check)
+    report_ids<kThreads>(o.targets, o.targets != nullptr ? n : 0u, v, o.status);
 }
 
 // The parts of a row, one per lane, in one wave: their sums joined, their
@@ -727,8 +727,8 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   // after the rows: the other blocks' work hides it
-  if (blockIdx.x == 0 && blockIdx.y == 0 && !check && targets != nullptr)
-    report_ids<kThreads>(targets, n, v, status);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && !check)
+    report_ids<kThreads>(targets, targets != nullptr ? n : 0u, v, status);
 }
 
 uint32_t capped(uint64_t blocks) { return (uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks); }
@@ -826,9 +826,8 @@ hipError_t launch_logprobs(const LogprobsPlan &plan, const void *logits, uint32_
                            uint32_t v, uint64_t ld, const int32_t *targets, uint32_t top_k,
                            float *logp, float *entropy, float *stats, int32_t *top_idx,
                            float *top_logp, void *ws, uint32_t *status, hipStream_t stream) {
-  // a block looks at all targets where it can; else (and without targets) the
-  // status is cleared first
-  const bool one = targets != nullptr && n > 0 && n <= kIdsOfOneBlock;
+  // one block looks at all targets, or the status is cleared first
+  const bool one = one_block_reports(targets != nullptr ? n : n != 0, v, dtype_size(dtype));
   if (!one) {
     const hipError_t e = launch_status_clear(status, stream);
     if (e != hipSuccess || n == 0) return e;
@@ -862,7 +861,7 @@ hipError_t launch_logprobs_grad(const void *logits, uint32_t dtype, uint32_t n, 
                                 const float *entropy, const float *d_logp, const float *d_entropy,
                                 void *d_logits, uint64_t d_logits_ld, uint32_t *status,
                                 hipStream_t stream) {
-  const bool one = targets != nullptr && n > 0 && n <= kIdsOfOneBlock;
+  const bool one = one_block_reports(targets != nullptr ? n : n != 0, v, dtype_size(dtype));
   if (!one) {
     const hipError_t e = launch_status_clear(status, stream);
     if (e != hipSuccess || n == 0) return e;

@@ -489,6 +489,40 @@ def test_logprobs_flags_classes_beyond_the_row():
     assert flags(saa.seacells_logprobs(x, tgt, 0, status=st)[5]) == []
 
 
+@pytest.mark.parametrize("n,d", [(5, 3), (32768, 2), (32769, 2), (33001, 151), (40003, 299),
+                                 (33000, 300), (33003, 8200)])
+@pytest.mark.parametrize("at", [0, 1, -2, -1])
+def test_status_of_every_launch_that_reports_it(n, d, at):
+    """Few and many ids, narrow and wide rows (one block looks over the ids, or
+    the rows' lanes do), a wrong id at either end, statuses that an earlier
+    call left set."""
+    if d == 8200 and at not in (1, -1):
+        pytest.skip("one end is enough for the large rows")
+    x = torch.zeros(n, d, dtype=torch.bfloat16, device="cuda")
+    tok = torch.zeros(n, dtype=torch.int32, device="cuda")
+    bad = tok.clone()
+    bad[at] = d
+    table = torch.ones(d, d, dtype=torch.bfloat16, device="cuda")
+    st = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    for t in (tok, bad, tok):
+        want = ["BAD_INDEX"] if t is bad else []
+        if d < 8200:
+            assert flags(saa.seacells_embed(table, t, status=st)[1]) == want
+        _, H, stats = saa.seacells_logprobs(x, t, 0, status=st)[:3]
+        assert flags(st) == want
+        one = torch.ones(n, device="cuda")
+        assert flags(saa.seacells_logprobs_grad(x, t, stats, d_logp=one, status=st)[1]) == want
+    for t in (bad, None):  # set, then cleared without targets
+        st.fill_(-1)
+        stats = saa.seacells_logprobs(x, t, 0, status=st)[2]
+        assert flags(st) == (["BAD_INDEX"] if t is bad else [])
+        st.fill_(-1)
+        one = torch.ones(n, device="cuda")
+        saa.seacells_logprobs_grad(x, t, stats, d_logp=one if t is not None else None,
+                                   entropy=H, d_entropy=one, status=st)
+        assert flags(st) == (["BAD_INDEX"] if t is bad else [])
+
+
 def test_logprobs_of_no_rows():
     x = torch.empty(0, 9, device="cuda")
     none = torch.empty(0, dtype=torch.int32, device="cuda")
