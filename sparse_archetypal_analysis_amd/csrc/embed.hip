@@ -116,7 +116,7 @@ typedef int32_t Four __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr uint32_t kChunkThreads = 256;
 constexpr uint32_t kChunkWaves = kChunkThreads / kWave;
-constexpr uint32_t kMaxBuckets = 1024;
+constexpr uint32_t kMaxBuckets = 1024;  // with that of the frequent id
 
 constexpr uint32_t kSortThreads = 512;
 constexpr uint32_t kSortWaves = kSortThreads / kWave;
@@ -149,14 +149,45 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t x, uint32_t *lds, uint
   return before + incl - x;
 }
 
+// The id that most lanes hold in t (a wave takes 64 tokens at even distances),
+// kNoId if none is there kOften times. A bucket with such an id (padding, a frequent
+// word) would keep its one block busy long after the others, so the id has a
+// bucket of its own, after the ids' own, that several blocks share: 50000 tokens
+// of one id of 100000, 100 columns, 111 us without and 34 with it, 131072 of
+// 20000 ids, 4 columns, 233 and 30, with frequencies as 1 / rank 47 and 42, all
+// even 28.9 and 30.1. Fewer tokens than kOwnFrom do without.
+constexpr uint32_t kNoId = 0xffffffffu;
+constexpr uint32_t kOften = 4;
+constexpr uint32_t kOwnFrom = 16384;
+
+__device__ __forceinline__ uint32_t frequent_id(int32_t t, uint32_t v) {
+  const bool has = t >= 0 && t < (int32_t)v;
+  uint64_t same = __ballot(has);
+  for (uint32_t bit = 1; bit != 0 && bit < v; bit <<= 1) {
+    const uint64_t set = __ballot(((uint32_t)t & bit) != 0);
+    same &= ((uint32_t)t & bit) != 0 ? set : ~set;
+  }
+  const uint32_t times = has ? (uint32_t)__popcll(same) : 0u;
+  uint64_t more = __ballot(times >= kOften);
+  uint32_t id = kNoId;
+  while (more != 0) {
+    const uint32_t from = (uint32_t)__builtin_ctzll(more);
+    id = readlane_u32((uint32_t)t, from);
+    more = __ballot(times > readlane_u32(times, from));
+  }
+  return id;
+}
+
 // A chunk of kPer * 256 tokens, ordered by bucket: entry_id, entry_pos, and
-// cuts[chunk][k] = the first place of bucket k in the chunk, then the tokens
-// kept, then whether an id was v or more.
+// cuts[chunk][k] = the first place of bucket k in the chunk, the last bucket
+// that of the frequent id (if `own`), then the tokens kept, then whether an id
+// was v or more.
 template <uint32_t kPer>
 __global__ void __launch_bounds__(kChunkThreads)
     token_chunk_kernel(const int32_t *__restrict__ tokens, uint32_t n, uint32_t v, uint32_t shift,
-                       uint32_t buckets, uint32_t *__restrict__ entry_id,
-                       uint32_t *__restrict__ entry_pos, uint32_t *__restrict__ cuts) {
+                       uint32_t buckets, bool own, uint32_t *__restrict__ entry_id,
+                       uint32_t *__restrict__ entry_pos, uint32_t *__restrict__ cuts,
+                       uint32_t *__restrict__ frequent) {
   __shared__ uint32_t cnt[kChunkWaves][kMaxBuckets];
   __shared__ uint32_t part[kChunkWaves];
   const uint32_t lane = lane_id(), wave = threadIdx.x / kWave;
@@ -167,9 +198,15 @@ __global__ void __launch_bounds__(kChunkThreads)
 #pragma unroll
   for (uint32_t u = 0; u < kPer; ++u)
     t[u] = first + u * kWave < n ? tokens[first + u * kWave] : -1;
+  const int32_t sample = own ? tokens[(uint64_t)lane * n / kWave] : -1;
   for (uint32_t i = threadIdx.x; i < kMaxBuckets; i += kChunkThreads)
 #pragma unroll
     for (uint32_t w = 0; w < kChunkWaves; ++w) cnt[w][i] = 0u;
+  const uint32_t often = own ? frequent_id(sample, v) : kNoId;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *frequent = often;
+  auto bucket_of = [&](int32_t id) {
+    return (uint32_t)id == often ? buckets : (uint32_t)id >> shift;
+  };
   __syncthreads();
 
   uint32_t place[kPer];
@@ -178,9 +215,9 @@ __global__ void __launch_bounds__(kChunkThreads)
   for (uint32_t u = 0; u < kPer; ++u) {
     bad |= t[u] >= (int32_t)v;
     const bool has = t[u] >= 0 && t[u] < (int32_t)v;
-    const uint32_t k = has ? (uint32_t)t[u] >> shift : 0u;
+    const uint32_t k = has ? bucket_of(t[u]) : 0u;
     uint64_t same = __ballot(has);  // the lanes with this one's bucket
-    for (uint32_t bit = 1; bit < buckets; bit <<= 1) {
+    for (uint32_t bit = 1; bit <= buckets; bit <<= 1) {
       const uint64_t set = __ballot((k & bit) != 0);
       same &= (k & bit) != 0 ? set : ~set;
     }
@@ -203,11 +240,11 @@ __global__ void __launch_bounds__(kChunkThreads)
       sum += c[m][w];
     }
   uint32_t at = block_prefix<kChunkWaves>(sum, part, &total);
-  uint32_t *row = cuts + (uint64_t)blockIdx.x * (buckets + 2);
+  uint32_t *row = cuts + (uint64_t)blockIdx.x * (buckets + 3);
 #pragma unroll
   for (uint32_t m = 0; m < kMine; ++m) {
     const uint32_t k = threadIdx.x * kMine + m;
-    if (k < buckets) row[k] = at;
+    if (k <= buckets) row[k] = at;
 #pragma unroll
     for (uint32_t w = 0; w < kChunkWaves; ++w) {
       cnt[w][k] = at;
@@ -215,14 +252,14 @@ __global__ void __launch_bounds__(kChunkThreads)
     }
   }
   if (threadIdx.x == 0) {
-    row[buckets] = total;
-    row[buckets + 1] = any_bad ? 1u : 0u;
+    row[buckets + 1] = total;
+    row[buckets + 2] = any_bad ? 1u : 0u;
   }
   __syncthreads();
 #pragma unroll
   for (uint32_t u = 0; u < kPer; ++u) {
     if (t[u] < 0 || t[u] >= (int32_t)v) continue;
-    const uint64_t to = chunk + cnt[wave][(uint32_t)t[u] >> shift] + place[u];
+    const uint64_t to = chunk + cnt[wave][bucket_of(t[u])] + place[u];
     entry_id[to] = (uint32_t)t[u];
     entry_pos[to] = (uint32_t)(first + u * kWave);
   }
@@ -232,13 +269,16 @@ __global__ void __launch_bounds__(kChunkThreads)
 // them (kFew), from the tokens themselves. Each wave takes an equal run of
 // them, in the order of their positions, counts it by counters of its own and
 // then places it: cursors follow the order (id, wave). A bucket of one id is in
-// order as it comes, and several blocks (grid y) may share it.
+// order as it comes, and several blocks (grid y) may share it. The blocks from
+// `buckets` on share the frequent id's tokens: these stand among its bucket's,
+// after those of the ids before it, which they count first.
 template <bool kFew>
 __global__ void __launch_bounds__(kSortThreads)
     token_sort_kernel(const int32_t *__restrict__ tokens, uint32_t n, uint32_t v, uint32_t shift,
                       uint32_t buckets, const uint32_t *__restrict__ cuts, uint32_t chunks,
                       uint32_t chunk_len, const uint32_t *__restrict__ entry_id,
-                      const uint32_t *__restrict__ entry_pos, uint32_t *__restrict__ perm,
+                      const uint32_t *__restrict__ entry_pos,
+                      const uint32_t *__restrict__ frequent, uint32_t *__restrict__ perm,
                       uint32_t *__restrict__ sorted, uint32_t *__restrict__ start,
                       uint32_t *__restrict__ status) {
   extern __shared__ uint32_t counts[];  // [kSortWaves][ids at once]
@@ -246,7 +286,12 @@ __global__ void __launch_bounds__(kSortThreads)
   __shared__ uint32_t lds[kSortWaves];
   const uint32_t lane = lane_id(), wave = threadIdx.x / kWave;
   const uint64_t lower = (1ull << lane) - 1ull;
-  const uint32_t bucket = blockIdx.x;
+  uint32_t bucket = blockIdx.x;
+  const bool sharing = !kFew && blockIdx.x >= buckets;
+  if (sharing) {
+    if (*frequent == kNoId) return;
+    bucket = *frequent >> shift;
+  }
   const uint32_t lo = bucket << shift;
   const uint32_t mine = min(1u << shift, v - lo);
   const uint32_t at_once = min(1u << shift, kSortIds);
@@ -255,7 +300,7 @@ __global__ void __launch_bounds__(kSortThreads)
   // its tokens the chunks before hold; returns the tokens in all of them
   auto load_cuts = [&](uint32_t c0) {
     const uint32_t c = c0 + threadIdx.x;
-    const uint32_t *cut = cuts + (uint64_t)(c < chunks ? c : 0u) * (buckets + 2) + bucket;
+    const uint32_t *cut = cuts + (uint64_t)(c < chunks ? c : 0u) * (buckets + 3) + bucket;
     const uint32_t e0 = cut[0], e1 = c < chunks ? cut[1] : e0;
     uint32_t all;
     const uint32_t before = block_prefix<kSortWaves>(e1 - e0, lds, &all);
@@ -297,7 +342,7 @@ __global__ void __launch_bounds__(kSortThreads)
 
   uint32_t base = 0, have = 0;  // where the bucket begins in perm, and its tokens
   bool bad = false;
-  uint32_t below = 0;
+  uint32_t below = 0, of_often = 0;
   if constexpr (kFew) {
     for (uint32_t i = threadIdx.x; i < n; i += kSortThreads) {
       const int32_t t = tokens[i];
@@ -308,23 +353,38 @@ __global__ void __launch_bounds__(kSortThreads)
     for (uint32_t c0 = 0; c0 < chunks; c0 += kSortThreads) {
       have += load_cuts(c0);
       if (c0 + threadIdx.x < chunks) {
+        const uint32_t *last = cuts + (uint64_t)(c0 + threadIdx.x) * (buckets + 3) + buckets;
         below += begin[threadIdx.x];
-        if (bucket == 0)
-          bad |= cuts[(uint64_t)(c0 + threadIdx.x) * (buckets + 2) + buckets + 1] != 0;
+        of_often += last[1] - last[0];
+        bad |= last[2] != 0;
       }
     }
     if (chunks > kSortThreads) load_cuts(0);
   }
   block_prefix<kSortWaves>(below, lds, &base);
   const bool any_bad = __syncthreads_or(bad);
-  if (bucket == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = any_bad ? kFlagBadIndex : 0u;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = any_bad ? kFlagBadIndex : 0u;
 
-  const uint32_t part = blockIdx.y * kSortWaves + wave, parts = gridDim.y * kSortWaves;
-  const uint32_t w0 = (uint32_t)((uint64_t)have * part / parts);
-  const uint32_t w1 = (uint32_t)((uint64_t)have * (part + 1) / parts);
+  // the frequent id's tokens, where they stand in this bucket or before
+  const uint32_t often = kFew ? kNoId : *frequent;
+  if (often != kNoId && bucket >= often >> shift) {
+    uint32_t all;
+    block_prefix<kSortWaves>(of_often, lds, &all);
+    of_often = all;
+    if (bucket > often >> shift) base += all;
+  }
+
+  uint32_t w0, w1;  // the wave's run
+  auto share = [&](uint32_t part, uint32_t parts) {
+    part = part * kSortWaves + wave;
+    parts *= kSortWaves;
+    w0 = (uint32_t)((uint64_t)have * part / parts);
+    w1 = (uint32_t)((uint64_t)have * (part + 1) / parts);
+  };
+  share(blockIdx.y, gridDim.y);
   // a run of one batch from the chunks stays in registers (28509 tokens 29.6 us
   // against 31.1; of tokens read directly it cost 1.3 at 200)
-  const bool once = !kFew && chunks <= kSortThreads && w0 < w1 && w1 - w0 <= kBatch;
+  bool once = !kFew && chunks <= kSortThreads && w0 < w1 && w1 - w0 <= kBatch;
   if (once) read_chunks(w0, w1, 0, 0);
 
   // f(has, id, position, place among the bucket's tokens (from chunks)) for
@@ -376,6 +436,25 @@ __global__ void __launch_bounds__(kSortThreads)
     return;
   }
 
+  if (!kFew && sharing) {
+    uint32_t x = 0, before;
+    every([&](bool has, uint32_t id, uint32_t, uint32_t) { x += has && id < often ? 1u : 0u; });
+    block_prefix<kSortWaves>(x, lds, &before);
+    base += before;
+    bucket = buckets;
+    have = of_often;
+    once = false;
+    share(blockIdx.x - buckets, gridDim.x - buckets);
+    if (chunks <= kSortThreads) load_cuts(0);
+    every([&](bool has, uint32_t, uint32_t pos, uint32_t at) {
+      if (has) {
+        perm[base + at] = pos;
+        sorted[base + at] = often;
+      }
+    });
+    return;
+  }
+
   uint32_t *cnt = counts + wave * at_once;
   for (uint32_t s0 = 0; s0 < mine; s0 += at_once) {
     const uint32_t ids = min(at_once, mine - s0), from = lo + s0;
@@ -400,6 +479,8 @@ __global__ void __launch_bounds__(kSortThreads)
     if (threadIdx.x < ids) {
 #pragma unroll
       for (uint32_t w = 0; w < kSortWaves; ++w) total += counts[w * at_once + threadIdx.x];
+      // (the blocks that share them place them)
+      if (from + threadIdx.x == often) total = of_often;
     }
     uint32_t at = base + block_prefix<kSortWaves>(total, lds, &sum);
     if (threadIdx.x < ids) {
@@ -764,7 +845,8 @@ EmbedGradPlan plan_embed_grad(uint32_t n, uint32_t v, uint32_t d) {
   // buckets for every compute unit where the ids allow it, and no more than
   // the chunks' counters
   while ((2u << p.shift) <= v / 256u && (1u << p.shift) < kSortIds) ++p.shift;
-  while (((uint64_t)kMaxBuckets << p.shift) < v) ++p.shift;
+  p.own = n >= kOwnFrom && p.shift != 0;
+  while (((uint64_t)(kMaxBuckets - (p.own ? 1u : 0u)) << p.shift) < v) ++p.shift;
   p.buckets = (uint32_t)(((uint64_t)v + (1u << p.shift) - 1) >> p.shift);
   p.per = n <= 32768 ? 1 : n <= 262144 ? 2 : 4;  // chunks grow with the tokens
   p.chunks = n <= kDirect ? 0 : div_up(n, p.per * kChunkThreads);
@@ -783,7 +865,8 @@ EmbedGradPlan plan_embed_grad(uint32_t n, uint32_t v, uint32_t d) {
   p.off_open = take(2 * (size_t)windows);
   p.off_entry_id = take(p.chunks != 0 ? n : 0);
   p.off_entry_pos = take(p.chunks != 0 ? n : 0);
-  p.off_cuts = take((size_t)p.chunks * (p.buckets + 2));
+  p.off_cuts = take((size_t)p.chunks * (p.buckets + 3));
+  p.off_frequent = take(p.chunks != 0 ? 1 : 0);
   p.off_part = take((size_t)windows * 2 * d);
   p.ws_bytes = at;
   return p;
@@ -798,13 +881,15 @@ hipError_t launch_embed_grad(const EmbedGradPlan &plan, const int32_t *tokens, u
   auto words = [&](size_t off) { return reinterpret_cast<uint32_t *>(base + off); };
   uint32_t *perm = words(plan.off_perm), *sorted = words(plan.off_sorted);
   uint32_t *start = words(plan.off_start), *cuts = words(plan.off_cuts);
+  uint32_t *frequent = words(plan.off_frequent);
   uint32_t *entry_id = words(plan.off_entry_id), *entry_pos = words(plan.off_entry_pos);
   Open *open = reinterpret_cast<Open *>(base + plan.off_open);
   float *part = reinterpret_cast<float *>(base + plan.off_part);
   if (plan.chunks != 0) {
     auto cut = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3(plan.chunks), dim3(kChunkThreads), 0, stream, tokens, n, v,
-                         plan.shift, plan.buckets, entry_id, entry_pos, cuts);
+                         plan.shift, plan.buckets, plan.own, entry_id, entry_pos, cuts,
+                         frequent);
     };
     if (plan.per == 1) cut(token_chunk_kernel<1>);
     else if (plan.per == 2) cut(token_chunk_kernel<2>);
@@ -817,11 +902,13 @@ hipError_t launch_embed_grad(const EmbedGradPlan &plan, const int32_t *tokens, u
   // 93 us, shared 6)
   const uint32_t share =
       plan.shift == 0 && plan.chunks != 0 ? div_up(kSortBlocks, plan.buckets) : 1u;
+  // a batch for each wave of the blocks that share the frequent id
+  const uint32_t helpers = plan.own ? min(kSortBlocks, div_up(n, 2048)) : 0u;
   auto sort = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(plan.buckets, share), dim3(kSortThreads),
+    hipLaunchKernelGGL(kernel, dim3(plan.buckets + helpers, share), dim3(kSortThreads),
                        kSortWaves * at_once * sizeof(uint32_t), stream, tokens, n, v, plan.shift,
                        plan.buckets, cuts, plan.chunks, plan.per * kChunkThreads, entry_id,
-                       entry_pos, perm, sorted, start, status);
+                       entry_pos, frequent, perm, sorted, start, status);
   };
   if (plan.chunks != 0) sort(token_sort_kernel<false>);
   else sort(token_sort_kernel<true>);

@@ -222,7 +222,9 @@ struct EmbedGradPlan {
   uint32_t buckets;
   uint32_t per;      // tokens of a chunk per thread
   uint32_t chunks;   // 0: the buckets read the tokens themselves
-  size_t off_perm, off_sorted, off_start, off_open, off_entry_id, off_entry_pos, off_cuts, off_part;
+  bool own;          // a frequent id has a bucket of its own
+  size_t off_perm, off_sorted, off_start, off_open, off_entry_id, off_entry_pos, off_cuts, off_part,
+      off_frequent;
   size_t ws_bytes;
 };
 EmbedGradPlan plan_embed_grad(uint32_t n, uint32_t v, uint32_t d);

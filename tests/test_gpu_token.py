@@ -163,6 +163,34 @@ def test_embed_grad_of_many_tokens_and_ids(n, v, d, dtype):
     assert flags(saa.seacells_embed_grad(tok, d_out, v, d_table=out)[1]) == ["BAD_INDEX"]
 
 
+@pytest.mark.parametrize("n,v", [(16383, 3000), (16384, 3000), (20001, 512), (50000, 262144),
+                                 (50000, 261889), (300001, 40000), (600001, 700)])
+@pytest.mark.parametrize("often", ["first", "second", "last", "middle", "two", "none", "all"])
+def test_embed_grad_of_frequent_ids(n, v, often):
+    """Ids that many tokens share, at the ends of the table and of the buckets
+    that the sort forms, beside other ids and without any."""
+    rng = np.random.default_rng(n + v)
+    t = rng.integers(-1, v, n)
+    id = {"first": 0, "second": 1, "last": v - 1}.get(often, v // 2)
+    if often == "all":
+        t[:] = id
+    elif often != "none":
+        t[rng.random(n) < 0.4] = id
+        t[rng.random(n) < 0.05] = max(id - 1, 0)
+        t[rng.random(n) < 0.05] = min(id + 1, v - 1)
+    if often == "two":
+        t[rng.random(n) < 0.4] = id // 2
+    tok = torch.from_numpy(t.astype(np.int32)).cuda()
+    d_out = rows(rng, n, 2, "f32")
+    got, st = saa.seacells_embed_grad(tok, d_out, v)
+    assert flags(st) == []
+    want, bound = R.embed_grad(exact(tok), exact(d_out), v, 1.0, None, "f32")
+    within(got, want, bound, "d_table")
+    assert torch.equal(saa.seacells_embed_grad(tok, d_out, v)[0], got)
+    tok[-1] = v
+    assert flags(saa.seacells_embed_grad(tok, d_out, v)[1]) == ["BAD_INDEX"]
+
+
 @pytest.mark.parametrize("n", [4095, 4096, 4097, 131071, 131500])
 @pytest.mark.parametrize("v,d", [(1, 9), (31, 3), (3000, 17), (70001, 2)])
 def test_embed_grad_around_the_steps_of_its_sort(n, v, d):
