@@ -622,7 +622,7 @@ __device__ __forceinline__ void fill_rows(const uint32_t *__restrict__ start, ui
 //
 // The blocks after windows * slabs write the rows without a token, whose
 // stores fill the time that the sums' loads take (32768 x 1024 bf16 into 65536
-// f32 rows: 69 us for 332 MB, 4.8 TB/s; in a launch of their own 30 + 42).
+// f32 rows: 67 us for 332 MB, 5 TB/s; in a launch of their own 30 + 42).
 template <class T, class O, bool kWhole>
 __global__ void __launch_bounds__(kSumThreads)
     embed_grad_sum_kernel(const uint32_t *__restrict__ perm, const uint32_t *__restrict__ sorted,
