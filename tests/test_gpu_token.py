@@ -163,6 +163,35 @@ def test_embed_grad_of_many_tokens_and_ids(n, v, d, dtype):
     assert flags(saa.seacells_embed_grad(tok, d_out, v, d_table=out)[1]) == ["BAD_INDEX"]
 
 
+@pytest.mark.parametrize("n", [1, 2, 63, 255, 256, 257])
+@pytest.mark.parametrize("v,d", [(1, 3), (15, 1031), (16, 8), (17, 2049), (900, 64), (5001, 20),
+                                 (262144, 1), (4200000, 1)])
+@pytest.mark.parametrize("spread", ["even", "one", "two", "beside"])
+def test_embed_grad_of_few_tokens(n, v, d, spread):
+    """The sizes that take one launch and the first that do not; tokens spread,
+    on one id, on two, on neighbouring ids; with and without add_to, in place."""
+    rng = np.random.default_rng(n + v + d)
+    t = {"even": rng.integers(-1, v, n), "one": np.full(n, v - 1),
+         "two": np.where(rng.random(n) < 0.5, 0, v // 2),
+         "beside": np.arange(n) % min(v, 96)}[spread]
+    tok = torch.from_numpy(t.astype(np.int32)).cuda()
+    d_out = rows(rng, n, d, "bf16", gap=1, start=1)
+    base, out = blank(v, d, "f32", gap=2, start=3)
+    before = rows(rng, v, d, "f32", gap=2)
+    for add in (None, before):
+        _, st = saa.seacells_embed_grad(tok, d_out, v, 0.5, add_to=add, d_table=out)
+        assert flags(st) == []
+        want, bound = R.embed_grad(exact(tok), exact(d_out), v, 0.5,
+                                   None if add is None else exact(add), "f32")
+        within(out, want, bound, "d_table")
+        untouched(base, out)
+    again = out.clone()
+    saa.seacells_embed_grad(tok, d_out, v, 0.5, add_to=before, d_table=before)
+    assert torch.equal(before, again)
+    tok[n // 2] = v
+    assert flags(saa.seacells_embed_grad(tok, d_out, v, d_table=out)[1]) == ["BAD_INDEX"]
+
+
 @pytest.mark.parametrize("n,v", [(16383, 3000), (16384, 3000), (20001, 512), (50000, 262144),
                                  (50000, 261889), (300001, 40000), (600001, 700)])
 @pytest.mark.parametrize("often", ["first", "second", "last", "middle", "two", "none", "all"])
