@@ -3,7 +3,8 @@
  *
  * Nothing here is needed to run the Frank-Wolfe updates. These entry points
  * exist so that tests can (a) pin the A update's plan to one kernel and
- * compare kernels bit for bit, and (b) exercise the check the B argmin's
+ * compare kernels bit for bit, (b) see the plan of a table gradient's token
+ * sort, and (c) exercise the check the B argmin's
  * reduce stage makes on its partials: the source page (bixverse-rs 0.6.4,
  * seacells_kernels.rs, the `B_ARGMIN_WG_TIERS` doc and
  * `reduce_argmin_blocks`) warns that a reduce which trusts its partials
@@ -89,6 +90,29 @@ uint32_t seacells_debug_b_last_epoch(void);
 int seacells_debug_b_reduce(uint32_t n, uint32_t k, uint32_t aat_nnz, uint32_t epoch,
                             float *out_val, uint32_t *out_idx, float *gap, void *workspace,
                             size_t workspace_bytes, uint32_t *status, seacells_stream_t stream);
+
+/*
+ * How seacells_embed_grad sorts n tokens of a table of v rows and d columns.
+ * Buckets of 2^shift ids, in order, hold all v of them. Chunks of chunk_len
+ * tokens (chunks = 0: few tokens, no chunks) are ordered by bucket with
+ * `counters` counters: one per bucket and one for the frequent id, which has a
+ * bucket of its own after them where `frequent` is 1. A chunk leaves
+ * buckets + 3 u32 at byte cuts_offset of the workspace (a chunk after the
+ * other): the place where each bucket begins, where the frequent id's begins
+ * (without one the count of tokens), the count of tokens, and whether an id
+ * was v or more.
+ */
+typedef struct seacells_embed_plan {
+    uint32_t shift;
+    uint32_t buckets;
+    uint32_t counters;
+    uint32_t chunks;
+    uint32_t chunk_len;
+    uint32_t frequent;
+    uint64_t cuts_offset;
+} seacells_embed_plan;
+
+int seacells_debug_embed_plan(uint32_t n, uint32_t v, uint32_t d, seacells_embed_plan *out);
 
 #ifdef __cplusplus
 }

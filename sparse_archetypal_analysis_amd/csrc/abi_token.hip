@@ -3,6 +3,7 @@
 // before any HIP call, so they also work on a machine without a GPU.
 #include <cmath>
 
+#include "seacells_debug.h"
 #include "seacells_token.h"
 #include "token.hpp"
 
@@ -188,6 +189,21 @@ int seacells_logprobs_grad(const void *logits, uint32_t dtype, uint32_t n, uint3
   return done(launch_logprobs_grad(logits, dtype, n, v, ld, targets, stats, entropy, d_logp,
                                    d_entropy, d_logits, d_logits_ld, status, hip_stream(stream)),
               "logprobs_grad launch");
+}
+
+int seacells_debug_embed_plan(uint32_t n, uint32_t v, uint32_t d, seacells_embed_plan *out) {
+  if (out == nullptr) return SEACELLS_E_NULL;
+  if (v == 0 || d == 0) return SEACELLS_E_SHAPE;
+  if (n >= kTooLarge || v >= kTooLarge || d > kMaxWidth) return SEACELLS_E_TOO_LARGE;
+  const EmbedGradPlan p = plan_embed_grad(n, v, d);
+  out->shift = p.shift;
+  out->buckets = p.buckets;
+  out->counters = p.counters;
+  out->chunks = p.chunks;
+  out->chunk_len = p.chunk_len;
+  out->frequent = p.own ? 1u : 0u;
+  out->cuts_offset = p.off_cuts;
+  return SEACELLS_OK;
 }
 
 }  // extern "C"

@@ -116,7 +116,7 @@ typedef int32_t Four __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr uint32_t kChunkThreads = 256;
 constexpr uint32_t kChunkWaves = kChunkThreads / kWave;
-constexpr uint32_t kMaxBuckets = 1024;  // with that of the frequent id
+constexpr uint32_t kMaxBuckets = 1024;  // with that of the frequent id (there or not)
 
 constexpr uint32_t kSortThreads = 512;
 constexpr uint32_t kSortWaves = kSortThreads / kWave;
@@ -180,8 +180,8 @@ __device__ __forceinline__ uint32_t frequent_id(int32_t t, uint32_t v) {
 
 // A chunk of kPer * 256 tokens, ordered by bucket: entry_id, entry_pos, and
 // cuts[chunk][k] = the first place of bucket k in the chunk, the last bucket
-// that of the frequent id (if `own`), then the tokens kept, then whether an id
-// was v or more.
+// that of the frequent id (if `own`, else empty: buckets < kMaxBuckets, so a
+// thread writes it), then the tokens kept, then whether an id was v or more.
 template <uint32_t kPer>
 __global__ void __launch_bounds__(kChunkThreads)
     token_chunk_kernel(const int32_t *__restrict__ tokens, uint32_t n, uint32_t v, uint32_t shift,
@@ -1006,14 +1006,17 @@ hipError_t launch_embed(const void *table, uint32_t dtype, uint32_t v, uint32_t 
 
 EmbedGradPlan plan_embed_grad(uint32_t n, uint32_t v, uint32_t d) {
   EmbedGradPlan p{};
-  // buckets for every compute unit where the ids allow it, and no more than
-  // the chunks' counters
+  // buckets for every compute unit where the ids allow it, and fewer than the
+  // chunks' counters: the cut after the last bucket needs one too, with or
+  // without a frequent id
   while ((2u << p.shift) <= v / 256u && (1u << p.shift) < kSortIds) ++p.shift;
   p.own = n >= kOwnFrom && p.shift != 0;
-  while (((uint64_t)(kMaxBuckets - (p.own ? 1u : 0u)) << p.shift) < v) ++p.shift;
+  while (((uint64_t)(kMaxBuckets - 1) << p.shift) < v) ++p.shift;
   p.buckets = (uint32_t)(((uint64_t)v + (1u << p.shift) - 1) >> p.shift);
+  p.counters = kMaxBuckets;
   p.per = n <= 32768 ? 1 : n <= 262144 ? 2 : 4;  // chunks grow with the tokens
-  p.chunks = n <= kDirect ? 0 : div_up(n, p.per * kChunkThreads);
+  p.chunk_len = p.per * kChunkThreads;
+  p.chunks = n <= kDirect ? 0 : div_up(n, p.chunk_len);
   // an f32 row takes more lanes, so its windows are smaller (one size covers
   // every type)
   const uint32_t windows = div_up(n, window_of(cover<kVec<float>>(d).lanes));
@@ -1095,7 +1098,7 @@ hipError_t launch_embed_grad(const EmbedGradPlan &plan, const int32_t *tokens, u
   auto sort = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(plan.buckets + helpers, share), dim3(kSortThreads),
                        kSortWaves * at_once * sizeof(uint32_t), stream, tokens, n, v, plan.shift,
-                       plan.buckets, cuts, plan.chunks, plan.per * kChunkThreads, entry_id,
+                       plan.buckets, cuts, plan.chunks, plan.chunk_len, entry_id,
                        entry_pos, frequent, perm, sorted, start, status);
   };
   if (plan.chunks != 0) sort(token_sort_kernel<false>);

@@ -220,7 +220,9 @@ hipError_t launch_embed(const void *table, uint32_t dtype, uint32_t v, uint32_t 
 struct EmbedGradPlan {
   uint32_t shift;    // table rows per bucket of the token sort: 2^shift
   uint32_t buckets;
-  uint32_t per;      // tokens of a chunk per thread
+  uint32_t counters;  // of a chunk: the buckets' and the frequent id's fit
+  uint32_t per;       // tokens of a chunk per thread
+  uint32_t chunk_len;
   uint32_t chunks;   // 0: the buckets read the tokens themselves
   bool own;          // a frequent id has a bucket of its own
   size_t off_perm, off_sorted, off_start, off_open, off_entry_id, off_entry_pos, off_cuts, off_part,

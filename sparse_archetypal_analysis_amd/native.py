@@ -39,7 +39,7 @@ EXPORTS = ("seacells_fw_a_columns_workspace", "seacells_fw_a_columns",
            "seacells_layer_norm", "seacells_layer_norm_grad_workspace", "seacells_layer_norm_grad",
            "seacells_logprobs_workspace", "seacells_logprobs", "seacells_logprobs_grad",
            "seacells_debug_set_a_options", "seacells_debug_b_layout",
-           "seacells_debug_b_last_epoch", "seacells_debug_b_reduce",
+           "seacells_debug_b_last_epoch", "seacells_debug_b_reduce", "seacells_debug_embed_plan",
            "seacells_fw_step_size",
            "seacells_status_string", "seacells_last_error", "seacells_version")
 
@@ -60,6 +60,13 @@ class seacells_b_layout(ctypes.Structure):
     _fields_ = [("keys_offset", ctypes.c_uint64), ("stamps_offset", ctypes.c_uint64),
                 ("n_row_blocks", ctypes.c_uint32), ("n_slices", ctypes.c_uint32),
                 ("slice_w", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class seacells_embed_plan(ctypes.Structure):
+    _fields_ = [("shift", ctypes.c_uint32), ("buckets", ctypes.c_uint32),
+                ("counters", ctypes.c_uint32), ("chunks", ctypes.c_uint32),
+                ("chunk_len", ctypes.c_uint32), ("frequent", ctypes.c_uint32),
+                ("cuts_offset", ctypes.c_uint64)]
 
 
 _CSR_P = ctypes.POINTER(seacells_csr)
@@ -174,6 +181,8 @@ def load():
     lib.seacells_debug_set_a_options.argtypes = [ctypes.POINTER(seacells_a_options)]
     lib.seacells_debug_b_layout.restype = ctypes.c_int
     lib.seacells_debug_b_layout.argtypes = [_U32, _U32, _U32, ctypes.POINTER(seacells_b_layout)]
+    lib.seacells_debug_embed_plan.restype = ctypes.c_int
+    lib.seacells_debug_embed_plan.argtypes = [_U32, _U32, _U32, ctypes.POINTER(seacells_embed_plan)]
     lib.seacells_debug_b_last_epoch.restype = ctypes.c_uint32
     lib.seacells_debug_b_last_epoch.argtypes = []
     lib.seacells_debug_b_reduce.restype = ctypes.c_int
@@ -1026,6 +1035,13 @@ def seacells_embed(table, tokens, scale=1.0, out=None, status=None, stream=None)
 
 def seacells_embed_grad_workspace(n, v, d) -> int:
     return _query(load().seacells_embed_grad_workspace, n, v, d)
+
+
+def seacells_debug_embed_plan(n: int, v: int, d: int) -> dict:
+    """How seacells_embed_grad sorts n tokens of a [v, d] table."""
+    out = seacells_embed_plan()
+    _check_rc(load().seacells_debug_embed_plan(n, v, d, ctypes.byref(out)))
+    return {nm: int(getattr(out, nm)) for nm, _ in seacells_embed_plan._fields_}
 
 
 def seacells_embed_grad(tokens, d_out, v: int, scale=1.0, add_to=None, d_table=None,

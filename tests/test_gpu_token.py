@@ -163,6 +163,32 @@ def test_embed_grad_of_many_tokens_and_ids(n, v, d, dtype):
     assert flags(saa.seacells_embed_grad(tok, d_out, v, d_table=out)[1]) == ["BAD_INDEX"]
 
 
+@pytest.mark.parametrize("n", [4096, 4097, 8192, 16383, 16384])
+@pytest.mark.parametrize("v", [523776, 523777, 524288, 524289, 1047552, 1048576])
+def test_embed_grad_where_the_buckets_meet_their_counters(n, v):
+    """Tables around the largest number of buckets, with tokens in the last
+    ones, for token counts with and without chunks and a frequent id's bucket;
+    a workspace that an earlier call left full."""
+    p = saa.seacells_debug_embed_plan(n, v, 2)
+    assert p["chunks"] == 0 or p["buckets"] < p["counters"]
+    rng = np.random.default_rng(n + v)
+    tok = ids(rng, n, v)
+    tok[: n // 4] = torch.from_numpy(rng.integers(v - 2000, v, n // 4).astype(np.int32)).cuda()
+    tok[n // 2], tok[0] = v - 1, 0
+    d_out = rows(rng, n, 2, "bf16", gap=1, start=1)
+    base, out = blank(v, 2, "f32", gap=1, start=1)
+    ws = torch.full((saa.seacells_embed_grad_workspace(n, v, 2),), 255, dtype=torch.uint8,
+                    device="cuda")
+    _, st = saa.seacells_embed_grad(tok, d_out, v, d_table=out, workspace=ws)
+    assert flags(st) == []
+    want, bound = R.embed_grad(exact(tok), exact(d_out), v, 1.0, None, "f32")
+    within(out, want, bound, "d_table")
+    untouched(base, out)
+    tok[n - 1] = v
+    assert flags(saa.seacells_embed_grad(tok, d_out, v, d_table=out, workspace=ws)[1]) == [
+        "BAD_INDEX"]
+
+
 @pytest.mark.parametrize("n", [1, 2, 63, 255, 256, 257])
 @pytest.mark.parametrize("v,d", [(1, 3), (15, 1031), (16, 8), (17, 2049), (900, 64), (5001, 20),
                                  (262144, 1), (4200000, 1)])

@@ -120,3 +120,39 @@ def test_binding_refuses_host_tensors_and_wrong_layouts():
                lambda: saa.seacells_layer_norm(torch.zeros(2, 3, 8).transpose(0, 1))):
         with pytest.raises(SeacellsError):
             go()
+
+
+def table_sizes():
+    """Both sides of every step of the sort's buckets: their number and their ids."""
+    steps = {1, 2, 255, 256, 511, 512, 1000, 2 ** 31 - 1}
+    for s in range(22):
+        for at in (1022 << s, 1023 << s, 1024 << s, 512 << s):
+            steps |= {t for t in (at - 1, at, at + 1) if 0 < t < 2 ** 31}
+    return sorted(steps)
+
+
+@pytest.mark.parametrize("n", [1, 4096, 4097, 8192, 16383, 16384, 32768, 32769, 262144, 262145,
+                               600000])
+def test_every_cut_of_the_token_sort_is_written(n):
+    """A chunk writes the cut of a bucket per counter, then its two totals; a
+    bucket reads its own cut and the next one's."""
+    for v in table_sizes():
+        p = saa.seacells_debug_embed_plan(n, v, 1)
+        assert (p["buckets"] - 1) << p["shift"] < v <= p["buckets"] << p["shift"], v
+        assert (p["chunks"] == 0) == (n <= 4096)
+        if p["chunks"] == 0:
+            continue
+        assert (p["chunks"] - 1) * p["chunk_len"] < n <= p["chunks"] * p["chunk_len"], v
+        written = set(range(min(p["counters"], p["buckets"] + 1)))
+        written |= {p["buckets"] + 1, p["buckets"] + 2}
+        assert written == set(range(p["buckets"] + 3)), v
+        end = p["cuts_offset"] + 4 * p["chunks"] * (p["buckets"] + 3)
+        assert end <= saa.seacells_embed_grad_workspace(n, v, 1), v
+
+
+def test_the_plan_of_the_token_sort_refuses():
+    with pytest.raises(SeacellsError):
+        saa.seacells_debug_embed_plan(4, 0, 8)
+    with pytest.raises(SeacellsError):
+        saa.seacells_debug_embed_plan(4, 2 ** 31, 8)
+    assert saa.load().seacells_debug_embed_plan(4, 8, 8, None) == NULL
