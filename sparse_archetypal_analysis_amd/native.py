@@ -940,11 +940,13 @@ def _rows(t, name, dev=None):
         except (RuntimeError, IndexError):
             raise SeacellsError("%s: the rows have no common stride" % name) from None
         shape = t.shape
+    n, d = shape
+    if d >= 1 << 31:  # (the library takes 32 bits)
+        raise SeacellsError("%s: a row of more than 2^31 - 1 elements" % name)
     at = t.get_device()
     if at < 0 or t.dtype not in _DTYPES or (dev is not None and at != dev):
         raise SeacellsError("%s must be a float32, float16 or bfloat16 tensor on the call's GPU"
                             % name)
-    n, d = shape
     ld, step = t.stride()
     if d > 1 and step != 1:
         raise SeacellsError("%s: a row's elements must be consecutive" % name)

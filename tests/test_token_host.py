@@ -156,3 +156,18 @@ def test_the_plan_of_the_token_sort_refuses():
     with pytest.raises(SeacellsError):
         saa.seacells_debug_embed_plan(4, 2 ** 31, 8)
     assert saa.load().seacells_debug_embed_plan(4, 8, 8, None) == NULL
+
+
+@pytest.mark.parametrize("d", [2 ** 31, 2 ** 32 + 5])
+def test_binding_refuses_rows_whose_length_32_bits_cannot_hold(d):
+    """A length is passed in 32 bits, where 2^32 + 5 elements would count as 5."""
+    one = torch.empty(1, d, dtype=torch.bfloat16, device="meta")
+    f = torch.empty(1)
+    for go in (lambda: saa.seacells_embed(one, torch.zeros(1, dtype=torch.int32)),
+               lambda: saa.seacells_embed_grad(torch.zeros(1, dtype=torch.int32), one, 3),
+               lambda: saa.seacells_layer_norm(one), lambda: saa.seacells_layer_norm(one[0]),
+               lambda: saa.seacells_layer_norm_grad(one, one, f, f),
+               lambda: saa.seacells_logprobs(one),
+               lambda: saa.seacells_logprobs_grad(one, None, torch.empty(1, 2))):
+        with pytest.raises(SeacellsError, match=r"2\^31 - 1 elements"):
+            go()
