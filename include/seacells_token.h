@@ -26,7 +26,8 @@
  * least the row's length; anything the element type's alignment allows).
  * dtype arguments are SEACELLS_F32 / F16 / BF16. Sums, statistics and norms
  * are f32; each output element is rounded to its type once. n = 0 rows is
- * allowed and writes only what does not depend on rows.
+ * allowed and writes only what does not depend on rows. An output overlaps no
+ * other operand, but where it is said that it may be one.
  */
 #ifndef SEACELLS_TOKEN_H
 #define SEACELLS_TOKEN_H
@@ -94,7 +95,8 @@ int seacells_embed_grad(const int32_t *tokens, uint32_t n, const void *d_out, ui
 /*
  * Layer norm of n rows of d elements: mean = sum x / d, rstd =
  * 1 / sqrt(sum (x - mean)^2 / d + eps), out = (x - mean) * rstd * weight + bias.
- * x, out        device [n, d] of dtype, row strides x_ld, out_ld. out may be x.
+ * x, out        device [n, d] of dtype, row strides x_ld, out_ld. out may be x
+ *               (same stride).
  * weight, bias  device [d] of weight_type (dtype or SEACELLS_F32); either may
  *               be NULL (1 and 0).
  * mean, rstd    device [n] f32 out, or NULL.
@@ -116,7 +118,7 @@ size_t seacells_layer_norm_grad_workspace(uint32_t n, uint32_t d);
  *   d_weight = sum over rows of d_out * h
  *   d_bias   = sum over rows of d_out
  * d_out, x, d_x      device [n, d] of dtype with row strides; d_x may be
- *                    d_out or x, or NULL (not computed).
+ *                    d_out or x (same stride), or NULL (not computed).
  * mean, rstd         device [n] f32 as the forward call wrote them.
  * weight             device [d] of weight_type, or NULL (1).
  * d_weight, d_bias   device [d] of weight_type, out; either may be NULL (not

@@ -25,6 +25,11 @@ int check_rows(uint32_t n, uint32_t d, uint64_t ld) {
   return SEACELLS_OK;
 }
 
+// Whether rows written in place of an operand's would lie on other rows of it.
+bool in_place_apart(uint32_t n, const void *out, uint64_t out_ld, const void *in, uint64_t in_ld) {
+  return n > 1 && out != nullptr && out == in && out_ld != in_ld;
+}
+
 int check_workspace(const void *ws, size_t bytes, size_t need) {
   if (need == 0) return SEACELLS_OK;
   if (ws == nullptr || bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
@@ -100,6 +105,7 @@ int seacells_layer_norm(const void *x, uint32_t dtype, uint32_t n, uint32_t d, u
       !aligned(bias, weight_type) || !aligned(mean, 0) || !aligned(rstd, 0))
     return SEACELLS_E_TYPE;
   if (!(eps >= 0.0f && std::isfinite(eps))) return SEACELLS_E_SHAPE;
+  if (in_place_apart(n, out, out_ld, x, x_ld)) return SEACELLS_E_SHAPE;
   int rc;
   if ((rc = check_rows(n, d, x_ld)) != SEACELLS_OK) return rc;
   if ((rc = check_rows(n, d, out_ld)) != SEACELLS_OK) return rc;
@@ -127,6 +133,8 @@ int seacells_layer_norm_grad(const void *d_out, uint64_t d_out_ld, const void *x
       !aligned(weight, weight_type) || !aligned(d_weight, weight_type) ||
       !aligned(d_bias, weight_type) || !aligned(mean, 0) || !aligned(rstd, 0))
     return SEACELLS_E_TYPE;
+  if (in_place_apart(n, d_x, d_x_ld, x, x_ld) || in_place_apart(n, d_x, d_x_ld, d_out, d_out_ld))
+    return SEACELLS_E_SHAPE;
   int rc;
   if ((rc = check_rows(n, d, d_out_ld)) != SEACELLS_OK) return rc;
   if ((rc = check_rows(n, d, x_ld)) != SEACELLS_OK) return rc;

@@ -1084,7 +1084,8 @@ def seacells_layer_norm(x, weight=None, bias=None, eps=1e-5, out=None, mean=None
     """Layer norm over the last dimension. Returns (out, mean, rstd); mean and
     rstd are float32 of one entry per row (what the gradient needs).
 
-    weight and bias [d] share a type: x's or float32. out may be x.
+    weight and bias [d] share a type: x's or float32. out may be x (a view of
+    the same start needs the same stride).
     """
     lib = load()
     n, d, ld, dev = _rows(x, "x")
@@ -1117,7 +1118,7 @@ def seacells_layer_norm_grad(d_out, x, mean, rstd, weight=None, d_x=None, d_weig
     """Gradients of seacells_layer_norm. Returns (d_x, d_weight, d_bias), the
     latter two of weight's type (x's without a weight).
 
-    d_x may be d_out or x. False for d_x, d_weight or d_bias leaves it out
+    d_x may be d_out or x (same stride). False for d_x, d_weight or d_bias leaves it out
     (returned as None).
     """
     lib = load()

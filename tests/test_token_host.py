@@ -171,3 +171,20 @@ def test_binding_refuses_rows_whose_length_32_bits_cannot_hold(d):
                lambda: saa.seacells_logprobs_grad(one, None, torch.empty(1, 2))):
         with pytest.raises(SeacellsError, match=r"2\^31 - 1 elements"):
             go()
+
+
+@pytest.mark.parametrize("fn,base,change,code", [
+    ("seacells_layer_norm", dict(NORM, n=2 ** 31, out=P, out_ld=16), dict(x_ld=16), TOO_LARGE),
+    ("seacells_layer_norm", dict(NORM, n=2 ** 31, out=P, x_ld=9), dict(out_ld=9), TOO_LARGE),
+    ("seacells_layer_norm_grad", dict(NORM_GRAD, ws_bytes=4, d_x=P, x=Q, d_x_ld=16),
+     dict(d_out_ld=16), WORKSPACE),
+    ("seacells_layer_norm_grad", dict(NORM_GRAD, ws_bytes=4, d_x=P, d_out=Q, x_ld=9),
+     dict(d_x_ld=9), WORKSPACE),
+    ("seacells_layer_norm_grad", dict(NORM_GRAD, ws_bytes=4, d_x=P, d_x_ld=16), dict(n=1),
+     WORKSPACE)], ids=lambda x: x if isinstance(x, str) else "")
+def test_in_place_norms_refuse_two_strides(fn, base, change, code):
+    """An output row would lie on input rows that other blocks have still to
+    read. (The base has a second fault, which alone is left with one stride
+    or one row: no call here comes to a launch.)"""
+    assert call(fn, **base)() == SHAPE
+    assert call(fn, **base)(**change) == code
