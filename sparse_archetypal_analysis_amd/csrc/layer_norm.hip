@@ -25,11 +25,11 @@ constexpr uint32_t kMaxBlocks = 1u << 20;
 constexpr uint32_t kFillThreads = 4096 * kThreads;
 
 // A row of d elements over kStride lanes, kR packs of kN each: x[k] holds the
-// elements from (k * kStride + at) * kN, those past the end `fill`. The row's
-// one broken pack has a branch of its own, its elements loaded at clamped
-// places (a branch in each load: 4096 bf16 65 us against 50, 2001 64 against
-// 41).
-template <class T, uint32_t kN, uint32_t kStride, uint32_t kR>
+// elements from (k * kStride + at) * kN, those past the end `fill` (in the
+// row's one broken pack its first element, if kRepeat). The broken pack has a
+// branch of its own, its elements loaded at clamped places (a branch in each
+// load: 4096 bf16 65 us against 50, 2001 64 against 41).
+template <class T, uint32_t kN, uint32_t kStride, uint32_t kR, bool kRepeat = false>
 __device__ __forceinline__ void load_row(const T *row, uint32_t at, uint32_t d, bool live, T fill,
                                          Pack<T, kN> (&x)[kR]) {
 #pragma unroll
@@ -44,7 +44,7 @@ __device__ __forceinline__ void load_row(const T *row, uint32_t at, uint32_t d, 
 #pragma unroll
     for (uint32_t j = 0; j < kN; ++j) y[j] = row[last * kN + j < d ? last * kN + j : d - 1];
 #pragma unroll
-    for (uint32_t j = 0; j < kN; ++j) y[j] = last * kN + j < d ? y[j] : fill;
+    for (uint32_t j = 0; j < kN; ++j) y[j] = last * kN + j < d ? y[j] : kRepeat ? y[0] : fill;
 #pragma unroll
     for (uint32_t k = 0; k < kR; ++k)
       if (k == last / kStride) x[k] = y;
@@ -236,21 +236,25 @@ __global__ void __launch_bounds__(kWaves > kGradWaves ? kWaves *kWave : kGradThr
     const T *row = x + (live ? i : 0) * x_ld, *dy = d_out + (live ? i : 0) * d_out_ld;
     Vec<T> v[kR], g[kR];
     load_row<T, kV, kRow, kR>(dy, at, d, live, (T)0.0f, g);
-    load_row<T, kV, kRow, kR>(row, at, d, live, (T)0.0f, v);
+    load_row<T, kV, kRow, kR, true>(row, at, d, live, (T)0.0f, v);
     const float mu = live ? mean[i] : 0.0f, rs = live ? rstd[i] : 0.0f;
-    // (columns past the end have d_y = 0 and add nothing to any sum)
-    float s[2] = {0.0f, 0.0f};
+    // (columns past the end have d_y = 0 and add nothing to any sum: their h is
+    // another column's, or 0, for mean * rstd may be past f32's range; d_x takes
+    // the same h, another one costs 16 registers: 100000 x 543 bf16 148 us for 95)
+    float s[2] = {0.0f, 0.0f}, r[kR];
 #pragma unroll
-    for (uint32_t k = 0; k < kR; ++k)
+    for (uint32_t k = 0; k < kR; ++k) {
+      r[k] = (k * kRow + at) * kV < d ? rs : 0.0f;
 #pragma unroll
       for (uint32_t j = 0; j < kV; ++j) {
-        const float y = (float)g[k][j], h = ((float)v[k][j] - mu) * rs;
+        const float y = (float)g[k][j], h = ((float)v[k][j] - mu) * r[k];
         const float t = y * (float)w[k][j];
         s[0] += t;
         s[1] += t * h;
         sw[k][j] += y * h;
         sb[k][j] += y;
       }
+    }
     if (d_x == nullptr) continue;
     if constexpr (kWaves > 1) {
       // groups of several waves: each its own part of the buffer
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(kWaves > kGradWaves ? kWaves *kWave : kGradThr
       Vec<T> y;
 #pragma unroll
       for (uint32_t j = 0; j < kV; ++j) {
-        const float h = ((float)v[k][j] - mu) * rs;
+        const float h = ((float)v[k][j] - mu) * r[k];
         y[j] = (T)(rs * ((float)g[k][j] * (float)w[k][j] - a - h * b));
       }
       if (c < d) store_vec_tail<T, true>(to, c, d, y);

@@ -397,6 +397,23 @@ def test_layer_norm_of_constant_rows(d):
     within(rstd, np.full(3, want), np.full(3, 4 * R.U * want), "rstd")
 
 
+@pytest.mark.parametrize("d", [1, 3, 5, 32, 33, 64, 130, 700, 1003, 5000, 70000])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_layer_norm_grad_of_constant_rows_far_from_zero(d, dtype):
+    """mean * rstd is past f32's range here, (x - mean) * rstd is 0: what a lane
+    holds past the row's end must not count."""
+    rng = np.random.default_rng(d)
+    x = torch.full((40, d), 2.0 ** 121, dtype=DT[dtype], device="cuda")
+    mean = torch.full((40,), 2.0 ** 121, device="cuda")
+    rstd = torch.full((40,), 316.0, device="cuda")
+    dy, w = rows(rng, 40, d, dtype), rows(rng, 1, d, "f32")[0]
+    got = saa.seacells_layer_norm_grad(dy, x, mean, rstd, w)
+    want, bound = R.layer_norm_grad(exact(dy), exact(x), exact(mean), exact(rstd), exact(w), dtype,
+                                    "f32")
+    for nm, g, y, e in zip(("d_x", "d_weight", "d_bias"), got, want, bound):
+        within(g, y, e, nm)
+
+
 @pytest.mark.parametrize("d", [5, 64, 700, 5000, 70000])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_layer_norm_of_rows_that_hold_no_numbers(d, dtype):
