@@ -86,14 +86,17 @@ def main():
     p.add_argument("--batch", type=int, default=8192)
     p.add_argument("--rate", type=float, default=0.3)
     a = p.parse_args()
+    if a.steps < 1:
+        p.error("--steps must be at least 1")
     w = W.make(a.config)
     cells, archetypes = (torch.from_numpy(t).cuda() for t in neighbour_pairs(w))
     model = Model(w.n, w.k, a.width)
     gen = torch.Generator(device="cuda").manual_seed(1)
     seen = []
+    first = min(3, a.steps - 1)  # the steps before load the kernels and are not timed
     for step in range(a.steps):
         pick = torch.randint(0, cells.numel(), (a.batch,), generator=gen, device="cuda")
-        if step == 3:  # the first steps load the kernels
+        if step == first:
             torch.cuda.synchronize()
             t0 = time.perf_counter()
         loss, grads, status = training_step(model, cells[pick], archetypes[pick], beta=0.01)
@@ -102,7 +105,7 @@ def main():
             value.sub_(grads[name], alpha=a.rate * (w.n / 64 if name == "table" else 1.0))
         seen.append(loss)
     torch.cuda.synchronize()
-    ms = (time.perf_counter() - t0) / max(1, a.steps - 3) * 1e3
+    ms = (time.perf_counter() - t0) / (a.steps - first) * 1e3
     for s in status:
         saa.raise_on_status(s)
     some = torch.arange(0, w.n, w.n // 4, dtype=torch.int32, device="cuda")[:4]

@@ -49,6 +49,21 @@ def test_a_training_step_gives_the_formulas_gradients(n, k, d, batch):
         assert float((g.cpu().double() - w).abs().max()) <= tol * float(w.abs().max()), name
 
 
+@pytest.mark.parametrize("steps", [1, 3, 5])
+def test_the_command_runs_any_number_of_steps(monkeypatch, capsys, steps):
+    monkeypatch.setattr("sys.argv", ["archetype_tokens", "--steps", str(steps), "--batch", "500"])
+    E.main()
+    out = capsys.readouterr().out
+    assert "ms per step" in out and "loss" in out and out.count("archetypes [") == 4
+
+
+def test_the_command_refuses_no_steps(monkeypatch, capsys):
+    monkeypatch.setattr("sys.argv", ["archetype_tokens", "--steps", "0"])
+    with pytest.raises(SystemExit):
+        E.main()
+    assert "--steps" in capsys.readouterr().err
+
+
 def test_the_model_learns_and_answers():
     rng = np.random.default_rng(0)
     n, k = 300, 12
