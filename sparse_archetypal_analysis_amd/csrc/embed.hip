@@ -112,8 +112,6 @@ __global__ void __launch_bounds__(kThreads)
 // in two launches; up to kDirect of them it saves the chunks' launch: 3500
 // tokens and 20000 ids of 64 columns 20.8 us against 25.8.)
 
-typedef int32_t Four __attribute__((ext_vector_type(4), aligned(4)));
-
 constexpr uint32_t kChunkThreads = 256;
 constexpr uint32_t kChunkWaves = kChunkThreads / kWave;
 constexpr uint32_t kMaxBuckets = 1024;  // with that of the frequent id (there or not)

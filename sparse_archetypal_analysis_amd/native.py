@@ -926,6 +926,7 @@ def outer_iteration(K: DeviceCSR, b: DeviceCSR, k2b: DeviceCSR, a_t: DeviceCSR, 
 # Row operands are [..., d] tensors of float32, float16 or bfloat16 with
 # consecutive elements in a row and one stride between rows. Outputs,
 # workspace and status are allocated on the call's stream when not given.
+# The calls record nothing for autograd: a backward pass calls the gradients.
 
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 TOP_MAX = 64  # SEACELLS_TOP_MAX

@@ -6,9 +6,13 @@ exact values and returns (outputs, bounds). U is f32's largest relative
 rounding error; ``half(t)`` the half step of an output type. Bounds count,
 for every f32 operation on the way to an output, U times the size of its
 result; a sum of c terms held in parts costs at most (its longest chain) U
-times the sum of the terms' sizes. No lane of a kernel adds more than
-1/64 of a row, so a row's chain is at most its length / 64 + 16 (the 16: a
-lane's own vector, and the levels that join 1024 lanes).
+times the sum of the terms' sizes. A row's chain is taken for its length / 64
++ 16: a wave's lane adds 1/64 of the row, rounded up to its vectors, and some
+levels join the lanes. That is not the longest chain of every spread of a row.
+The norms' is up to 37 for halves of 1025 to 2048 elements (32 per lane, 6
+levels), 5 more than said at 1025; log probabilities of short rows, 8 to 32
+lanes of up to 32 elements, have up to 37 where chain() says 18, and their
+bounds count four chains.
 """
 import numpy as np
 
