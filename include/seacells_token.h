@@ -4,8 +4,8 @@
  *
  * A fit gives cells (rows of K), archetypes and an assignment A. A model that
  * learns from them - cells or archetypes as tokens, K's neighbour lists as
- * training pairs, a cell's archetype as the class to predict - needs three
- * operators around its matrix products, each with its gradient:
+ * training pairs, a cell's archetype as the class to predict - needs these
+ * operators, each with its gradient:
  *
  *   embed        y[i] = scale * table[token[i]]
  *   embed_grad   d_table[t] = scale * sum of d_y[i] over token[i] = t
@@ -13,6 +13,11 @@
  *   layer_norm_grad, with the sums of the weight's and the bias' gradient
  *   logprobs     log p of given classes, entropy, the top alternatives
  *   logprobs_grad
+ *   gated_ffn    y = (act(x W_gate^T) * (x W_up^T)) W_out^T, the model's block
+ *   gated_ffn_grad
+ *   linear_logprobs   log p of given classes and entropy from hidden rows and
+ *                the class table, without the logits in memory
+ *   linear_logprobs_grad
  *
  * Conventions (as in seacells_fw.h): the caller allocates every buffer; the
  * library never allocates or synchronises and enqueues all work on `stream`.
@@ -179,6 +184,117 @@ int seacells_logprobs_grad(const void *logits, uint32_t dtype, uint32_t n, uint3
                            const float *entropy, const float *d_logp, const float *d_entropy,
                            void *d_logits, uint64_t d_logits_ld, uint32_t *status,
                            seacells_stream_t stream);
+
+/* Activations of the gated block: g / (1 + e^-g); g Phi(g), Phi the normal
+ * distribution's integral; max(g, 0) (derivative 0 at 0). */
+#define SEACELLS_ACT_SILU 0u
+#define SEACELLS_ACT_GELU 1u
+#define SEACELLS_ACT_RELU 2u
+
+/* Longest row of a matrix product's operand (d, f and m below). */
+#define SEACELLS_MAX_INNER (1u << 20)
+
+/*
+ * Workspace bytes that a call of these sizes needs (below: of the same name).
+ * on_16_bytes: nonzero if every matrix operand of the call starts on 16 bytes,
+ * has a row stride of a multiple of 16 bytes and at most 2^21 elements, and
+ * (f + 256) * w_in_ld is below 2^30: 16-bit operands with rows of a multiple
+ * of 8 elements are then multiplied where they are, others are copied to the
+ * workspace by every call. 0: room for copies of all. 0 is returned for sizes
+ * that no call takes, and for n = 0.
+ */
+size_t seacells_gated_ffn_workspace(uint32_t dtype, uint32_t n, uint32_t d, uint32_t f, uint32_t m,
+                                    uint32_t on_16_bytes);
+size_t seacells_gated_ffn_grad_workspace(uint32_t dtype, uint32_t n, uint32_t d, uint32_t f,
+                                         uint32_t m, uint32_t on_16_bytes);
+size_t seacells_linear_logprobs_workspace(uint32_t dtype, uint32_t n, uint32_t d, uint32_t v,
+                                          uint32_t on_16_bytes);
+size_t seacells_linear_logprobs_grad_workspace(uint32_t dtype, uint32_t n, uint32_t d, uint32_t v,
+                                               uint32_t on_16_bytes);
+
+/*
+ * Gated feed-forward block over n rows:
+ *   pre = x w_in^T;  h = act(pre[:, :f]) * pre[:, f:];  out = h w_out^T
+ * x      device [n, d]; w_in device [2f, d], f gate rows, then f up rows;
+ *        w_out device [m, f]; out device [n, m]; all of dtype, row strides *_ld.
+ * pre    device [n, 2f] of dtype out, or NULL: what the gradient needs.
+ * act    SEACELLS_ACT_*.
+ * h is computed from the unrounded pre and held in dtype between the products
+ * (f16: an h past 65504 is an infinity). f32 products are sums of bf16
+ * products of the operands' three parts, to f32's accuracy; where an operand
+ * holds an infinity, results that depend on it are NaN or infinite.
+ * (f + 256) * (d + 7) is below 2^30 (SEACELLS_E_TOO_LARGE).
+ * workspace: seacells_gated_ffn_workspace bytes, 256-byte aligned.
+ */
+int seacells_gated_ffn(const void *x, uint32_t dtype, uint32_t n, uint32_t d, uint64_t x_ld,
+                       const void *w_in, uint64_t w_in_ld, uint32_t f, const void *w_out,
+                       uint64_t w_out_ld, uint32_t m, uint32_t act, void *out, uint64_t out_ld,
+                       void *pre, uint64_t pre_ld, void *workspace, size_t workspace_bytes,
+                       seacells_stream_t stream);
+
+/*
+ * Gradients of seacells_gated_ffn from pre as the forward call wrote it. With
+ * g, u the halves of pre, dh = d_out w_out and
+ * d_pre = [dh u act'(g), dh act(g)]:
+ *   d_x = d_pre w_in [n, d];  d_w_in = d_pre^T x [2f, d];
+ *   d_w_out = d_out^T h [m, f], h = act(g) u
+ * All of dtype; each of the three may be NULL (not computed). d_pre and h are
+ * held in dtype between the products. n = 0 gives zero weight gradients.
+ * workspace: seacells_gated_ffn_grad_workspace bytes, 256-byte aligned.
+ */
+int seacells_gated_ffn_grad(const void *d_out, uint64_t d_out_ld, const void *x, uint32_t dtype,
+                            uint32_t n, uint32_t d, uint64_t x_ld, const void *pre, uint64_t pre_ld,
+                            const void *w_in, uint64_t w_in_ld, uint32_t f, const void *w_out,
+                            uint64_t w_out_ld, uint32_t m, uint32_t act, void *d_x, uint64_t d_x_ld,
+                            void *d_w_in, uint64_t d_w_in_ld, void *d_w_out, uint64_t d_w_out_ld,
+                            void *workspace, size_t workspace_bytes, seacells_stream_t stream);
+
+/*
+ * Log probabilities of n hidden rows over v classes, z = x table^T + bias, as
+ * seacells_logprobs gives them of logits z that stay in f32 and are not kept:
+ *   stats[i] = (m, s), m = max z, s = log sum exp(z - m)   [n, 2] f32 out, or NULL
+ *   logp[i] = z[targets[i]] - m - s                        [n] f32 out, or NULL
+ *   entropy[i] = -sum p log p                              [n] f32 out, or NULL
+ * x       device [n, d], table device [v, d], of dtype, row strides *_ld.
+ * bias    device [v] f32, or NULL (0). A class whose bias is -inf is masked
+ *         for every row (p = 0), whatever its row of the table holds.
+ * targets device [n] int32, or NULL with logp NULL. A negative target is
+ *         ignored (logp 0); a target >= v too, with SEACELLS_FLAG_BAD_INDEX.
+ * Where every class is masked: stats (-inf, 0), logp -inf, entropy 0. A row
+ * with a NaN or +inf among its z has no distribution: its outputs are NaN
+ * (logp of an ignored target stays 0).
+ * v is at most SEACELLS_MAX_WIDTH.
+ * workspace: seacells_linear_logprobs_workspace bytes, 256-byte aligned.
+ */
+int seacells_linear_logprobs(const void *x, uint32_t dtype, uint32_t n, uint32_t d, uint64_t x_ld,
+                             const void *table, uint64_t table_ld, uint32_t v, const float *bias,
+                             const int32_t *targets, float *logp, float *entropy, float *stats,
+                             void *workspace, size_t workspace_bytes, uint32_t *status,
+                             seacells_stream_t stream);
+
+/*
+ * Gradients of sum_i d_logp[i] logp[i] + d_entropy[i] entropy[i], with
+ *   d_z = d_logp (1[class = target] - p) - d_entropy p (log p + entropy):
+ *   d_x = d_z table [n, d];  d_table = d_z^T x [v, d];  d_bias = column sums [v]
+ * x, table, bias, targets  as the forward call's (targets NULL: all ignored).
+ * stats, entropy           as it wrote them; entropy may be NULL with d_entropy
+ *                          NULL.
+ * d_logp, d_entropy        device [n] f32; either may be NULL (0).
+ * d_x, d_table             of dtype, d_bias f32; each may be NULL.
+ * d_z is computed anew in pieces of the classes and held in dtype between the
+ * products (f16: times a power of two); d_bias sums it before that rounding.
+ * Masked classes and rows with nothing left have d_z 0 (a masked class' row of
+ * the table and every row of x still have to be finite for d_x and d_table to
+ * be); a row without a distribution has NaN. n = 0 gives zero d_table, d_bias.
+ * workspace: seacells_linear_logprobs_grad_workspace bytes, 256-byte aligned.
+ */
+int seacells_linear_logprobs_grad(const void *x, uint32_t dtype, uint32_t n, uint32_t d,
+                                  uint64_t x_ld, const void *table, uint64_t table_ld, uint32_t v,
+                                  const float *bias, const int32_t *targets, const float *stats,
+                                  const float *entropy, const float *d_logp, const float *d_entropy,
+                                  void *d_x, uint64_t d_x_ld, void *d_table, uint64_t d_table_ld,
+                                  float *d_bias, void *workspace, size_t workspace_bytes,
+                                  uint32_t *status, seacells_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -25,4 +25,7 @@ from .native import (DeviceCSR, SeacellsError, load, new_status, raise_on_status
                      seacells_embed, seacells_embed_grad_workspace, seacells_embed_grad,
                      seacells_layer_norm, seacells_layer_norm_grad_workspace,
                      seacells_layer_norm_grad, seacells_logprobs_workspace, seacells_logprobs,
-                     seacells_logprobs_grad)
+                     seacells_logprobs_grad, seacells_gated_ffn_workspace, seacells_gated_ffn,
+                     seacells_gated_ffn_grad_workspace, seacells_gated_ffn_grad,
+                     seacells_linear_logprobs_workspace, seacells_linear_logprobs,
+                     seacells_linear_logprobs_grad_workspace, seacells_linear_logprobs_grad)

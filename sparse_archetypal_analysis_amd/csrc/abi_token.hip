@@ -43,6 +43,49 @@ int done(hipError_t e, const char *what) {
   return e == hipSuccess ? SEACELLS_OK : hip_fail(e, what);
 }
 
+// A matrix product's rows: their length and stride are bounded too.
+constexpr uint32_t kMaxInner = SEACELLS_MAX_INNER;
+
+int check_inner(uint32_t n, uint32_t d, uint64_t ld) {
+  const int rc = check_rows(n, d, ld);
+  return rc != SEACELLS_OK ? rc : d > kMaxInner ? SEACELLS_E_TOO_LARGE : SEACELLS_OK;
+}
+
+bool ffn_sizes(uint32_t dtype, uint32_t act, uint32_t n, uint32_t d, uint32_t f, uint32_t m) {
+  return dtype_known(dtype) && act <= SEACELLS_ACT_RELU && n < kTooLarge && d > 0 && f > 0 && m > 0 &&
+         d <= kMaxInner && f <= kMaxInner && m <= kMaxInner &&
+         (f + 256ull) * (d + 7ull) < (1ull << 30);
+}
+
+int check_ffn(const FfnCall &c) {
+  if (c.w_in == nullptr || c.w_out == nullptr || (c.n > 0 && c.x == nullptr)) return SEACELLS_E_NULL;
+  if (!dtype_known(c.dtype) || !aligned(c.x, c.dtype) || !aligned(c.w_in, c.dtype) ||
+      !aligned(c.w_out, c.dtype))
+    return SEACELLS_E_TYPE;
+  if (static_cast<uint32_t>(c.act) > SEACELLS_ACT_RELU || c.f == 0 || c.m == 0)
+    return SEACELLS_E_SHAPE;
+  int rc;
+  if ((rc = check_inner(c.n, c.d, c.x_ld)) != SEACELLS_OK) return rc;
+  if (c.f > kMaxInner || c.m > kMaxInner) return SEACELLS_E_TOO_LARGE;
+  if ((rc = check_inner(2 * c.f, c.d, c.w_in_ld)) != SEACELLS_OK) return rc;
+  if ((rc = check_inner(c.m, c.f, c.w_out_ld)) != SEACELLS_OK) return rc;
+  if (!ffn_sizes(c.dtype, static_cast<uint32_t>(c.act), c.n, c.d, c.f, c.m))
+    return SEACELLS_E_TOO_LARGE;
+  return SEACELLS_OK;
+}
+
+int check_loss(const LossCall &c) {
+  if (c.table == nullptr || (c.n > 0 && c.x == nullptr)) return SEACELLS_E_NULL;
+  if (!dtype_known(c.dtype) || !aligned(c.x, c.dtype) || !aligned(c.table, c.dtype) ||
+      !aligned(c.bias, 0) || !aligned(c.targets, 0))
+    return SEACELLS_E_TYPE;
+  if (c.v == 0) return SEACELLS_E_SHAPE;
+  if (c.v > kMaxWidth) return SEACELLS_E_TOO_LARGE;
+  int rc;
+  if ((rc = check_inner(c.n, c.d, c.x_ld)) != SEACELLS_OK) return rc;
+  return check_inner(c.v, c.d, c.table_ld);
+}
+
 }  // namespace
 
 extern "C" {
@@ -197,6 +240,148 @@ int seacells_logprobs_grad(const void *logits, uint32_t dtype, uint32_t n, uint3
   return done(launch_logprobs_grad(logits, dtype, n, v, ld, targets, stats, entropy, d_logp,
                                    d_entropy, d_logits, d_logits_ld, status, hip_stream(stream)),
               "logprobs_grad launch");
+}
+
+size_t seacells_gated_ffn_workspace(uint32_t dtype, uint32_t n, uint32_t d, uint32_t f, uint32_t m,
+                                    uint32_t on_16_bytes) {
+  if (!ffn_sizes(dtype, 0, n, d, f, m)) return 0;
+  FfnCall c = {};
+  c.dtype = dtype;
+  c.n = n;
+  c.d = d;
+  c.f = f;
+  c.m = m;
+  return ffn_workspace(c, on_16_bytes != 0);
+}
+
+int seacells_gated_ffn(const void *x, uint32_t dtype, uint32_t n, uint32_t d, uint64_t x_ld,
+                       const void *w_in, uint64_t w_in_ld, uint32_t f, const void *w_out,
+                       uint64_t w_out_ld, uint32_t m, uint32_t act, void *out, uint64_t out_ld,
+                       void *pre, uint64_t pre_ld, void *workspace, size_t workspace_bytes,
+                       seacells_stream_t stream) {
+  const FfnCall c = {dtype, static_cast<Act>(act), n, d, f, m, x, w_in, w_out, x_ld, w_in_ld, w_out_ld};
+  int rc;
+  if (n > 0 && out == nullptr) return SEACELLS_E_NULL;
+  if ((rc = check_ffn(c)) != SEACELLS_OK) return rc;
+  if (!aligned(out, dtype) || !aligned(pre, dtype)) return SEACELLS_E_TYPE;
+  if ((rc = check_rows(n, m, out_ld)) != SEACELLS_OK) return rc;
+  if (pre != nullptr && (rc = check_rows(n, 2 * f, pre_ld)) != SEACELLS_OK) return rc;
+  if ((rc = check_workspace(workspace, workspace_bytes, ffn_need(c))) != SEACELLS_OK) return rc;
+  return done(launch_ffn(c, out, out_ld, pre, pre_ld, workspace, hip_stream(stream)),
+              "gated_ffn launch");
+}
+
+size_t seacells_gated_ffn_grad_workspace(uint32_t dtype, uint32_t n, uint32_t d, uint32_t f,
+                                         uint32_t m, uint32_t on_16_bytes) {
+  if (!ffn_sizes(dtype, 0, n, d, f, m)) return 0;
+  FfnGradCall c = {};
+  c.dtype = dtype;
+  c.n = n;
+  c.d = d;
+  c.f = f;
+  c.m = m;
+  return ffn_grad_workspace(c, on_16_bytes != 0);
+}
+
+int seacells_gated_ffn_grad(const void *d_out, uint64_t d_out_ld, const void *x, uint32_t dtype,
+                            uint32_t n, uint32_t d, uint64_t x_ld, const void *pre, uint64_t pre_ld,
+                            const void *w_in, uint64_t w_in_ld, uint32_t f, const void *w_out,
+                            uint64_t w_out_ld, uint32_t m, uint32_t act, void *d_x, uint64_t d_x_ld,
+                            void *d_w_in, uint64_t d_w_in_ld, void *d_w_out, uint64_t d_w_out_ld,
+                            void *workspace, size_t workspace_bytes, seacells_stream_t stream) {
+  FfnGradCall c = {};
+  static_cast<FfnCall &>(c) = {dtype, static_cast<Act>(act), n, d, f, m, x, w_in, w_out,
+                               x_ld,  w_in_ld, w_out_ld};
+  c.d_out = d_out;
+  c.pre = pre;
+  c.d_out_ld = d_out_ld;
+  c.pre_ld = pre_ld;
+  int rc;
+  if (n > 0 && (d_out == nullptr || pre == nullptr)) return SEACELLS_E_NULL;
+  if ((rc = check_ffn(c)) != SEACELLS_OK) return rc;
+  if (!aligned(d_out, dtype) || !aligned(pre, dtype) || !aligned(d_x, dtype) ||
+      !aligned(d_w_in, dtype) || !aligned(d_w_out, dtype))
+    return SEACELLS_E_TYPE;
+  if ((rc = check_rows(n, m, d_out_ld)) != SEACELLS_OK) return rc;
+  if ((rc = check_rows(n, 2 * f, pre_ld)) != SEACELLS_OK) return rc;
+  if (d_x != nullptr && (rc = check_rows(n, d, d_x_ld)) != SEACELLS_OK) return rc;
+  if (d_w_in != nullptr && (rc = check_rows(2 * f, d, d_w_in_ld)) != SEACELLS_OK) return rc;
+  if (d_w_out != nullptr && (rc = check_rows(m, f, d_w_out_ld)) != SEACELLS_OK) return rc;
+  if ((rc = check_workspace(workspace, workspace_bytes, ffn_grad_need(c))) != SEACELLS_OK) return rc;
+  return done(launch_ffn_grad(c, d_x, d_x_ld, d_w_in, d_w_in_ld, d_w_out, d_w_out_ld, workspace,
+                              hip_stream(stream)),
+              "gated_ffn_grad launch");
+}
+
+static bool loss_sizes(uint32_t dtype, uint32_t n, uint32_t d, uint32_t v) {
+  return dtype_known(dtype) && n < kTooLarge && d > 0 && d <= kMaxInner && v > 0 && v <= kMaxWidth;
+}
+
+size_t seacells_linear_logprobs_workspace(uint32_t dtype, uint32_t n, uint32_t d, uint32_t v,
+                                          uint32_t on_16_bytes) {
+  if (!loss_sizes(dtype, n, d, v)) return 0;
+  LossCall c = {};
+  c.dtype = dtype;
+  c.n = n;
+  c.d = d;
+  c.v = v;
+  return loss_workspace(c, on_16_bytes != 0);
+}
+
+int seacells_linear_logprobs(const void *x, uint32_t dtype, uint32_t n, uint32_t d, uint64_t x_ld,
+                             const void *table, uint64_t table_ld, uint32_t v, const float *bias,
+                             const int32_t *targets, float *logp, float *entropy, float *stats,
+                             void *workspace, size_t workspace_bytes, uint32_t *status,
+                             seacells_stream_t stream) {
+  const LossCall c = {dtype, n, d, v, x, table, x_ld, table_ld, bias, targets};
+  int rc;
+  if (status == nullptr || (logp != nullptr && targets == nullptr && n > 0)) return SEACELLS_E_NULL;
+  if ((rc = check_loss(c)) != SEACELLS_OK) return rc;
+  if (!aligned(logp, 0) || !aligned(entropy, 0) || !aligned(stats, 0)) return SEACELLS_E_TYPE;
+  if ((rc = check_workspace(workspace, workspace_bytes, loss_need(c))) != SEACELLS_OK) return rc;
+  return done(launch_loss(c, logp, entropy, stats, workspace, status, hip_stream(stream)),
+              "linear_logprobs launch");
+}
+
+size_t seacells_linear_logprobs_grad_workspace(uint32_t dtype, uint32_t n, uint32_t d, uint32_t v,
+                                               uint32_t on_16_bytes) {
+  if (!loss_sizes(dtype, n, d, v)) return 0;
+  LossGradCall c = {};
+  c.dtype = dtype;
+  c.n = n;
+  c.d = d;
+  c.v = v;
+  return loss_grad_workspace(c, on_16_bytes != 0);
+}
+
+int seacells_linear_logprobs_grad(const void *x, uint32_t dtype, uint32_t n, uint32_t d,
+                                  uint64_t x_ld, const void *table, uint64_t table_ld, uint32_t v,
+                                  const float *bias, const int32_t *targets, const float *stats,
+                                  const float *entropy, const float *d_logp, const float *d_entropy,
+                                  void *d_x, uint64_t d_x_ld, void *d_table, uint64_t d_table_ld,
+                                  float *d_bias, void *workspace, size_t workspace_bytes,
+                                  uint32_t *status, seacells_stream_t stream) {
+  LossGradCall c = {};
+  static_cast<LossCall &>(c) = {dtype, n, d, v, x, table, x_ld, table_ld, bias, targets};
+  c.stats = stats;
+  c.entropy = entropy;
+  c.d_logp = d_logp;
+  c.d_entropy = d_entropy;
+  int rc;
+  if (status == nullptr || (n > 0 && (stats == nullptr || (d_entropy != nullptr && entropy == nullptr))))
+    return SEACELLS_E_NULL;
+  if ((rc = check_loss(c)) != SEACELLS_OK) return rc;
+  if (!aligned(stats, 0) || !aligned(entropy, 0) || !aligned(d_logp, 0) || !aligned(d_entropy, 0) ||
+      !aligned(d_x, dtype) || !aligned(d_table, dtype) || !aligned(d_bias, 0))
+    return SEACELLS_E_TYPE;
+  if (d_x != nullptr && (rc = check_rows(n, d, d_x_ld)) != SEACELLS_OK) return rc;
+  if (d_table != nullptr && (rc = check_rows(v, d, d_table_ld)) != SEACELLS_OK) return rc;
+  if ((rc = check_workspace(workspace, workspace_bytes,
+                            loss_grad_need(c, d_x != nullptr, d_bias != nullptr))) != SEACELLS_OK)
+    return rc;
+  return done(launch_loss_grad(c, d_x, d_x_ld, d_table, d_table_ld, d_bias, workspace, status,
+                               hip_stream(stream)),
+              "linear_logprobs_grad launch");
 }
 
 int seacells_debug_embed_plan(uint32_t n, uint32_t v, uint32_t d, seacells_embed_plan *out) {

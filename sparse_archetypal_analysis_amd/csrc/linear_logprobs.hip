@@ -1,0 +1,565 @@
+// Log probabilities straight from hidden rows and a class table, and their
+// gradient, on gfx950: a product of x [n, d] and table [v, d] on the matrix
+// cores (mm.hpp) whose results z = x table^T + bias never reach memory as
+// logits.
+//
+// Forward: a wave keeps of its tile's rows the maximum, sum e^(z - m) and
+// sum (z - m) e^(z - m); the target's z is the one result that is written.
+// A second kernel joins the slices of a row.
+//
+// Backward, in pieces of the classes: z again, d_z from it and the rows'
+// figures, to a buffer of one piece (16 bits; f32: three bf16), then
+// d_table's rows of the piece, finished, and the piece's part of d_x, kept in
+// f32 between pieces. d_bias is summed from d_z before its rounding.
+#include "mm.hpp"
+
+namespace seacells {
+namespace {
+
+using namespace mm;
+
+constexpr float kInf = __builtin_huge_valf();
+
+// What a row's figures are made of: maximum, sum e^(z - m), sum (z - m) e^(z - m).
+struct Sums {
+  float m, s, u;
+};
+
+// The same for the maximum m (not below own.m); nothing: (-inf, 0, 0).
+__device__ __forceinline__ void rescale(Sums &a, float m) {
+  const bool none = a.m == -kInf;
+  const float t = none ? 0.0f : a.m - m;
+  const float e = none ? 0.0f : exp_neg(t);
+  a.u = none ? 0.0f : e * (a.u + t * a.s);
+  a.s *= e;
+  a.m = m;
+}
+
+__device__ __forceinline__ Sums joined(Sums a, Sums b) {
+  const float m = nan_max(a.m, b.m);
+  rescale(a, m);
+  rescale(b, m);
+  return Sums{m, a.s + b.s, a.u + b.u};
+}
+
+__device__ __forceinline__ float logit(float z, float bias) {
+  return bias == -kInf ? -kInf : z + bias;  // (a masked class' row may hold anything)
+}
+
+// The bias of a lane's columns, -inf behind the last class.
+template <uint32_t kSub>
+__device__ __forceinline__ void load_bias(const float *bias, uint32_t col0, uint32_t n,
+                                          float (&b)[kSub][4]) {
+  const uint32_t lane = lane_id();
+#pragma unroll
+  for (uint32_t j = 0; j < kSub; ++j) {
+    const uint32_t col = col0 + outer_of(j, (lane / 16) * 4);
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e)
+      b[j][e] = col + e >= n ? -kInf : bias != nullptr ? bias[min(col + e, n - 1)] : 0.0f;
+  }
+}
+
+// Epilogue of the forward product. A slice is a wave's columns (half a tile).
+struct RowSums {
+  const float *bias;
+  const int32_t *targets;  // of the first row here
+  float *sums;             // [slice][3][rows]
+  float *at_target;        // [rows]
+  uint32_t rows, n;
+
+  template <uint32_t kTile, bool kGated, uint32_t kSub>
+  __device__ __forceinline__ void run(const Acc (&acc)[kSub][kSub], uint32_t row0, uint32_t col0,
+                                      uint32_t) const {
+    const uint32_t lane = lane_id();
+    float b[kSub][4];
+    load_bias(bias, col0, n, b);
+    float *const out = sums + (uint64_t)(col0 / (kTile / 2)) * 3 * rows;
+#pragma unroll
+    for (uint32_t i = 0; i < kSub; ++i) {
+      const uint32_t row = row0 + outer_of(i, lane & 15);
+      float z[kSub][4];
+      float m = -kInf;
+#pragma unroll
+      for (uint32_t j = 0; j < kSub; ++j)
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) {
+          z[j][e] = logit(acc[i][j][e], b[j][e]);
+          m = nan_max(m, z[j][e]);
+        }
+      m = nan_max(m, __shfl_xor(m, 16, kWave));
+      m = nan_max(m, __shfl_xor(m, 32, kWave));
+      const float base = m == -kInf ? 0.0f : m;
+      float s = 0.0f, u = 0.0f;
+#pragma unroll
+      for (uint32_t j = 0; j < kSub; ++j)
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) {
+          const float t = z[j][e] - base;
+          const float x = exp_neg(t);
+          s += x;
+          u += t == -kInf ? 0.0f : t * x;
+        }
+      s += __shfl_xor(s, 16, kWave);
+      u += __shfl_xor(u, 16, kWave);
+      s += __shfl_xor(s, 32, kWave);
+      u += __shfl_xor(u, 32, kWave);
+      if (row >= rows) continue;
+      if (lane < 16) {
+        out[row] = m;
+        out[(uint64_t)rows + row] = s;
+        out[2ull * rows + row] = u;
+      }
+      if (targets == nullptr) continue;
+      const uint32_t in = (uint32_t)targets[row] - col0;
+      if (in < kTile / 2 && in + col0 < n) {
+#pragma unroll
+        for (uint32_t j = 0; j < kSub; ++j)
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e)
+            if (in == outer_of(j, (lane / 16) * 4) + e) at_target[row] = z[j][e];
+      }
+    }
+  }
+};
+
+// Rows' slices joined, 16 threads a row and 16 rows a block; the last block
+// reports targets past the classes.
+__global__ __launch_bounds__(kThreads) void join_rows(const float *__restrict__ sums,
+                                                      const float *__restrict__ at_target,
+                                                      uint32_t slices, uint32_t rows, uint32_t v,
+                                                      const int32_t *__restrict__ targets,
+                                                      float *__restrict__ logp,
+                                                      float *__restrict__ entropy,
+                                                      float *__restrict__ stats,
+                                                      const int32_t *__restrict__ all_targets,
+                                                      uint32_t all, uint32_t *__restrict__ status) {
+  if (blockIdx.x == gridDim.x - 1) {
+    if (status != nullptr) report_ids<kThreads>(all_targets, all, v, status);
+    return;
+  }
+  __shared__ Sums part[16][17];
+  const uint32_t in = threadIdx.x & 15, lane = threadIdx.x / 16;
+  const uint32_t row = blockIdx.x * 16 + in;
+  Sums a = {-kInf, 0.0f, 0.0f};
+  if (row < rows)
+    for (uint32_t k = lane; k < slices; k += 16) {
+      const float *const p = sums + (uint64_t)k * 3 * rows + row;
+      a = joined(a, Sums{p[0], p[rows], p[2ull * rows]});
+    }
+  part[lane][in] = a;
+  __syncthreads();
+  if (threadIdx.x >= 16 || row >= rows) return;
+  for (uint32_t k = 1; k < 16; ++k) a = joined(a, part[k][in]);
+  const bool none = a.m == -kInf;
+  // NaN: a row that holds NaN or +inf has no distribution
+  const float m = a.m == kInf ? __builtin_nanf("") : a.m;
+  const float ls = none ? 0.0f : logf(a.s) + (m - m);
+  if (stats != nullptr) {
+    stats[2ull * row] = m;
+    stats[2ull * row + 1] = ls;
+  }
+  if (entropy != nullptr) entropy[row] = none ? 0.0f : ls - a.u / a.s;
+  if (logp != nullptr) {
+    const int32_t t = targets[row];
+    const bool known = t >= 0 && (uint32_t)t < v;
+    logp[row] = !known ? 0.0f : none ? -kInf : at_target[row] - m - ls;
+  }
+}
+
+// --- backward ------------------------------------------------------------------
+
+// f16 holds 2^-24 to 2^15; d_z of a mean over rows is far below that. It is
+// kept times a power of two that takes its bound, max |d_logp| + 17 |d_entropy|
+// (p |log p + H| <= 0.4 + log v), to below 2^15. Also reports targets past the
+// classes. One block.
+constexpr uint32_t kPrepare = 1024;
+__global__ __launch_bounds__(kPrepare) void prepare_rows(const int32_t *__restrict__ targets,
+                                                         const float *__restrict__ d_logp,
+                                                         const float *__restrict__ d_entropy,
+                                                         uint32_t n, uint32_t v,
+                                                         float *__restrict__ scale,
+                                                         uint32_t *__restrict__ status) {
+  if (targets != nullptr) report_ids<kPrepare>(targets, n, v, status);
+  else if (threadIdx.x == 0) *status = 0u;
+  if (scale == nullptr) return;
+  float most = 0.0f;
+  for (uint32_t i = threadIdx.x; i < n; i += kPrepare) {
+    float x = d_logp != nullptr ? fabsf(d_logp[i]) : 0.0f;
+    if (d_entropy != nullptr) x += 17.0f * fabsf(d_entropy[i]);
+    most = x < kInf ? fmaxf(most, x) : most;
+  }
+  most = group_max<kWave>(most);
+  __shared__ float wave_most[kPrepare / kWave];
+  if (lane_id() == 0) wave_most[threadIdx.x / kWave] = most;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (uint32_t w = 1; w < kPrepare / kWave; ++w) most = fmaxf(most, wave_most[w]);
+  // most < 2^(e + 1); powers between 2^-100 and 2^100 keep both factors normal
+  int e = (int)((__float_as_uint(most) >> 23) & 255u) - 127;
+  e = most > 0.0f ? min(max(14 - e, -100), 100) : 0;
+  scale[0] = __uint_as_float((uint32_t)(e + 127) << 23);
+  scale[1] = __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
+// Epilogue of the backward's first product: d_z of a piece of the classes.
+template <class O>
+struct PutDz {
+  const float *bias;  // of the piece
+  const int32_t *targets;
+  const float *stats, *entropy, *d_logp, *d_entropy, *scale;
+  uint16_t *dz;
+  uint64_t ld, plane;
+  float *column_sums;  // [half tiles of rows][ld], or nullptr
+  uint32_t rows, n, first, classes;
+
+  template <uint32_t kTile, bool kGated, uint32_t kSub>
+  __device__ __forceinline__ void run(const Acc (&acc)[kSub][kSub], uint32_t row0, uint32_t col0,
+                                      uint32_t) const {
+    const uint32_t lane = lane_id();
+    float b[kSub][4], sum[kSub][4];
+    load_bias(bias, col0, n, b);
+#pragma unroll
+    for (uint32_t j = 0; j < kSub; ++j)
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e) sum[j][e] = 0.0f;
+    const float by = scale != nullptr ? scale[0] : 1.0f;
+#pragma unroll
+    for (uint32_t i = 0; i < kSub; ++i) {
+      const uint32_t row = row0 + outer_of(i, lane & 15);
+      const bool in_row = row < rows;
+      const uint32_t r = in_row ? row : rows - 1;
+      const float m = stats[2ull * r], ls = stats[2ull * r + 1];
+      const int32_t t = targets != nullptr ? targets[r] : -1;
+      const bool known = t >= 0 && (uint32_t)t < classes;
+      const uint32_t hit = known ? (uint32_t)t - first : ~0u;  // (another piece's is none here)
+      const float g = known && d_logp != nullptr ? d_logp[r] : 0.0f;
+      const float h = d_entropy != nullptr ? d_entropy[r] : 0.0f;
+      const float gh = d_entropy != nullptr ? g + h * entropy[r] : g;
+#pragma unroll
+      for (uint32_t j = 0; j < kSub; j += 2) {
+        const uint32_t at = outer_of(j, (lane / 16) * 4);
+        Row8 d;
+#pragma unroll
+        for (uint32_t e = 0; e < 8; ++e) {
+          const float z = logit(acc[i][j + e / 4][e & 3], b[j + e / 4][e & 3]);
+          const float lp = z - m - ls;
+          const float p = exp_neg(lp);
+          const float y = (col0 + at + e == hit ? g : 0.0f) - (p == 0.0f ? 0.0f : p * (gh + h * lp));
+          // masked: 0, but NaN in a row without a distribution
+          d[e] = z == -kInf && m == m ? 0.0f : y;
+          sum[j + e / 4][e & 3] += in_row ? d[e] : 0.0f;
+          d[e] *= by;
+        }
+        if (in_row && col0 + at < n) put_operand<O>(dz + row * ld + col0 + at, plane, d);
+      }
+    }
+    if (column_sums == nullptr) return;
+    float *const to = column_sums + (uint64_t)(row0 / (kTile / 2)) * ld;
+#pragma unroll
+    for (uint32_t j = 0; j < kSub; ++j) {
+      Acc s;
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e) s[e] = group_sum<16>(sum[j][e]);
+      const uint32_t col = col0 + outer_of(j, (lane / 16) * 4);
+      if ((lane & 15) == 0 && col < n) *reinterpret_cast<Acc *>(to + col) = s;
+    }
+  }
+};
+
+// A piece's part of d_x to f32, beside the pieces before.
+struct AddParts {
+  float *to;
+  uint32_t m, n, wide;
+  bool add;
+
+  template <uint32_t kTile, bool kGated, uint32_t kSub>
+  __device__ __forceinline__ void run(const Acc (&acc)[kSub][kSub], uint32_t row0, uint32_t col0,
+                                      uint32_t part) const {
+    const uint32_t lane = lane_id();
+#pragma unroll
+    for (uint32_t i = 0; i < kSub; ++i) {
+      const uint32_t row = row0 + outer_of(i, lane & 15);
+      if (row >= m) continue;
+      float *const at = to + ((uint64_t)part * m + row) * wide;
+#pragma unroll
+      for (uint32_t j = 0; j < kSub; j += 2) {
+        const uint32_t col = col0 + outer_of(j, (lane / 16) * 4);
+        if (col >= n) continue;
+        Row8 v = eight(acc[i][j], acc[i][j + 1]);
+        if (add) v += *reinterpret_cast<const Row8 *>(at + col);
+        *reinterpret_cast<Row8 *>(at + col) = v;
+      }
+    }
+  }
+};
+
+// Results of d_z times its scale to the caller's rows.
+template <class O>
+struct ToScaledRows {
+  O *out;
+  uint64_t ld;
+  uint32_t n;
+  const float *scale;  // or nullptr
+  __device__ __forceinline__ void operator()(uint32_t row, uint32_t col, Row8 v) const {
+    if (scale != nullptr) v *= scale[1];
+    store_pack_tail<O, 8>(out + row * ld, col, n, __builtin_convertvector(v, Pack<O, 8>));
+  }
+};
+
+// d_bias of a piece: the tiles' column sums, in order.
+__global__ __launch_bounds__(kThreads) void join_columns(const float *__restrict__ sums,
+                                                         uint32_t slices, uint64_t ld, uint32_t n,
+                                                         float *__restrict__ out) {
+  const uint32_t col = blockIdx.x * kThreads + threadIdx.x;
+  if (col >= n) return;
+  float a = 0.0f;
+#pragma unroll 8
+  for (uint32_t k = 0; k < slices; ++k) a += sums[k * ld + col];
+  out[col] = a;
+}
+
+template <class O>
+__global__ __launch_bounds__(kThreads) void zero_table(O *out, uint64_t ld, uint32_t v, uint32_t d,
+                                                       float *bias) {
+  for (uint64_t id = (uint64_t)blockIdx.x * kThreads + threadIdx.x; id < (uint64_t)v * d;
+       id += (uint64_t)gridDim.x * kThreads) {
+    const uint64_t row = id / d;
+    if (out != nullptr) out[row * ld + (id - row * d)] = (O)0.0f;
+    if (bias != nullptr && id - row * d == 0) bias[row] = 0.0f;
+  }
+}
+
+// Rows of one launch of the forward product: its slices' sums stay below this.
+constexpr uint64_t kSumsBytes = 512ull << 20;
+
+struct LossRoom {
+  Matrix x, table;
+  float *sums, *at_target;
+  Pack3 list = {};
+  Shape shape;
+  uint32_t rows;  // of a launch
+  size_t bytes;
+};
+
+LossRoom lay_out(const LossCall &c, bool x_stays, bool table_stays, void *ws) {
+  LossRoom r;
+  Room room{static_cast<char *>(ws)};
+  r.x = operand(c.x, c.dtype, c.x_ld, c.n, c.d, x_stays, room, r.list);
+  r.table = operand(c.table, c.dtype, c.table_ld, c.v, c.d, table_stays, room, r.list);
+  const uint64_t a_row = 3ull * 4 * 2 * div_up(c.v, 128);
+  uint64_t rows = kSumsBytes / a_row / 256 * 256;
+  if (rows < 4096) rows = 4096;
+  r.rows = rows < c.n ? (uint32_t)rows : c.n;
+  r.shape = plan_shape(r.rows, c.v, tiles_of(c.dtype, 1, up8(c.d)));
+  if (r.shape.parts > 1) r.shape = Shape{128, 1, tiles_of(c.dtype, 1, up8(c.d))};
+  r.sums = static_cast<float *>(
+      room.take((size_t)r.rows * 12 * 2 * div_up(c.v, r.shape.tile)));
+  r.at_target = static_cast<float *>(room.take((size_t)r.rows * 4));
+  r.bytes = room.used;
+  return r;
+}
+
+// Classes of a piece: d_z of one stays below this (and the rows' whole length
+// below that where they are few).
+constexpr uint64_t kPieceBytes = 256ull << 20;
+
+struct LossGradRoom {
+  Matrix x, table;
+  uint16_t *dz;
+  uint64_t dz_ld;
+  float *parts, *columns, *scale;
+  Pack3 list = {};
+  Shape z, dx, dt;
+  uint32_t piece;  // classes
+  size_t bytes;
+};
+
+LossGradRoom lay_out_grad(const LossGradCall &c, bool x_stays, bool table_stays, bool d_x, bool d_bias,
+                          void *ws) {
+  LossGradRoom r;
+  Room room{static_cast<char *>(ws)};
+  r.x = operand(c.x, c.dtype, c.x_ld, c.n, c.d, x_stays, room, r.list);
+  r.table = operand(c.table, c.dtype, c.table_ld, c.v, c.d, table_stays, room, r.list);
+  uint64_t piece = kPieceBytes / ((uint64_t)c.n * 2 * planes_of(c.dtype)) / 256 * 256;
+  if (piece < 256) piece = 256;
+  const uint32_t count = div_up(c.v, piece);
+  // pieces of equal size
+  piece = (div_up(c.v, count) + 255) / 256 * 256;
+  r.piece = piece < c.v ? (uint32_t)piece : c.v;
+  r.dz_ld = up8(r.piece);
+  r.dz = static_cast<uint16_t *>(room.take(matrix_bytes(c.dtype, c.n, r.piece)));
+  const uint32_t tiles = tiles_of(c.dtype, 1, up8(c.d));
+  r.z = plan_shape(c.n, r.piece, tiles);
+  if (r.z.parts > 1) r.z = Shape{128, 1, tiles};
+  r.dx = plan_shape(c.n, c.d, tiles_of(c.dtype, 1, up8(r.piece)));
+  r.dt = plan_shape(r.piece, c.d, tiles_of(c.dtype, 1, c.n));
+  const size_t a = d_x ? (size_t)r.dx.parts * c.n * up8(c.d) * 4 : 0;
+  const size_t b = parts_bytes(r.dt, r.piece, up8(c.d));
+  r.parts = static_cast<float *>(room.take(a));
+  r.columns = static_cast<float *>(room.take(b));
+  const size_t s = d_bias ? (size_t)div_up(c.n, r.z.tile) * 2 * r.dz_ld * 4 : 0;
+  // (the table's parts and the bias' sums are not there at the same time)
+  if (s > b) {
+    room.used -= align_up(b, 256);
+    r.columns = static_cast<float *>(room.take(s));
+  }
+  r.scale = static_cast<float *>(room.take(8));
+  r.bytes = room.used;
+  return r;
+}
+
+}  // namespace
+
+size_t loss_workspace(const LossCall &c, bool aligned) {
+  if (c.n == 0) return 0;
+  const bool s = aligned && c.dtype != 0u && c.d % 8 == 0;
+  return lay_out(c, s, s, nullptr).bytes;
+}
+
+size_t loss_need(const LossCall &c) {
+  if (c.n == 0) return 0;
+  return lay_out(c, in_place(c.x, c.dtype, c.x_ld, c.d), in_place(c.table, c.dtype, c.table_ld, c.d),
+                 nullptr)
+      .bytes;
+}
+
+hipError_t launch_loss(const LossCall &c, float *logp, float *entropy, float *stats, void *ws,
+                       uint32_t *status, hipStream_t stream) {
+  const LossRoom r =
+      c.n == 0 ? LossRoom{}
+               : lay_out(c, in_place(c.x, c.dtype, c.x_ld, c.d),
+                         in_place(c.table, c.dtype, c.table_ld, c.d), ws);
+  hipError_t e = launch_pack(r.list, c.dtype, stream);
+  const uint32_t d8 = up8(c.d);
+  for (uint64_t i = 0; e == hipSuccess && (i < c.n || i == 0); i += r.rows) {
+    const uint32_t rows = (uint32_t)(c.n - i < r.rows ? c.n - i : r.rows);
+    const uint32_t slices = rows == 0 ? 0 : 2 * div_up(c.v, r.shape.tile);
+    const int32_t *const targets = c.targets == nullptr ? nullptr : c.targets + i;
+    if (rows > 0) {
+      const uint64_t a_base[1] = {i * r.x.ld};
+      const Args g = make_args(c.dtype, r.x, r.table, rows, c.v, d8, d8, 1, a_base, nullptr, r.shape, c.v);
+      const RowSums sums = {c.bias, targets, r.sums, r.at_target, rows, c.v};
+      e = with_types(c.dtype, [&](auto, auto t) {
+        return launch_tiles<decltype(t), kAlongK, kAlongK, false>(g, r.shape, sums, stream);
+      });
+      if (e != hipSuccess) break;
+    }
+    join_rows<<<div_up(rows, 16) + 1, kThreads, 0, stream>>>(
+        r.sums, r.at_target, slices, rows, c.v, targets, logp == nullptr ? nullptr : logp + i,
+        entropy == nullptr ? nullptr : entropy + i, stats == nullptr ? nullptr : stats + 2 * i,
+        c.targets, c.targets == nullptr ? 0 : c.n, i == 0 ? status : nullptr);
+    e = hipGetLastError();
+    if (c.n == 0) break;
+  }
+  return e;
+}
+
+size_t loss_grad_workspace(const LossGradCall &c, bool aligned) {
+  if (c.n == 0) return 0;
+  const bool s = aligned && c.dtype != 0u && c.d % 8 == 0;
+  return lay_out_grad(c, s, s, true, true, nullptr).bytes;
+}
+
+size_t loss_grad_need(const LossGradCall &c, bool d_x, bool d_bias) {
+  if (c.n == 0) return 0;
+  return lay_out_grad(c, in_place(c.x, c.dtype, c.x_ld, c.d),
+                      in_place(c.table, c.dtype, c.table_ld, c.d), d_x, d_bias, nullptr)
+      .bytes;
+}
+
+hipError_t launch_loss_grad(const LossGradCall &c, void *d_x, uint64_t d_x_ld, void *d_table,
+                            uint64_t d_table_ld, float *d_bias, void *ws, uint32_t *status,
+                            hipStream_t stream) {
+  if (c.n == 0)
+    return with_type(c.dtype, [&](auto o) {
+      typedef decltype(o) O;
+      prepare_rows<<<1, kPrepare, 0, stream>>>(nullptr, nullptr, nullptr, 0, c.v, nullptr, status);
+      if (d_table != nullptr || d_bias != nullptr)
+        zero_table<O><<<1024, kThreads, 0, stream>>>(static_cast<O *>(d_table), d_table_ld, c.v, c.d,
+                                                     d_bias);
+      return hipGetLastError();
+    });
+  const LossGradRoom r = lay_out_grad(c, in_place(c.x, c.dtype, c.x_ld, c.d),
+                                      in_place(c.table, c.dtype, c.table_ld, c.d), d_x != nullptr,
+                                      d_bias != nullptr, ws);
+  hipError_t e = launch_pack(r.list, c.dtype, stream);
+  if (e != hipSuccess) return e;
+  const bool scaled = static_cast<Dtype>(c.dtype) == Dtype::f16;
+  float *const scale = scaled ? r.scale : nullptr;
+  prepare_rows<<<1, kPrepare, 0, stream>>>(c.targets, c.d_logp, c.d_entropy, c.n, c.v, scale, status);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const uint64_t plane = (uint64_t)c.n * r.dz_ld;
+  const Matrix dz = {r.dz, r.dz_ld, plane};
+  const uint32_t d8 = up8(c.d);
+  return with_types(c.dtype, [&](auto o, auto t) {
+    typedef decltype(o) O;
+    typedef decltype(t) T;
+    hipError_t rc = hipSuccess;
+    for (uint32_t first = 0; rc == hipSuccess && first < c.v; first += r.piece) {
+      const uint32_t n = c.v - first < r.piece ? c.v - first : r.piece;
+      const uint32_t n8 = up8(n);
+      const uint64_t t_base[1] = {first * r.table.ld};
+      {
+        const Args g = make_args(c.dtype, r.x, r.table, c.n, n, d8, d8, 1, nullptr, t_base, r.z, n);
+        const PutDz<O> put = {c.bias == nullptr ? nullptr : c.bias + first,
+                              c.targets,
+                              c.stats,
+                              c.entropy,
+                              c.d_logp,
+                              c.d_entropy,
+                              scale,
+                              r.dz,
+                              r.dz_ld,
+                              plane,
+                              d_bias == nullptr ? nullptr : r.columns,
+                              c.n,
+                              n,
+                              first,
+                              c.v};
+        rc = launch_tiles<T, kAlongK, kAlongK, false>(g, r.z, put, stream);
+        if (rc != hipSuccess) break;
+        if (d_bias != nullptr) {
+          const uint32_t slices = 2 * div_up(c.n, r.z.tile);
+          join_columns<<<div_up(n, kThreads), kThreads, 0, stream>>>(r.columns, slices, r.dz_ld, n,
+                                                                     d_bias + first);
+          if ((rc = hipGetLastError()) != hipSuccess) break;
+        }
+      }
+      if (d_x != nullptr) {
+        Shape s = r.dx;
+        const uint32_t tiles = tiles_of(c.dtype, 1, n8);
+        s.per_part = (tiles + s.parts - 1) / s.parts;
+        s.per_part += s.per_part & 1;
+        s.parts = (tiles + s.per_part - 1) / s.per_part;
+        const Args g = make_args(c.dtype, dz, r.table, c.n, c.d, n8, n, 1, nullptr, t_base, s, c.d);
+        const ToScaledRows<O> to = {static_cast<O *>(d_x), d_x_ld, c.d, scale};
+        if (r.piece >= c.v && r.dx.parts == 1) {
+          rc = launch_tiles<T, kAlongK, kAcrossK, false>(g, s, Each<ToScaledRows<O>>{to, c.n, c.d},
+                                                         stream);
+        } else {
+          rc = launch_tiles<T, kAlongK, kAcrossK, false>(
+              g, s, AddParts{r.parts, c.n, c.d, d8, first > 0}, stream);
+          if (rc == hipSuccess && first + n == c.v) {
+            const uint64_t chunks = (uint64_t)c.n * div_up(c.d, 8);
+            join_parts<false><<<div_up(chunks, kThreads), kThreads, 0, stream>>>(
+                r.parts, r.dx.parts, c.n, c.d, d8, to);
+            rc = hipGetLastError();
+          }
+        }
+        if (rc != hipSuccess) break;
+      }
+      if (d_table != nullptr) {
+        Shape s = r.dt;
+        const Args g = make_args(c.dtype, dz, r.x, n, c.d, c.n, c.n, 1, nullptr, nullptr, s, c.d);
+        rc = launch_product<T, kAcrossK, kAcrossK, false>(
+            g, s,
+            ToScaledRows<O>{static_cast<O *>(d_table) + first * d_table_ld, d_table_ld, c.d, scale},
+            r.columns, stream);
+      }
+    }
+    return rc;
+  });
+}
+
+}  // namespace seacells

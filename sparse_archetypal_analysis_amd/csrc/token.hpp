@@ -269,4 +269,51 @@ hipError_t launch_logprobs_grad(const void *logits, uint32_t dtype, uint32_t n, 
                                 void *d_logits, uint64_t d_logits_ld, uint32_t *status,
                                 hipStream_t stream);
 
+// Activations of the gated block, same values as SEACELLS_ACT_*.
+enum class Act : uint32_t { silu = 0, gelu = 1, relu = 2 };
+
+struct FfnCall {
+  uint32_t dtype;
+  Act act;
+  uint32_t n, d, f, m;
+  const void *x, *w_in, *w_out;
+  uint64_t x_ld, w_in_ld, w_out_ld;
+};
+struct FfnGradCall : FfnCall {
+  const void *d_out, *pre;
+  uint64_t d_out_ld, pre_ld;
+};
+// What any call of these sizes needs (aligned: with rows on 16 bytes), and
+// what this one does.
+size_t ffn_workspace(const FfnCall &call, bool aligned);
+size_t ffn_need(const FfnCall &call);
+hipError_t launch_ffn(const FfnCall &call, void *out, uint64_t out_ld, void *pre, uint64_t pre_ld,
+                      void *ws, hipStream_t stream);
+size_t ffn_grad_workspace(const FfnGradCall &call, bool aligned);
+size_t ffn_grad_need(const FfnGradCall &call);
+hipError_t launch_ffn_grad(const FfnGradCall &call, void *d_x, uint64_t d_x_ld, void *d_w_in,
+                           uint64_t d_w_in_ld, void *d_w_out, uint64_t d_w_out_ld, void *ws,
+                           hipStream_t stream);
+
+struct LossCall {
+  uint32_t dtype;
+  uint32_t n, d, v;
+  const void *x, *table;
+  uint64_t x_ld, table_ld;
+  const float *bias;  // or nullptr
+  const int32_t *targets;
+};
+struct LossGradCall : LossCall {
+  const float *stats, *entropy, *d_logp, *d_entropy;
+};
+size_t loss_workspace(const LossCall &call, bool aligned);
+size_t loss_need(const LossCall &call);
+hipError_t launch_loss(const LossCall &call, float *logp, float *entropy, float *stats, void *ws,
+                       uint32_t *status, hipStream_t stream);
+size_t loss_grad_workspace(const LossGradCall &call, bool aligned);
+size_t loss_grad_need(const LossGradCall &call, bool d_x, bool d_bias);
+hipError_t launch_loss_grad(const LossGradCall &call, void *d_x, uint64_t d_x_ld, void *d_table,
+                            uint64_t d_table_ld, float *d_bias, void *ws, uint32_t *status,
+                            hipStream_t stream);
+
 }  // namespace seacells

@@ -38,6 +38,10 @@ EXPORTS = ("seacells_fw_a_columns_workspace", "seacells_fw_a_columns",
            "seacells_embed", "seacells_embed_grad_workspace", "seacells_embed_grad",
            "seacells_layer_norm", "seacells_layer_norm_grad_workspace", "seacells_layer_norm_grad",
            "seacells_logprobs_workspace", "seacells_logprobs", "seacells_logprobs_grad",
+           "seacells_gated_ffn_workspace", "seacells_gated_ffn",
+           "seacells_gated_ffn_grad_workspace", "seacells_gated_ffn_grad",
+           "seacells_linear_logprobs_workspace", "seacells_linear_logprobs",
+           "seacells_linear_logprobs_grad_workspace", "seacells_linear_logprobs_grad",
            "seacells_debug_set_a_options", "seacells_debug_b_layout",
            "seacells_debug_b_last_epoch", "seacells_debug_b_reduce", "seacells_debug_embed_plan",
            "seacells_fw_step_size",
@@ -177,6 +181,26 @@ def load():
     lib.seacells_logprobs_grad.restype = ctypes.c_int
     lib.seacells_logprobs_grad.argtypes = [_VP, _U32, _U32, _U32, _U64, _VP, _VP, _VP, _VP, _VP, _VP,
                                            _U64, _VP, _VP]
+    for name in ("seacells_gated_ffn_workspace", "seacells_gated_ffn_grad_workspace"):
+        getattr(lib, name).restype = _SIZE
+        getattr(lib, name).argtypes = [_U32] * 6
+    lib.seacells_gated_ffn.restype = ctypes.c_int
+    lib.seacells_gated_ffn.argtypes = [_VP, _U32, _U32, _U32, _U64, _VP, _U64, _U32, _VP, _U64, _U32, _U32,
+                                       _VP, _U64, _VP, _U64, _VP, _SIZE, _VP]
+    lib.seacells_gated_ffn_grad.restype = ctypes.c_int
+    lib.seacells_gated_ffn_grad.argtypes = [_VP, _U64, _VP, _U32, _U32, _U32, _U64, _VP, _U64, _VP, _U64,
+                                            _U32, _VP, _U64, _U32, _U32, _VP, _U64, _VP, _U64, _VP, _U64,
+                                            _VP, _SIZE, _VP]
+    for name in ("seacells_linear_logprobs_workspace", "seacells_linear_logprobs_grad_workspace"):
+        getattr(lib, name).restype = _SIZE
+        getattr(lib, name).argtypes = [_U32] * 5
+    lib.seacells_linear_logprobs.restype = ctypes.c_int
+    lib.seacells_linear_logprobs.argtypes = [_VP, _U32, _U32, _U32, _U64, _VP, _U64, _U32, _VP, _VP, _VP,
+                                             _VP, _VP, _VP, _SIZE, _VP, _VP]
+    lib.seacells_linear_logprobs_grad.restype = ctypes.c_int
+    lib.seacells_linear_logprobs_grad.argtypes = [_VP, _U32, _U32, _U32, _U64, _VP, _U64, _U32, _VP, _VP,
+                                                  _VP, _VP, _VP, _VP, _VP, _U64, _VP, _U64, _VP, _VP,
+                                                  _SIZE, _VP, _VP]
     lib.seacells_debug_set_a_options.restype = ctypes.c_int
     lib.seacells_debug_set_a_options.argtypes = [ctypes.POINTER(seacells_a_options)]
     lib.seacells_debug_b_layout.restype = ctypes.c_int
@@ -1228,3 +1252,221 @@ def seacells_logprobs_grad(logits, targets, stats, entropy=None, d_logp=None, d_
              _vector(d_entropy, "d_entropy", n, dev, torch.float32), d_logits.data_ptr(), d_ld,
              _vector(status, "status", 1, dev, torch.int32))
     return d_logits, status
+
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}  # SEACELLS_ACT_*
+
+
+def _code(dtype):
+    if dtype not in _DTYPES:
+        raise SeacellsError("float32, float16 or bfloat16, not %s" % dtype)
+    return _DTYPES[dtype]
+
+
+def _act(act):
+    if act not in ACTIVATIONS:
+        raise SeacellsError("act must be one of %s" % ", ".join(ACTIVATIONS))
+    return ACTIVATIONS[act]
+
+
+def _on_16_bytes(f, *operands):
+    """Whether the products can take (pointer, row stride, element size)
+    operands where they are; the second one's rows go by pairs f rows apart."""
+    if any(p % 16 or ld * e % 16 or ld >= 1 << 22 for p, ld, e in operands):
+        return False
+    return f == 0 or (f + 256) * operands[1][1] < 1 << 30
+
+
+def _same(t, name, n, d, dev, dtype):
+    """The row stride of an operand that has to be [n, d] of dtype."""
+    tn, td, ld, _ = _rows(t, name, dev)
+    if td != d or t.dtype != dtype or (n is not None and tn != n):
+        raise SeacellsError("%s must be [%s, %d] of %s" % (name, "rows" if n is None else n, d, dtype))
+    return ld
+
+
+def _ffn_operands(x, w_in, w_out):
+    n, d, x_ld, dev = _rows(x, "x")
+    dt = x.dtype
+    m, f, out_ld, _ = _rows(w_out, "w_out", dev)
+    if w_out.dtype != dt:
+        raise SeacellsError("w_out must be of x's type")
+    in_ld = _same(w_in, "w_in", 2 * f, d, dev, dt)
+    return n, d, f, m, x_ld, in_ld, out_ld, dt, dev
+
+
+def seacells_gated_ffn_workspace(dtype, n, d, f, m, on_16_bytes=False) -> int:
+    """Bytes for seacells_gated_ffn; on_16_bytes: every operand starts on 16
+    bytes and so does every row of it (without: room for copies)."""
+    return _query(load().seacells_gated_ffn_workspace, _code(dtype), n, d, f, m, int(on_16_bytes))
+
+
+def seacells_gated_ffn(x, w_in, w_out, act="silu", out=None, pre=None, workspace=None, stream=None):
+    """Gated feed-forward block: pre = x w_in^T, h = act(pre[..., :f]) *
+    pre[..., f:], out = h w_out^T. Returns (out [..., m], pre [..., 2f]).
+
+    x [..., d]; w_in [2f, d], f gate rows, then f up rows; w_out [m, f]; all of
+    one type. act: "silu", "gelu" or "relu". pre is what the gradient needs;
+    False leaves it out (returned as None).
+    """
+    lib = load()
+    n, d, f, m, x_ld, in_ld, wo_ld, dt, dev = _ffn_operands(x, w_in, w_out)
+    code = _act(act)
+    if out is None:
+        out = _new((*x.shape[:-1], m), dt, dev, stream)
+    out_ld = _out_rows(out, "out", n, m, dev, dt)
+    pre_ld = 2 * f
+    if pre is False:
+        pre = None
+    else:
+        if pre is None:
+            pre = _new((*x.shape[:-1], 2 * f), dt, dev, stream)
+        pre_ld = _out_rows(pre, "pre", n, 2 * f, dev, dt)
+    px, pi, po = x.data_ptr(), w_in.data_ptr(), w_out.data_ptr()
+    if workspace is None:
+        e = x.element_size()
+        size = lib.seacells_gated_ffn_workspace(
+            _DTYPES[dt], n, d, f, m, _on_16_bytes(f, (px, x_ld, e), (pi, in_ld, e), (po, wo_ld, e)))
+        workspace = _new(max(size, 1), torch.uint8, dev, stream)
+    ws, ws_bytes, keep = _workspace(workspace, 1, dev, stream)
+    _enqueue(lib.seacells_gated_ffn, dev, stream, px, _DTYPES[dt], n, d, x_ld, pi, in_ld, f, po, wo_ld, m,
+             code, out.data_ptr(), out_ld, None if pre is None else pre.data_ptr(), pre_ld, ws, ws_bytes)
+    return out, pre
+
+
+def seacells_gated_ffn_grad_workspace(dtype, n, d, f, m, on_16_bytes=False) -> int:
+    return _query(load().seacells_gated_ffn_grad_workspace, _code(dtype), n, d, f, m, int(on_16_bytes))
+
+
+def _wanted(t, name, shape, n, d, dev, dtype, stream):
+    """(tensor or None, pointer, row stride) of a gradient that False leaves out."""
+    if t is False:
+        return None, None, d
+    if t is None:
+        t = _new(shape, dtype, dev, stream)
+    ld = _out_rows(t, name, n, d, dev, dtype)
+    return t, t.data_ptr(), ld
+
+
+def seacells_gated_ffn_grad(d_out, x, pre, w_in, w_out, act="silu", d_x=None, d_w_in=None,
+                            d_w_out=None, workspace=None, stream=None):
+    """Gradients of seacells_gated_ffn from the pre that it returned. Returns
+    (d_x, d_w_in, d_w_out), of x's type; False leaves one out (None).
+    """
+    lib = load()
+    n, d, f, m, x_ld, in_ld, wo_ld, dt, dev = _ffn_operands(x, w_in, w_out)
+    code = _act(act)
+    dy_ld = _same(d_out, "d_out", n, m, dev, dt)
+    pre_ld = _same(pre, "pre", n, 2 * f, dev, dt)
+    d_x, pdx, dx_ld = _wanted(d_x, "d_x", x.shape, n, d, dev, dt, stream)
+    d_w_in, pdi, di_ld = _wanted(d_w_in, "d_w_in", (2 * f, d), 2 * f, d, dev, dt, stream)
+    d_w_out, pdo, do_ld = _wanted(d_w_out, "d_w_out", (m, f), m, f, dev, dt, stream)
+    px, pi, po, py = x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), d_out.data_ptr()
+    if workspace is None:
+        e = x.element_size()
+        size = lib.seacells_gated_ffn_grad_workspace(
+            _DTYPES[dt], n, d, f, m,
+            _on_16_bytes(f, (px, x_ld, e), (pi, in_ld, e), (po, wo_ld, e), (py, dy_ld, e)))
+        workspace = _new(max(size, 1), torch.uint8, dev, stream)
+    ws, ws_bytes, keep = _workspace(workspace, 1, dev, stream)
+    _enqueue(lib.seacells_gated_ffn_grad, dev, stream, py, dy_ld, px, _DTYPES[dt], n, d, x_ld,
+             pre.data_ptr(), pre_ld, pi, in_ld, f, po, wo_ld, m, code, pdx, dx_ld, pdi, di_ld, pdo, do_ld,
+             ws, ws_bytes)
+    return d_x, d_w_in, d_w_out
+
+
+def _head_operands(x, table, bias, targets):
+    n, d, x_ld, dev = _rows(x, "x")
+    dt = x.dtype
+    v, t_d, t_ld, _ = _rows(table, "table", dev)
+    if t_d != d or table.dtype != dt:
+        raise SeacellsError("table must have rows of %d elements of %s" % (d, dt))
+    return (n, d, v, x_ld, t_ld, dt, dev, _vector(bias, "bias", v, dev, torch.float32),
+            _vector(targets, "targets", n, dev, torch.int32))
+
+
+def seacells_linear_logprobs_workspace(dtype, n, d, v, on_16_bytes=False) -> int:
+    return _query(load().seacells_linear_logprobs_workspace, _code(dtype), n, d, v, int(on_16_bytes))
+
+
+def seacells_linear_logprobs(x, table, targets=None, bias=None, logp=None, entropy=None, stats=None,
+                             workspace=None, status=None, stream=None):
+    """Log probabilities of the target classes and entropies of hidden rows x
+    [..., d] over the classes of table [v, d], z = x table^T + bias, without
+    the logits in memory.
+
+    Returns (logp, entropy, stats, status): logp (None without targets) and
+    entropy of one float32 per row, stats [..., 2] (row maximum, log sum
+    exp(z - maximum)). targets int32, negative: ignored (logp 0). bias float32
+    [v]; -inf masks a class.
+    """
+    lib = load()
+    n, d, v, x_ld, t_ld, dt, dev, b, tgt = _head_operands(x, table, bias, targets)
+    lead = x.shape[:-1]
+    if targets is None:
+        logp = None
+    elif logp is None:
+        logp = _new(lead, torch.float32, dev, stream)
+    if entropy is None:
+        entropy = _new(lead, torch.float32, dev, stream)
+    if stats is None:
+        stats = _new((*lead, 2), torch.float32, dev, stream)
+    if status is None:
+        status = _new(1, torch.int32, dev, stream)
+    px, pt = x.data_ptr(), table.data_ptr()
+    if workspace is None:
+        e = x.element_size()
+        size = lib.seacells_linear_logprobs_workspace(_DTYPES[dt], n, d, v,
+                                                      _on_16_bytes(0, (px, x_ld, e), (pt, t_ld, e)))
+        workspace = _new(max(size, 1), torch.uint8, dev, stream)
+    ws, ws_bytes, keep = _workspace(workspace, 1, dev, stream)
+    _enqueue(lib.seacells_linear_logprobs, dev, stream, px, _DTYPES[dt], n, d, x_ld, pt, t_ld, v, b, tgt,
+             _vector(logp, "logp", n, dev, torch.float32),
+             _vector(entropy, "entropy", n, dev, torch.float32),
+             _vector(stats, "stats", 2 * n, dev, torch.float32), ws, ws_bytes,
+             _vector(status, "status", 1, dev, torch.int32))
+    return logp, entropy, stats, status
+
+
+def seacells_linear_logprobs_grad_workspace(dtype, n, d, v, on_16_bytes=False) -> int:
+    return _query(load().seacells_linear_logprobs_grad_workspace, _code(dtype), n, d, v,
+                  int(on_16_bytes))
+
+
+def seacells_linear_logprobs_grad(x, table, targets, stats, entropy=None, d_logp=None,
+                                  d_entropy=None, bias=None, d_x=None, d_table=None, d_bias=None,
+                                  workspace=None, status=None, stream=None):
+    """Gradients of sum(d_logp * logp + d_entropy * entropy). Returns (d_x,
+    d_table, d_bias, status): d_x and d_table of x's type, d_bias float32 (None
+    without a bias); False leaves one out (None).
+
+    stats and entropy as seacells_linear_logprobs returned them (entropy only
+    with d_entropy); targets may be None (no part of d_logp).
+    """
+    lib = load()
+    n, d, v, x_ld, t_ld, dt, dev, b, tgt = _head_operands(x, table, bias, targets)
+    d_x, pdx, dx_ld = _wanted(d_x, "d_x", x.shape, n, d, dev, dt, stream)
+    d_table, pdt, dt_ld = _wanted(d_table, "d_table", (v, d), v, d, dev, dt, stream)
+    if d_bias is False or (bias is None and d_bias is None):
+        d_bias = None
+    elif d_bias is None:
+        d_bias = _new(v, torch.float32, dev, stream)
+    if d_entropy is not None and entropy is None:
+        raise SeacellsError("d_entropy needs the entropies")
+    if status is None:
+        status = _new(1, torch.int32, dev, stream)
+    px, pt = x.data_ptr(), table.data_ptr()
+    if workspace is None:
+        e = x.element_size()
+        size = lib.seacells_linear_logprobs_grad_workspace(
+            _DTYPES[dt], n, d, v, _on_16_bytes(0, (px, x_ld, e), (pt, t_ld, e)))
+        workspace = _new(max(size, 1), torch.uint8, dev, stream)
+    ws, ws_bytes, keep = _workspace(workspace, 1, dev, stream)
+    _enqueue(lib.seacells_linear_logprobs_grad, dev, stream, px, _DTYPES[dt], n, d, x_ld, pt, t_ld, v, b,
+             tgt, _vector(stats, "stats", 2 * n, dev, torch.float32),
+             _vector(entropy, "entropy", n, dev, torch.float32),
+             _vector(d_logp, "d_logp", n, dev, torch.float32),
+             _vector(d_entropy, "d_entropy", n, dev, torch.float32), pdx, dx_ld, pdt, dt_ld,
+             _vector(d_bias, "d_bias", v, dev, torch.float32), ws, ws_bytes,
+             _vector(status, "status", 1, dev, torch.int32))
+    return d_x, d_table, d_bias, status
