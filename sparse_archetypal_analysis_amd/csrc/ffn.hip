@@ -16,58 +16,13 @@
 // f32.
 #include <type_traits>
 
+#include "few.hpp"
 #include "mm.hpp"
 
 namespace seacells {
 namespace {
 
 using namespace mm;
-
-// 1 / (1 + e^-g), from e^-|g| so that neither end overflows.
-__device__ __forceinline__ float sigmoid(float g) {
-  const float e = exp_neg(-fabsf(g));
-  const float r = __builtin_amdgcn_rcpf(1.0f + e);
-  return g >= 0.0f ? r : e * r;
-}
-
-// The normal distribution's integral and density (times sqrt(2 pi)) at g:
-// erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2), t = 1 / (1 + p x), to 1.5e-7
-// (Abramowitz and Stegun, 7.1.26), mirrored for g > 0.
-__device__ __forceinline__ float normal(float g, float *density) {
-  const float x = fabsf(g) * 0.70710678118654752440f;
-  const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
-  const float e = exp_neg(-x * x);
-  const float q = ((((1.061405429f * t - 1.453152027f) * t + 1.421413741f) * t - 0.284496736f) * t +
-                   0.254829592f) * t * (0.5f * e);
-  *density = e;
-  return g >= 0.0f ? 1.0f - q : q;
-}
-
-// act(g) and act'(g). NaN stays NaN.
-template <Act kAct>
-__device__ __forceinline__ float act(float g) {
-  if (kAct == Act::silu) return g * sigmoid(g);
-  float e;
-  if (kAct == Act::gelu) return g * normal(g, &e);
-  return g <= 0.0f ? 0.0f : g;
-}
-
-template <Act kAct>
-__device__ __forceinline__ void act_both(float g, float *a, float *da) {
-  if (kAct == Act::silu) {
-    const float s = sigmoid(g);
-    *a = g * s;
-    *da = s + *a * (1.0f - s);
-  } else if (kAct == Act::gelu) {
-    float e;
-    const float p = normal(g, &e);
-    *a = g * p;
-    *da = p + g * 0.39894228040143267794f * e;
-  } else {
-    *a = act<Act::relu>(g);
-    *da = g > 0.0f ? 1.0f : (g <= 0.0f ? 0.0f : g);
-  }
-}
 
 // Gate and up results to pre (where it is kept) and h. Columns behind f are
 // products with zeros: h's row ends in zeros, as its own product needs.
@@ -78,20 +33,21 @@ struct PutGated {
   uint16_t *h;
   uint64_t h_ld, plane;
   uint32_t f;
-  __device__ __forceinline__ void operator()(uint32_t row, uint32_t col, Row8 g, Row8 u) const {
+  template <bool kWhole>
+  __device__ __forceinline__ void put(uint32_t row, uint32_t col, Row8 g, Row8 u) const {
     if (pre != nullptr) {
       O *const at = pre + row * pre_ld;
-      store_pack_tail<O, 8>(at, col, f, __builtin_convertvector(g, Pack<O, 8>));
-      store_pack_tail<O, 8>(at + f, col, f, __builtin_convertvector(u, Pack<O, 8>));
+      put_row<kWhole>(at, col, f, g);
+      put_row<kWhole>(at + f, col, f, u);
     }
     Row8 v;
 #pragma unroll
-    for (uint32_t e = 0; e < 8; ++e) v[e] = col + e < f ? act<kAct>(g[e]) * u[e] : 0.0f;
+    for (uint32_t e = 0; e < 8; ++e) v[e] = kWhole || col + e < f ? act<kAct>(g[e]) * u[e] : 0.0f;
     put_operand<O>(h + row * h_ld + col, plane, v);
   }
 };
 
-// dh to d_pre (its up half f8 columns behind the gate's) and h.
+// dh to d_pre (its up half ld columns behind the gate's) and h.
 template <class O, Act kAct>
 struct PutPre {
   const O *pre;
@@ -99,9 +55,10 @@ struct PutPre {
   uint16_t *d_pre, *h;
   uint64_t ld, d_plane, h_plane;  // ld: h's; d_pre's is twice that
   uint32_t f;
-  __device__ __forceinline__ void operator()(uint32_t row, uint32_t col, Row8 dh) const {
+  template <bool kWhole>
+  __device__ __forceinline__ void put(uint32_t row, uint32_t col, Row8 dh) const {
     const O *const at = pre + row * pre_ld;
-    const bool whole = col + 8 <= f;
+    const bool whole = kWhole || col + 8 <= f;
     Row8 g, u;
     if (whole) {
       g = __builtin_convertvector(*reinterpret_cast<const Pack<O, 8> *>(at + col), Row8);
@@ -131,18 +88,17 @@ struct PutPre {
   }
 };
 
-// Rows of [gate columns, up columns] of d_pre (f8 each) to W_in's rows.
+// Rows of [gate columns, up columns] of d_pre (`apart` each) to W_in's rows.
 template <class O>
 struct ToGatedRows {
   O *out;
   uint64_t ld;
-  uint32_t n, f, f8;
-  __device__ __forceinline__ void operator()(uint32_t row, uint32_t col, Row8 v) const {
-    const bool up = row >= f8;
-    const uint32_t in = up ? row - f8 : row;
-    if (in >= f) return;
-    store_pack_tail<O, 8>(out + (uint64_t)(up ? f + in : in) * ld, col, n,
-                          __builtin_convertvector(v, Pack<O, 8>));
+  uint32_t n, f, apart;
+  template <bool kWhole>
+  __device__ __forceinline__ void put(uint32_t row, uint32_t col, Row8 v) const {
+    const bool up = row >= apart;
+    const uint32_t in = up ? row - apart : row;
+    if (in < f) put_row<kWhole>(out + (uint64_t)(up ? f + in : in) * ld, col, n, v);
   }
 };
 
@@ -194,19 +150,19 @@ struct GradRoom {
 GradRoom lay_out_grad(const FfnGradCall &c, const bool stays[4], void *ws) {
   GradRoom r;
   Room room{static_cast<char *>(ws)};
-  const uint32_t f8 = up8(c.f);
+  const uint32_t f8 = up8(c.f), wide = up64(c.f);
   r.x = operand(c.x, c.dtype, c.x_ld, c.n, c.d, stays[0], room, r.list);
   r.d_out = operand(c.d_out, c.dtype, c.d_out_ld, c.n, c.m, stays[1], room, r.list);
   r.w_in = operand(c.w_in, c.dtype, c.w_in_ld, 2 * c.f, c.d, stays[2], room, r.list);
   r.w_out = operand(c.w_out, c.dtype, c.w_out_ld, c.m, c.f, stays[3], room, r.list);
   r.h = static_cast<uint16_t *>(room.take(matrix_bytes(c.dtype, c.n, c.f)));
-  r.d_pre = static_cast<uint16_t *>(room.take(matrix_bytes(c.dtype, c.n, 2 * f8)));
+  r.d_pre = static_cast<uint16_t *>(room.take(matrix_bytes(c.dtype, c.n, 2 * wide)));
   r.dh = plan_shape(c.n, c.f, tiles_of(c.dtype, 1, up8(c.m)));
   r.dx = plan_shape(c.n, c.d, tiles_of(c.dtype, 2, f8));
-  r.d_in = plan_shape(2ull * f8, c.d, tiles_of(c.dtype, 1, c.n));
+  r.d_in = plan_shape(2ull * wide, c.d, tiles_of(c.dtype, 1, c.n));
   r.d_out_w = plan_shape(c.m, c.f, tiles_of(c.dtype, 1, c.n));
   size_t most = parts_bytes(r.dh, c.n, f8);
-  const size_t more[3] = {parts_bytes(r.dx, c.n, up8(c.d)), parts_bytes(r.d_in, 2ull * f8, up8(c.d)),
+  const size_t more[3] = {parts_bytes(r.dx, c.n, up8(c.d)), parts_bytes(r.d_in, 2ull * wide, up8(c.d)),
                           parts_bytes(r.d_out_w, c.m, f8)};
   for (size_t b : more) most = b > most ? b : most;
   r.parts = static_cast<float *>(room.take(most));
@@ -226,14 +182,21 @@ __global__ __launch_bounds__(kThreads) void zero_rows(O *out, uint64_t ld, uint6
 
 }  // namespace
 
+// Few rows: h alone.
+static size_t few_bytes(const FfnCall &c) {
+  return align_up((size_t)c.n * c.f * dtype_size(c.dtype), 256);
+}
+
 size_t ffn_workspace(const FfnCall &c, bool aligned) {
   if (c.n == 0) return 0;
+  if (c.n <= kFewRows) return few_bytes(c);
   const bool s = aligned && c.dtype != 0u;
   return lay_out(c, s && c.d % 8 == 0, s && c.d % 8 == 0, s && c.f % 8 == 0, nullptr).bytes;
 }
 
 size_t ffn_need(const FfnCall &c) {
   if (c.n == 0) return 0;
+  if (c.n <= kFewRows) return few_bytes(c);
   return lay_out(c, in_place(c.x, c.dtype, c.x_ld, c.d), in_place(c.w_in, c.dtype, c.w_in_ld, c.d, c.f),
                  in_place(c.w_out, c.dtype, c.w_out_ld, c.f), nullptr)
       .bytes;
@@ -242,21 +205,28 @@ size_t ffn_need(const FfnCall &c) {
 hipError_t launch_ffn(const FfnCall &c, void *out, uint64_t out_ld, void *pre, uint64_t pre_ld,
                       void *ws, hipStream_t stream) {
   if (c.n == 0) return hipSuccess;
+  if (c.n <= kFewRows) {
+    const FewProduct in = {c.x, c.w_in, ws, pre, c.x_ld, c.w_in_ld, c.f, pre_ld, c.n, c.d, c.f, c.act};
+    const hipError_t e = launch_few_product(in, true, c.dtype, stream);
+    if (e != hipSuccess) return e;
+    const FewProduct up = {ws, c.w_out, out, nullptr, c.f, c.w_out_ld, out_ld, 0, c.n, c.f, c.m, c.act};
+    return launch_few_product(up, false, c.dtype, stream);
+  }
   const FfnRoom r =
       lay_out(c, in_place(c.x, c.dtype, c.x_ld, c.d), in_place(c.w_in, c.dtype, c.w_in_ld, c.d, c.f),
               in_place(c.w_out, c.dtype, c.w_out_ld, c.f), ws);
   hipError_t e = launch_pack(r.list, c.dtype, stream);
   if (e != hipSuccess) return e;
-  const uint32_t f8 = up8(c.f), d8 = up8(c.d);
-  const uint64_t plane = (uint64_t)c.n * f8;
-  const Matrix h = {r.h, f8, plane};
+  const uint32_t f8 = up8(c.f), d8 = up8(c.d), wide = up64(c.f);
+  const uint64_t plane = (uint64_t)c.n * wide;
+  const Matrix h = {r.h, wide, plane};
   return with_types(c.dtype, [&](auto o, auto t) {
     typedef decltype(o) O;
     typedef decltype(t) T;
     hipError_t rc = with_act(c.act, [&](auto a) {
       const Args g = make_args(c.dtype, r.x, r.w_in, c.n, c.f, d8, d8, 1, nullptr, nullptr, r.in,
                                2 * c.f);
-      const PutGated<O, decltype(a)::value> put = {static_cast<O *>(pre), pre_ld, r.h, f8, plane, c.f};
+      const PutGated<O, decltype(a)::value> put = {static_cast<O *>(pre), pre_ld, r.h, wide, plane, c.f};
       return launch_product<T, kAlongK, kAlongK, true>(g, r.in, put, r.parts, stream);
     });
     if (rc != hipSuccess) return rc;
@@ -290,7 +260,7 @@ size_t ffn_grad_need(const FfnGradCall &c) {
 hipError_t launch_ffn_grad(const FfnGradCall &c, void *d_x, uint64_t d_x_ld, void *d_w_in,
                            uint64_t d_w_in_ld, void *d_w_out, uint64_t d_w_out_ld, void *ws,
                            hipStream_t stream) {
-  const uint32_t f8 = up8(c.f), m8 = up8(c.m);
+  const uint32_t f8 = up8(c.f), m8 = up8(c.m), wide = up64(c.f);
   if (c.n == 0)
     return with_type(c.dtype, [&](auto o) {
       typedef decltype(o) O;
@@ -305,8 +275,8 @@ hipError_t launch_ffn_grad(const FfnGradCall &c, void *d_x, uint64_t d_x_ld, voi
   const GradRoom r = lay_out_grad(c, stays, ws);
   hipError_t e = launch_pack(r.list, c.dtype, stream);
   if (e != hipSuccess) return e;
-  const uint64_t h_plane = (uint64_t)c.n * f8, d_plane = 2 * h_plane;
-  const Matrix h = {r.h, f8, h_plane}, d_pre = {r.d_pre, 2ull * f8, d_plane};
+  const uint64_t h_plane = (uint64_t)c.n * wide, d_plane = 2 * h_plane;
+  const Matrix h = {r.h, wide, h_plane}, d_pre = {r.d_pre, 2ull * wide, d_plane};
   return with_types(c.dtype, [&](auto o, auto t) {
     typedef decltype(o) O;
     typedef decltype(t) T;
@@ -314,20 +284,20 @@ hipError_t launch_ffn_grad(const FfnGradCall &c, void *d_x, uint64_t d_x_ld, voi
       const Args g = make_args(c.dtype, r.d_out, r.w_out, c.n, c.f, m8, c.m, 1, nullptr, nullptr,
                                r.dh, c.f);
       const PutPre<O, decltype(a)::value> put = {static_cast<const O *>(c.pre), c.pre_ld, r.d_pre,
-                                                 r.h,  f8,  d_plane, h_plane, c.f};
+                                                 r.h,  wide, d_plane, h_plane, c.f};
       return launch_product<T, kAlongK, kAcrossK, false>(g, r.dh, put, r.parts, stream);
     });
     if (rc == hipSuccess && d_x != nullptr) {
-      const uint64_t a_base[2] = {0, f8}, b_base[2] = {0, (uint64_t)c.f * r.w_in.ld};
+      const uint64_t a_base[2] = {0, wide}, b_base[2] = {0, (uint64_t)c.f * r.w_in.ld};
       const Args g = make_args(c.dtype, d_pre, r.w_in, c.n, c.d, f8, c.f, 2, a_base, b_base, r.dx, c.d);
       rc = launch_product<T, kAlongK, kAcrossK, false>(
           g, r.dx, ToRows<O>{static_cast<O *>(d_x), d_x_ld, c.d}, r.parts, stream);
     }
     if (rc == hipSuccess && d_w_in != nullptr) {
-      const Args g = make_args(c.dtype, d_pre, r.x, 2 * f8, c.d, c.n, c.n, 1, nullptr, nullptr, r.d_in,
+      const Args g = make_args(c.dtype, d_pre, r.x, 2 * wide, c.d, c.n, c.n, 1, nullptr, nullptr, r.d_in,
                                c.d);
       rc = launch_product<T, kAcrossK, kAcrossK, false>(
-          g, r.d_in, ToGatedRows<O>{static_cast<O *>(d_w_in), d_w_in_ld, c.d, c.f, f8}, r.parts,
+          g, r.d_in, ToGatedRows<O>{static_cast<O *>(d_w_in), d_w_in_ld, c.d, c.f, wide}, r.parts,
           stream);
     }
     if (rc == hipSuccess && d_w_out != nullptr) {

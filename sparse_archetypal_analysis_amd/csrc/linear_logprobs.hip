@@ -11,6 +11,7 @@
 // figures, to a buffer of one piece (16 bits; f32: three bf16), then
 // d_table's rows of the piece, finished, and the piece's part of d_x, kept in
 // f32 between pieces. d_bias is summed from d_z before its rounding.
+#include "few.hpp"
 #include "mm.hpp"
 
 namespace seacells {
@@ -18,49 +19,32 @@ namespace {
 
 using namespace mm;
 
-constexpr float kInf = __builtin_huge_valf();
+// z of a lane's results in one row: with the bias, -inf for masked classes
+// (whatever their rows hold) and behind the last class. kPlain: no bias, and
+// the wave's columns are all there.
+template <bool kPlain, uint32_t kSub>
+struct Logits {
+  float bias[kPlain ? 1 : kSub][4];
 
-// What a row's figures are made of: maximum, sum e^(z - m), sum (z - m) e^(z - m).
-struct Sums {
-  float m, s, u;
+  __device__ __forceinline__ void load(const float *from, uint32_t col0, uint32_t n) {
+    if (kPlain) return;
+#pragma unroll
+    for (uint32_t j = 0; j < kSub; ++j) {
+      const uint32_t col = col0 + outer_of(j, (lane_id() / 16) * 4);
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e) {
+        const float b = from != nullptr ? from[min(col + e, n - 1)] : 0.0f;
+        bias[j][e] = col + e < n ? b : -kInf;
+      }
+    }
+  }
+  __device__ __forceinline__ float of(const Acc &acc, uint32_t j, uint32_t e) const {
+    if (kPlain) return acc[e];
+    return bias[j][e] == -kInf ? -kInf : acc[e] + bias[j][e];
+  }
 };
 
-// The same for the maximum m (not below own.m); nothing: (-inf, 0, 0).
-__device__ __forceinline__ void rescale(Sums &a, float m) {
-  const bool none = a.m == -kInf;
-  const float t = none ? 0.0f : a.m - m;
-  const float e = none ? 0.0f : exp_neg(t);
-  a.u = none ? 0.0f : e * (a.u + t * a.s);
-  a.s *= e;
-  a.m = m;
-}
-
-__device__ __forceinline__ Sums joined(Sums a, Sums b) {
-  const float m = nan_max(a.m, b.m);
-  rescale(a, m);
-  rescale(b, m);
-  return Sums{m, a.s + b.s, a.u + b.u};
-}
-
-__device__ __forceinline__ float logit(float z, float bias) {
-  return bias == -kInf ? -kInf : z + bias;  // (a masked class' row may hold anything)
-}
-
-// The bias of a lane's columns, -inf behind the last class.
-template <uint32_t kSub>
-__device__ __forceinline__ void load_bias(const float *bias, uint32_t col0, uint32_t n,
-                                          float (&b)[kSub][4]) {
-  const uint32_t lane = lane_id();
-#pragma unroll
-  for (uint32_t j = 0; j < kSub; ++j) {
-    const uint32_t col = col0 + outer_of(j, (lane / 16) * 4);
-#pragma unroll
-    for (uint32_t e = 0; e < 4; ++e)
-      b[j][e] = col + e >= n ? -kInf : bias != nullptr ? bias[min(col + e, n - 1)] : 0.0f;
-  }
-}
-
-// Epilogue of the forward product. A slice is a wave's columns (half a tile).
+// Epilogue of the forward product. A slice is a wave's columns.
 struct RowSums {
   const float *bias;
   const int32_t *targets;  // of the first row here
@@ -68,63 +52,76 @@ struct RowSums {
   float *at_target;        // [rows]
   uint32_t rows, n;
 
-  template <uint32_t kTile, bool kGated, uint32_t kSub>
-  __device__ __forceinline__ void run(const Acc (&acc)[kSub][kSub], uint32_t row0, uint32_t col0,
-                                      uint32_t) const {
+  template <bool kPlain, uint32_t kSubM, uint32_t kSubN>
+  __device__ __forceinline__ void go(const Acc (&acc)[kSubM][kSubN], uint32_t row0,
+                                     uint32_t col0) const {
     const uint32_t lane = lane_id();
-    float b[kSub][4];
-    load_bias(bias, col0, n, b);
-    float *const out = sums + (uint64_t)(col0 / (kTile / 2)) * 3 * rows;
+    Logits<kPlain, kSubN> logits;
+    logits.load(bias, col0, n);
+    float *const out = sums + (uint64_t)(col0 / (kSubN * 16)) * 3 * rows;
+    uint32_t in[kSubM];  // the target's place among the wave's columns
 #pragma unroll
-    for (uint32_t i = 0; i < kSub; ++i) {
+    for (uint32_t i = 0; i < kSubM; ++i) {
       const uint32_t row = row0 + outer_of(i, lane & 15);
-      float z[kSub][4];
-      float m = -kInf;
+      in[i] = targets != nullptr ? (uint32_t)targets[min(row, rows - 1)] - col0 : ~0u;
+    }
 #pragma unroll
-      for (uint32_t j = 0; j < kSub; ++j)
+    for (uint32_t i = 0; i < kSubM; ++i) {
+      const uint32_t row = row0 + outer_of(i, lane & 15);
+      float z[kSubN][4], m = -kInf;
+#pragma unroll
+      for (uint32_t j = 0; j < kSubN; ++j)
 #pragma unroll
         for (uint32_t e = 0; e < 4; ++e) {
-          z[j][e] = logit(acc[i][j][e], b[j][e]);
+          z[j][e] = logits.of(acc[i][j], j, e);
           m = nan_max(m, z[j][e]);
         }
       m = nan_max(m, __shfl_xor(m, 16, kWave));
       m = nan_max(m, __shfl_xor(m, 32, kWave));
       const float base = m == -kInf ? 0.0f : m;
-      float s = 0.0f, u = 0.0f;
+      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (uint32_t j = 0; j < kSub; ++j)
+      for (uint32_t j = 0; j < kSubN; ++j)
 #pragma unroll
         for (uint32_t e = 0; e < 4; ++e) {
-          const float t = z[j][e] - base;
+          const float t = not_below(z[j][e] - base);
           const float x = exp_neg(t);
-          s += x;
-          u += t == -kInf ? 0.0f : t * x;
+          s[e] += x;
+          u[e] = fmaf(t, x, u[e]);
         }
-      s += __shfl_xor(s, 16, kWave);
-      u += __shfl_xor(u, 16, kWave);
-      s += __shfl_xor(s, 32, kWave);
-      u += __shfl_xor(u, 32, kWave);
-      if (row >= rows) continue;
-      if (lane < 16) {
+      float s1 = (s[0] + s[1]) + (s[2] + s[3]), u1 = (u[0] + u[1]) + (u[2] + u[3]);
+      s1 += __shfl_xor(s1, 16, kWave);
+      u1 += __shfl_xor(u1, 16, kWave);
+      s1 += __shfl_xor(s1, 32, kWave);
+      u1 += __shfl_xor(u1, 32, kWave);
+      if (lane < 16 && row < rows) {
         out[row] = m;
-        out[(uint64_t)rows + row] = s;
-        out[2ull * rows + row] = u;
+        out[(uint64_t)rows + row] = s1;
+        out[2ull * rows + row] = u1;
       }
-      if (targets == nullptr) continue;
-      const uint32_t in = (uint32_t)targets[row] - col0;
-      if (in < kTile / 2 && in + col0 < n) {
+      if (in[i] < kSubN * 16 && row < rows && col0 + in[i] < n) {
 #pragma unroll
-        for (uint32_t j = 0; j < kSub; ++j)
+        for (uint32_t j = 0; j < kSubN; ++j)
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e)
-            if (in == outer_of(j, (lane / 16) * 4) + e) at_target[row] = z[j][e];
+            if (in[i] == outer_of(j, (lane / 16) * 4) + e) at_target[row] = z[j][e];
       }
     }
   }
+
+  template <bool kGated, uint32_t kSubM, uint32_t kSubN>
+  __device__ __forceinline__ void run(const Acc (&acc)[kSubM][kSubN], uint32_t row0, uint32_t col0,
+                                      bool whole, uint32_t) const {
+    if (whole && bias == nullptr) go<true>(acc, row0, col0);
+    else go<false>(acc, row0, col0);
+  }
 };
 
-// Rows' slices joined, 16 threads a row and 16 rows a block; the last block
-// reports targets past the classes.
+// Rows' slices joined, kLanes threads a row; the last block reports targets past
+// the classes. Where rows are few the slices of one want a whole block (4 rows
+// of 1024 slices 50 us with 16 threads a row, 5 with 256; 8192 rows 40 us and
+// 16 threads read whole lines of 16 rows).
+template <uint32_t kLanes>
 __global__ __launch_bounds__(kThreads) void join_rows(const float *__restrict__ sums,
                                                       const float *__restrict__ at_target,
                                                       uint32_t slices, uint32_t rows, uint32_t v,
@@ -138,19 +135,24 @@ __global__ __launch_bounds__(kThreads) void join_rows(const float *__restrict__ 
     if (status != nullptr) report_ids<kThreads>(all_targets, all, v, status);
     return;
   }
-  __shared__ Sums part[16][17];
-  const uint32_t in = threadIdx.x & 15, lane = threadIdx.x / 16;
-  const uint32_t row = blockIdx.x * 16 + in;
+  constexpr uint32_t kRows = kThreads / kLanes;
+  __shared__ Sums part[kLanes][kRows + (kRows > 1)];
+  const uint32_t in = threadIdx.x % kRows, lane = threadIdx.x / kRows;
+  const uint32_t row = blockIdx.x * kRows + in;
   Sums a = {-kInf, 0.0f, 0.0f};
   if (row < rows)
-    for (uint32_t k = lane; k < slices; k += 16) {
+    for (uint32_t k = lane; k < slices; k += kLanes) {
       const float *const p = sums + (uint64_t)k * 3 * rows + row;
       a = joined(a, Sums{p[0], p[rows], p[2ull * rows]});
     }
-  part[lane][in] = a;
-  __syncthreads();
-  if (threadIdx.x >= 16 || row >= rows) return;
-  for (uint32_t k = 1; k < 16; ++k) a = joined(a, part[k][in]);
+#pragma unroll
+  for (uint32_t half = kLanes / 2; half > 0; half /= 2) {
+    if (lane < 2 * half) part[lane][in] = a;
+    __syncthreads();
+    if (lane < half) a = joined(a, part[lane + half][in]);
+    __syncthreads();
+  }
+  if (lane > 0 || row >= rows) return;
   const bool none = a.m == -kInf;
   // NaN: a row that holds NaN or +inf has no distribution
   const float m = a.m == kInf ? __builtin_nanf("") : a.m;
@@ -203,6 +205,7 @@ __global__ __launch_bounds__(kPrepare) void prepare_rows(const int32_t *__restri
 }
 
 // Epilogue of the backward's first product: d_z of a piece of the classes.
+// With lp = log p: d_z = g [target] - p (g + h H + h lp).
 template <class O>
 struct PutDz {
   const float *bias;  // of the piece
@@ -213,51 +216,77 @@ struct PutDz {
   float *column_sums;  // [half tiles of rows][ld], or nullptr
   uint32_t rows, n, first, classes;
 
-  template <uint32_t kTile, bool kGated, uint32_t kSub>
-  __device__ __forceinline__ void run(const Acc (&acc)[kSub][kSub], uint32_t row0, uint32_t col0,
-                                      uint32_t) const {
+  template <bool kPlain, uint32_t kSubM, uint32_t kSubN>
+  __device__ __forceinline__ void go(const Acc (&acc)[kSubM][kSubN], uint32_t row0,
+                                     uint32_t col0) const {
     const uint32_t lane = lane_id();
-    float b[kSub][4], sum[kSub][4];
-    load_bias(bias, col0, n, b);
+    Logits<kPlain, kSubN> logits;
+    logits.load(bias, col0, n);
+    float sum[kSubN][4];
 #pragma unroll
-    for (uint32_t j = 0; j < kSub; ++j)
+    for (uint32_t j = 0; j < kSubN; ++j)
 #pragma unroll
       for (uint32_t e = 0; e < 4; ++e) sum[j][e] = 0.0f;
     const float by = scale != nullptr ? scale[0] : 1.0f;
+    // the rows' figures, all in flight together
+    float m[kSubM], ls[kSubM], g[kSubM], h[kSubM], gh[kSubM];
+    uint32_t hit[kSubM];
 #pragma unroll
-    for (uint32_t i = 0; i < kSub; ++i) {
+    for (uint32_t i = 0; i < kSubM; ++i) {
+      const uint32_t r = min(row0 + outer_of(i, lane & 15), rows - 1);
+      m[i] = stats[2ull * r];
+      ls[i] = stats[2ull * r + 1];
+      hit[i] = targets != nullptr ? (uint32_t)targets[r] : ~0u;
+      g[i] = d_logp != nullptr ? d_logp[r] : 0.0f;
+      h[i] = d_entropy != nullptr ? d_entropy[r] : 0.0f;
+      gh[i] = d_entropy != nullptr ? entropy[r] : 0.0f;
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kSubM; ++i) {
+      g[i] = hit[i] < classes ? g[i] : 0.0f;
+      gh[i] = m[i] == m[i] ? fmaf(h[i], gh[i], g[i]) : m[i];  // no distribution: NaN
+      hit[i] -= first;
+      if (bias != nullptr && hit[i] < n && bias[hit[i]] == -kInf) hit[i] = ~0u;  // masked
+      hit[i] = hit[i] < n ? hit[i] - col0 : ~0u;
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kSubM; ++i) {
       const uint32_t row = row0 + outer_of(i, lane & 15);
       const bool in_row = row < rows;
-      const uint32_t r = in_row ? row : rows - 1;
-      const float m = stats[2ull * r], ls = stats[2ull * r + 1];
-      const int32_t t = targets != nullptr ? targets[r] : -1;
-      const bool known = t >= 0 && (uint32_t)t < classes;
-      const uint32_t hit = known ? (uint32_t)t - first : ~0u;  // (another piece's is none here)
-      const float g = known && d_logp != nullptr ? d_logp[r] : 0.0f;
-      const float h = d_entropy != nullptr ? d_entropy[r] : 0.0f;
-      const float gh = d_entropy != nullptr ? g + h * entropy[r] : g;
+      float d[kSubN][4];
 #pragma unroll
-      for (uint32_t j = 0; j < kSub; j += 2) {
-        const uint32_t at = outer_of(j, (lane / 16) * 4);
-        Row8 d;
+      for (uint32_t j = 0; j < kSubN; ++j)
 #pragma unroll
-        for (uint32_t e = 0; e < 8; ++e) {
-          const float z = logit(acc[i][j + e / 4][e & 3], b[j + e / 4][e & 3]);
-          const float lp = z - m - ls;
-          const float p = exp_neg(lp);
-          const float y = (col0 + at + e == hit ? g : 0.0f) - (p == 0.0f ? 0.0f : p * (gh + h * lp));
-          // masked: 0, but NaN in a row without a distribution
-          d[e] = z == -kInf && m == m ? 0.0f : y;
-          sum[j + e / 4][e & 3] += in_row ? d[e] : 0.0f;
-          d[e] *= by;
+        for (uint32_t e = 0; e < 4; ++e) {
+          const float lp = not_below(logits.of(acc[i][j], j, e) - m[i] - ls[i]);
+          d[j][e] = -exp_neg(lp) * fmaf(h[i], lp, gh[i]);
         }
-        if (in_row && col0 + at < n) put_operand<O>(dz + row * ld + col0 + at, plane, d);
+      if (hit[i] < kSubN * 16) {
+#pragma unroll
+        for (uint32_t j = 0; j < kSubN; ++j)
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e)
+            if (hit[i] == outer_of(j, (lane / 16) * 4) + e) d[j][e] += g[i];
+      }
+      if (column_sums != nullptr && in_row) {
+#pragma unroll
+        for (uint32_t j = 0; j < kSubN; ++j)
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) sum[j][e] += d[j][e];
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < kSubN; j += 2) {
+        const uint32_t col = col0 + outer_of(j, (lane / 16) * 4);
+        Row8 v;
+#pragma unroll
+        for (uint32_t e = 0; e < 8; ++e) v[e] = d[j + e / 4][e & 3] * by;
+        if (in_row && (kPlain || col < n)) put_operand<O>(dz + row * ld + col, plane, v);
       }
     }
     if (column_sums == nullptr) return;
-    float *const to = column_sums + (uint64_t)(row0 / (kTile / 2)) * ld;
+    float *const to = column_sums + (uint64_t)(row0 / (kSubM * 16)) * ld;
 #pragma unroll
-    for (uint32_t j = 0; j < kSub; ++j) {
+    for (uint32_t j = 0; j < kSubN; ++j) {
       Acc s;
 #pragma unroll
       for (uint32_t e = 0; e < 4; ++e) s[e] = group_sum<16>(sum[j][e]);
@@ -265,32 +294,12 @@ struct PutDz {
       if ((lane & 15) == 0 && col < n) *reinterpret_cast<Acc *>(to + col) = s;
     }
   }
-};
 
-// A piece's part of d_x to f32, beside the pieces before.
-struct AddParts {
-  float *to;
-  uint32_t m, n, wide;
-  bool add;
-
-  template <uint32_t kTile, bool kGated, uint32_t kSub>
-  __device__ __forceinline__ void run(const Acc (&acc)[kSub][kSub], uint32_t row0, uint32_t col0,
-                                      uint32_t part) const {
-    const uint32_t lane = lane_id();
-#pragma unroll
-    for (uint32_t i = 0; i < kSub; ++i) {
-      const uint32_t row = row0 + outer_of(i, lane & 15);
-      if (row >= m) continue;
-      float *const at = to + ((uint64_t)part * m + row) * wide;
-#pragma unroll
-      for (uint32_t j = 0; j < kSub; j += 2) {
-        const uint32_t col = col0 + outer_of(j, (lane / 16) * 4);
-        if (col >= n) continue;
-        Row8 v = eight(acc[i][j], acc[i][j + 1]);
-        if (add) v += *reinterpret_cast<const Row8 *>(at + col);
-        *reinterpret_cast<Row8 *>(at + col) = v;
-      }
-    }
+  template <bool kGated, uint32_t kSubM, uint32_t kSubN>
+  __device__ __forceinline__ void run(const Acc (&acc)[kSubM][kSubN], uint32_t row0, uint32_t col0,
+                                      bool whole, uint32_t) const {
+    if (whole && bias == nullptr) go<true>(acc, row0, col0);
+    else go<false>(acc, row0, col0);
   }
 };
 
@@ -301,9 +310,10 @@ struct ToScaledRows {
   uint64_t ld;
   uint32_t n;
   const float *scale;  // or nullptr
-  __device__ __forceinline__ void operator()(uint32_t row, uint32_t col, Row8 v) const {
+  template <bool kWhole>
+  __device__ __forceinline__ void put(uint32_t row, uint32_t col, Row8 v) const {
     if (scale != nullptr) v *= scale[1];
-    store_pack_tail<O, 8>(out + row * ld, col, n, __builtin_convertvector(v, Pack<O, 8>));
+    put_row<kWhole>(out + row * ld, col, n, v);
   }
 };
 
@@ -345,9 +355,16 @@ struct LossRoom {
 LossRoom lay_out(const LossCall &c, bool x_stays, bool table_stays, void *ws) {
   LossRoom r;
   Room room{static_cast<char *>(ws)};
+  if (c.n <= kFewRows) {
+    r.rows = c.n;
+    r.sums = static_cast<float *>(room.take((size_t)c.n * 12 * few_slices(c.v)));
+    r.at_target = static_cast<float *>(room.take((size_t)c.n * 4));
+    r.bytes = room.used;
+    return r;
+  }
   r.x = operand(c.x, c.dtype, c.x_ld, c.n, c.d, x_stays, room, r.list);
   r.table = operand(c.table, c.dtype, c.table_ld, c.v, c.d, table_stays, room, r.list);
-  const uint64_t a_row = 3ull * 4 * 2 * div_up(c.v, 128);
+  const uint64_t a_row = 3ull * 4 * 2 * div_up(c.v, 128);  // (of the most slices)
   uint64_t rows = kSumsBytes / a_row / 256 * 256;
   if (rows < 4096) rows = 4096;
   r.rows = rows < c.n ? (uint32_t)rows : c.n;
@@ -387,7 +404,7 @@ LossGradRoom lay_out_grad(const LossGradCall &c, bool x_stays, bool table_stays,
   // pieces of equal size
   piece = (div_up(c.v, count) + 255) / 256 * 256;
   r.piece = piece < c.v ? (uint32_t)piece : c.v;
-  r.dz_ld = up8(r.piece);
+  r.dz_ld = up64(r.piece);
   r.dz = static_cast<uint16_t *>(room.take(matrix_bytes(c.dtype, c.n, r.piece)));
   const uint32_t tiles = tiles_of(c.dtype, 1, up8(c.d));
   r.z = plan_shape(c.n, r.piece, tiles);
@@ -434,9 +451,14 @@ hipError_t launch_loss(const LossCall &c, float *logp, float *entropy, float *st
   const uint32_t d8 = up8(c.d);
   for (uint64_t i = 0; e == hipSuccess && (i < c.n || i == 0); i += r.rows) {
     const uint32_t rows = (uint32_t)(c.n - i < r.rows ? c.n - i : r.rows);
-    const uint32_t slices = rows == 0 ? 0 : 2 * div_up(c.v, r.shape.tile);
+    const bool few = c.n <= kFewRows;
+    const uint32_t slices = few ? few_slices(c.v) : 2 * div_up(c.v, r.shape.tile);
     const int32_t *const targets = c.targets == nullptr ? nullptr : c.targets + i;
-    if (rows > 0) {
+    if (few && rows > 0) {
+      const FewSums sums = {c.x, c.table, c.bias, targets, r.sums, r.at_target, c.x_ld, c.table_ld,
+                            rows, c.d, c.v};
+      if ((e = launch_few_sums(sums, c.dtype, stream)) != hipSuccess) break;
+    } else if (rows > 0) {
       const uint64_t a_base[1] = {i * r.x.ld};
       const Args g = make_args(c.dtype, r.x, r.table, rows, c.v, d8, d8, 1, a_base, nullptr, r.shape, c.v);
       const RowSums sums = {c.bias, targets, r.sums, r.at_target, rows, c.v};
@@ -445,7 +467,8 @@ hipError_t launch_loss(const LossCall &c, float *logp, float *entropy, float *st
       });
       if (e != hipSuccess) break;
     }
-    join_rows<<<div_up(rows, 16) + 1, kThreads, 0, stream>>>(
+    const auto join = rows < 4096 ? join_rows<256> : join_rows<16>;
+    join<<<div_up(rows, rows < 4096 ? 1 : 16) + 1, kThreads, 0, stream>>>(
         r.sums, r.at_target, slices, rows, c.v, targets, logp == nullptr ? nullptr : logp + i,
         entropy == nullptr ? nullptr : entropy + i, stats == nullptr ? nullptr : stats + 2 * i,
         c.targets, c.targets == nullptr ? 0 : c.n, i == 0 ? status : nullptr);
@@ -539,7 +562,7 @@ hipError_t launch_loss_grad(const LossGradCall &c, void *d_x, uint64_t d_x_ld, v
                                                          stream);
         } else {
           rc = launch_tiles<T, kAlongK, kAcrossK, false>(
-              g, s, AddParts{r.parts, c.n, c.d, d8, first > 0}, stream);
+              g, s, Parts{r.parts, c.n, c.d, d8, first > 0}, stream);
           if (rc == hipSuccess && first + n == c.v) {
             const uint64_t chunks = (uint64_t)c.n * div_up(c.d, 8);
             join_parts<false><<<div_up(chunks, kThreads), kThreads, 0, stream>>>(

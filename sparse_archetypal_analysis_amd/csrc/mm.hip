@@ -26,7 +26,7 @@ __global__ __launch_bounds__(kThreads) void pack_rows(Pack3 list) {
         v[e] = col + e < it.len ? (float)x : 0.0f;
       }
     }
-    put_operand<O>(it.to + row * it.row_chunks * 8 + col, it.plane, v);
+    put_operand<O>(it.to + row * it.to_ld + col, it.plane, v);
   }
 }
 
@@ -58,11 +58,12 @@ Shape plan_shape(uint64_t m, uint64_t n, uint32_t tiles) {
       const uint64_t blocks = count * real;
       double t;
       if (tile == 256) {
-        t = (double)((blocks + 255) / 256) * (4000.0 + 800.0 * per);
+        t = (double)((blocks + 255) / 256) * (8000.0 + 735.0 * per);
       } else {
         const uint64_t full = blocks / 512, rest = blocks % 512;
-        t = (double)full * (4000.0 + 590.0 * per);
-        if (rest > 0) t += 3000.0 + (rest > 256 ? 590.0 : 350.0) * per;
+        t = (double)full * (3500.0 + 555.0 * per);
+        if (rest > 256) t += 6000.0 + 555.0 * per;
+        else if (rest > 0) t += 5000.0 + 317.0 * per;
       }
       if (real > 1) t += 3000.0 + (double)(m * n) * 4.0 * (2.0 * real) / 3500.0;
       if (least == 0.0 || t < least) {

@@ -3,6 +3,9 @@
 // results left to the caller (an Epilogue). Nothing here is exported.
 #pragma once
 
+#include <type_traits>
+#include <utility>
+
 #include "token.hpp"
 
 namespace seacells {
@@ -14,7 +17,6 @@ enum Side : uint32_t { kAlongK = 0, kAcrossK = 1 };
 
 constexpr uint32_t kMaxSegs = 12;
 constexpr uint32_t kTileK = 32;
-constexpr uint32_t kStages = 4;
 constexpr uint32_t kThreads = 256;
 constexpr uint32_t kOutside = 0x80000000u;  // a byte offset past every operand's range
 
@@ -32,6 +34,16 @@ struct Args {
   uint32_t tiles_m, tiles_n;
   uint64_t a_off[kMaxSegs], b_off[kMaxSegs];
 };
+
+// f(0), f(1), ... as constants.
+template <class F, uint32_t... kI>
+__device__ __forceinline__ void each_of(F &&f, std::integer_sequence<uint32_t, kI...>) {
+  (f(std::integral_constant<uint32_t, kI>{}), ...);
+}
+template <uint32_t kCount, class F>
+__device__ __forceinline__ void each(F &&f) {
+  each_of(f, std::make_integer_sequence<uint32_t, kCount>{});
+}
 
 typedef int Srd __attribute__((ext_vector_type(4)));
 typedef short Half4 __attribute__((ext_vector_type(4)));
@@ -69,10 +81,11 @@ __device__ __forceinline__ void settle() {
 // wait state is M0's; the descriptor is older than settled() below.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
+template <uint32_t kOffset>
 __device__ __forceinline__ void load_to_lds(uint32_t lds, const Srd &srd, uint32_t at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
-               "v"(at), "s"(srd)
-               : "m0");
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds),
+               "v"(at), "s"(srd), "n"(kOffset)
+               : "m0", "scc");
 }
 #pragma clang diagnostic pop
 
@@ -82,13 +95,16 @@ __device__ __forceinline__ void settled(Srd &a, Srd &b) {
   asm volatile("s_nop 4" : "+s"(a), "+s"(b));
 }
 
-// Waits until at most kLeft of the wave's loads are in flight, then for the
-// block's other waves.
-template <uint32_t kLeft>
+// Waits until at most kLeft of the wave's loads are in flight (and, kReads, its
+// LDS reads are done), then for the block's other waves.
+template <uint32_t kLeft, bool kReads>
 __device__ __forceinline__ void landed() {
   static_assert(kLeft < 64, "vmcnt");
   __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLeft) : "memory");
+  if constexpr (kReads)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
+  else
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLeft) : "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -100,24 +116,32 @@ __device__ __forceinline__ constexpr uint32_t outer_of(uint32_t tile, uint32_t i
 }
 
 // One operand's way into registers. kSize: outer indexes of the block's tile.
-// LDS holds a stage as 1 KB pieces, one per wave load, 16 bytes a lane; the
-// order of the 16-byte chunks within a row is what keeps the banks apart:
-//   along K:  rows of 64 bytes (4 chunks) per outer index, chunk ^ s(row).
-//             The 16 lanes of a fragment read rows {0-3, 8-11, 16-19, 24-27}
-//             of a pair of tiles; s gives them 16 places of the 256 bytes that
-//             4 rows span, and 8 places of 128 bytes to each 8 of them.
-//   across K: rows of kSize elements per k, chunk ^ 4 (k % 4). A transposing
-//             read takes 4 k and 4 chunks' halves: 4 times 64 bytes apart.
+// LDS holds two pairs of tiles of 32 k, as 1 KB pieces, one per wave load, 16
+// bytes a lane; the order of the 16-byte chunks within a row is what keeps the
+// banks apart:
+//   along K:  a pair of tiles is loaded as one, rows of 128 bytes (8 chunks, a
+//             cache line) per outer index, chunk ^ s(row). 16 lanes of a
+//             fragment read rows {0-3, 8-11, 16-19, 24-27} of a pair of tiles of
+//             16; s gives them 16 places of the 256 bytes that 2 rows span, and
+//             each 8 of them 8 places of 128 bytes.
+//   across K: tiles are loaded one by one, rows of kSize elements per k, chunk ^
+//             4 (k % 4). A transposing read takes 4 k and 4 chunks' halves: 4
+//             times 64 bytes apart.
 template <Side kSide, uint32_t kSize>
 struct Lane {
-  static constexpr uint32_t kBytes = kSize * kTileK * 2;  // of a stage
-  static constexpr uint32_t kLoads = kBytes / 4096;       // of a wave and stage
-  static constexpr uint32_t kTiles = kSize / 32;          // of 16, of a wave (half the block's)
-  static constexpr uint32_t kChunks = kSize / 8;          // of a row across K
+  static constexpr bool kPairs = kSide == kAlongK;            // what is loaded at once
+  static constexpr uint32_t kPair = kSize * kTileK * 4;       // bytes of a pair of tiles
+  static constexpr uint32_t kBytes = 2 * kPair;               // of the ring
+  static constexpr uint32_t kLoads = kPair / (kPairs ? 4096 : 8192);  // of a wave at once
+  static constexpr uint32_t kStep = kPairs ? 2 * kTileK : kTileK;     // k of them
+  static constexpr uint32_t kChunks = kSize / 8;              // of a row across K
+  static constexpr uint32_t kRows = 1024 / (kSize * 2);       // k of a wave load across K
+  static constexpr uint32_t kReads = kPairs ? 2 : kSize / 64;
 
-  uint32_t at[kLoads];      // byte offsets of the lane's loads behind the tile's corner
-  uint32_t k_of;            // the lane's first k of a stage (across K: of its first load)
-  uint32_t read[kTiles / 2];  // byte offsets of the lane's LDS reads, per pair of tiles
+  uint32_t at[kLoads];    // byte offsets of the lane's loads behind the tile's corner
+  uint32_t k_of;          // the lane's first k (across K: of its first load)
+  uint32_t read[kReads];  // byte offsets of the lane's LDS reads: along K per tile of the pair,
+                          // across K per two tiles of 16
 
   // outer: first outer index of the tile; limit: outer indexes that there are.
   // half: which half of the tile's outer indexes the wave multiplies. row_of(r)
@@ -126,64 +150,56 @@ struct Lane {
   __device__ __forceinline__ void init(uint64_t ld, uint32_t outer, uint32_t limit, uint32_t half,
                                        RowOf row_of) {
     const uint32_t lane = lane_id(), wave = threadIdx.x / kWave;
-    if constexpr (kSide == kAlongK) {
-      const uint32_t r0 = wave * 16 + lane / 4;
-      const uint32_t s = ((r0 >> 3) & 1) + 2 * (((r0 >> 4) ^ (r0 >> 1)) & 1);
-      const uint32_t chunk = (lane & 3) ^ s;
+    if constexpr (kPairs) {
+      const uint32_t r0 = wave * 8 + lane / 8;
+      const uint32_t chunk = (lane & 7) ^ swizzle(r0);
       k_of = chunk * 8;
 #pragma unroll
       for (uint32_t j = 0; j < kLoads; ++j) {
-        const uint32_t row = row_of(j * 64 + r0);
+        const uint32_t row = row_of(j * 32 + r0);
         at[j] = row == kOutside ? kOutside : (uint32_t)(row * ld * 2 + chunk * 16);
       }
-      const uint32_t i = lane & 15;
-      const uint32_t sr = ((i >> 2) & 1) + 2 * (((i >> 3) ^ (i >> 1)) & 1);
-      const uint32_t slot = (lane / 16) ^ sr;
-#pragma unroll
-      for (uint32_t p = 0; p < kTiles / 2; ++p)
-        read[p] = (half * (kSize / 2) + p * 32 + (i / 4) * 8 + (i & 3)) * 64 + slot * 16;
+      const uint32_t r = outer_of(0, lane & 15);
+      read[0] = (half * (kSize / 2) + r) * 128 + ((lane / 16) ^ swizzle(r)) * 16;
+      read[1] = read[0] ^ 64;
     } else {
-      constexpr uint32_t kRows = 1024 / (kSize * 2);  // k of a wave load
       const uint32_t row = wave * kRows + lane / kChunks;
       const uint32_t chunk = (lane % kChunks) ^ ((row & 3) * 4);
       const bool in = outer + chunk * 8 < limit;
       k_of = row;
-  #pragma unroll
+#pragma unroll
       for (uint32_t j = 0; j < kLoads; ++j)
         at[j] = in ? (uint32_t)((j * 4 * kRows + row) * ld * 2 + chunk * 16) : kOutside;
       const uint32_t r = (lane & 15) / 4, q = lane & 3;
 #pragma unroll
-      for (uint32_t p = 0; p < kTiles / 2; ++p) {
+      for (uint32_t p = 0; p < kReads; ++p) {
         const uint32_t c = (half * (kChunks / 2) + p * 4 + q) ^ (r * 4);
         read[p] = ((lane / 16) * 8 + r) * (kSize * 2) + c * 16;
       }
     }
   }
 
-  static __device__ __forceinline__ Srd srd(const char *base) {
-    Srd s;
-    s.x = (int)(uint32_t)(uintptr_t)base;
-    s.y = (int)((uint32_t)((uintptr_t)base >> 32) & 0xFFFFu);
-    s.z = 0x7FFFFFFF;
-    s.w = 0x00020000;
-    return s;
+  static __device__ __forceinline__ uint32_t swizzle(uint32_t row) {
+    return ((row >> 1) & 1) + ((row >> 3) & 1) * 2 + (((row >> 4) ^ row) & 1) * 4;
   }
 
-  // The wave's load j of a stage. k_left: k that the operand still has at the
-  // descriptor's base (0: zeros are loaded).
-  __device__ __forceinline__ void load(uint32_t j, uint32_t lds, const Srd &srd,
-                                       uint32_t k_left) const {
-    const uint32_t k = k_of + (kSide == kAlongK ? 0 : j * (4096 / (kSize * 2)));
-    load_to_lds(lds + j * 4096, srd, k < k_left ? at[j] : kOutside);
+  // The wave's load j. left: k that the operand still has at the descriptor's
+  // base (below 1: zeros are loaded).
+  template <uint32_t j>
+  __device__ __forceinline__ void load(uint32_t lds, const Srd &srd, int32_t left) const {
+    const int32_t k = (int32_t)(k_of + (kPairs ? 0 : j * 4 * kRows));
+    load_to_lds<j * 4096>(lds, srd, k < left ? at[j] : kOutside);
   }
 
-  // The fragment of one tile of 16 from a stage: 8 k of one outer index.
-  __device__ __forceinline__ Half8 fragment(const char *stage, uint32_t tile) const {
+  // The fragment of one tile of 16 from tile `odd` of the pair at `pair`: 8 k of
+  // one outer index.
+  template <uint32_t kOdd>
+  __device__ __forceinline__ Half8 fragment(const char *pair, uint32_t tile) const {
     typedef __attribute__((address_space(3))) Half4 *At;
-    if constexpr (kSide == kAlongK) {
-      return *reinterpret_cast<const Half8 *>(stage + read[tile / 2] + (tile & 1) * 256);
+    if constexpr (kPairs) {
+      return *reinterpret_cast<const Half8 *>(pair + read[kOdd] + (tile / 2) * 4096 + (tile & 1) * 512);
     } else {
-      const char *p = stage + read[tile / 2] + (tile & 1) * 8;
+      const char *p = pair + kOdd * (kPair / 2) + read[tile / 2] + (tile & 1) * 8;
       const Half4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)(p));
       const Half4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)(p + 4 * kSize * 2));
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -212,9 +228,9 @@ __device__ __forceinline__ void tile_of(uint32_t block, uint32_t tiles_m, uint32
   *tn = in / high;
 }
 
-// The rows of a tile of B along K: kTile consecutive ones, or for a gated
-// product kTile / 2 of the gate and the kTile / 2 up rows `pair` behind them,
-// 64 (32) and 64 (32) to each wave's half.
+// The rows of a tile of B along K: kTile consecutive ones, or for a gated product
+// half of them of the gate and half the up rows `pair` behind them, as many of
+// each to a wave's columns.
 template <uint32_t kTile, bool kGated>
 __device__ __forceinline__ uint32_t b_row(uint32_t r, uint32_t outer, uint32_t limit,
                                           uint32_t pair) {
@@ -225,26 +241,33 @@ __device__ __forceinline__ uint32_t b_row(uint32_t r, uint32_t outer, uint32_t l
   return outer + row < limit ? row + up * pair : kOutside;
 }
 
-// A block of 4 waves computes kTile x kTile results, each wave a quarter. The
-// LDS holds a ring of 4 stages of 32 k; loads run 3 tiles ahead, and the
-// fragments of the next tile are read while the present one multiplies, so
-// one barrier per tile is all that the waves wait for.
-// epi(acc, row, col): all results of the wave; see Epilogue use below.
+// A block of 4 waves computes kTile x kTile results, each wave a quarter: of 256
+// x 256 (128 KB of LDS) one block a CU, of 128 x 128 (64 KB) two. The LDS holds
+// two pairs of tiles of 32 k. While the products of tile t run, the fragments of
+// tile t + 1 are read, and loads go out: operands across K one tile at a time,
+// into the half that tile t - 1 has left; operands along K a pair at a time, in
+// odd t, into the pair that is then read to its end. One or two barriers a pair
+// are all that the waves wait for.
+// epi.run(acc, row0, col0, whole, part): the wave's results from (row0, col0)
+// on, the last of them inside of the whole or not, of part `part` of k.
 template <class T, uint32_t kTile, Side kA, Side kB, bool kGated, class Epilogue>
 __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void product(Args g, Epilogue epi) {
-  constexpr uint32_t kSub = kTile / 32;  // tiles of 16 of a wave, each way
+  constexpr uint32_t kPart = kTile / 2;  // rows and columns of a wave
+  constexpr uint32_t kSub = kPart / 16;  // in tiles of 16
   typedef Lane<kA, kTile> LaneA;
   typedef Lane<kB, kTile> LaneB;
-  constexpr uint32_t kStage = LaneA::kBytes + LaneB::kBytes;
-  constexpr uint32_t kLoads = LaneA::kLoads + LaneB::kLoads;
-  __shared__ __attribute__((aligned(1024))) char ring[kStages * kStage];
+  // loads that go out with an even and with an odd tile
+  constexpr uint32_t kEven = (LaneA::kPairs ? 0 : LaneA::kLoads) + (LaneB::kPairs ? 0 : LaneB::kLoads);
+  constexpr uint32_t kOdd = LaneA::kLoads + LaneB::kLoads;
+  constexpr bool kAnyPairs = LaneA::kPairs || LaneB::kPairs;
+  __shared__ __attribute__((aligned(1024))) char ring[LaneA::kBytes + LaneB::kBytes];
 
   const uint32_t wave = threadIdx.x / kWave;
   const uint32_t wm = wave & 1, wn = wave >> 1;
   uint32_t tm, tn;
   tile_of(blockIdx.x, g.tiles_m, g.tiles_n, &tm, &tn);
   const uint32_t row0 = tm * kTile;
-  const uint32_t col0 = tn * (kGated ? kTile / 2 : kTile);
+  const uint32_t col0 = tn * (kGated ? kPart : kTile);
   const uint32_t t0 = blockIdx.y * g.per_split;
   const uint32_t tiles = min(g.per_split, g.tiles - t0);
 
@@ -254,52 +277,75 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void product(Args g
   lb.init(g.ldb, col0, g.n, wn,
           [&](uint32_t r) { return b_row<kTile, kGated>(r, col0, g.n, g.n); });
 
-  // where the loads are: segment, k, corners of the tile there, and in the
-  // next segment
-  const uint64_t step_a = kA == kAlongK ? kTileK * 2 : g.lda * (kTileK * 2);
-  const uint64_t step_b = kB == kAlongK ? kTileK * 2 : g.ldb * (kTileK * 2);
-  const uint32_t seg_k = g.seg_tiles * kTileK;
-  uint32_t seg = t0 / g.seg_tiles, ahead = tiles;
-  uint32_t k = (t0 - seg * g.seg_tiles) * kTileK;
+  // Where the loads are: a descriptor of each operand whose base is the tile's
+  // corner, how much k it has from there on, and in how many pairs the segment
+  // (or the block's part of k) ends. That is looked at between two tiles.
+  const uint64_t step_a = LaneA::kPairs ? LaneA::kStep * 2 : g.lda * (LaneA::kStep * 2);
+  const uint64_t step_b = LaneB::kPairs ? LaneB::kStep * 2 : g.ldb * (LaneB::kStep * 2);
   const char *const at_a = reinterpret_cast<const char *>(g.a) + corner<kA>(g.lda, row0, 0);
   const char *const at_b = reinterpret_cast<const char *>(g.b) + corner<kB>(g.ldb, col0, 0);
-  const char *pa = at_a + g.a_off[seg] * 2 + corner<kA>(g.lda, 0, k);
-  const char *pb = at_b + g.b_off[seg] * 2 + corner<kB>(g.ldb, 0, k);
-  uint32_t known = min(seg + 1, kMaxSegs - 1);
-  const char *next_a = at_a + g.a_off[known] * 2;
-  const char *next_b = at_b + g.b_off[known] * 2;
+  uint32_t seg = t0 / g.seg_tiles;
+  const uint32_t in_seg = t0 - seg * g.seg_tiles;
+  uint32_t until = min(g.seg_tiles - in_seg, tiles) / 2, remain = tiles / 2 - until;
+  uint64_t base_a = (uint64_t)(at_a + g.a_off[seg] * 2 + corner<kA>(g.lda, 0, in_seg * kTileK));
+  uint64_t base_b = (uint64_t)(at_b + g.b_off[seg] * 2 + corner<kB>(g.ldb, 0, in_seg * kTileK));
+  int32_t left_a = (int32_t)g.ka - (int32_t)(in_seg * kTileK);
+  int32_t left_b = (int32_t)g.kb - (int32_t)(in_seg * kTileK);
+
+  // (addresses have 47 bits: a base's upper word is a descriptor's as it is)
+  Srd srd_a, srd_b;
+  auto aim_a = [&]() {
+    srd_a = Srd{(int)(uint32_t)base_a, (int)(uint32_t)(base_a >> 32), 0x7FFFFFFF, 0x00020000};
+  };
+  auto aim_b = [&]() {
+    srd_b = Srd{(int)(uint32_t)base_b, (int)(uint32_t)(base_b >> 32), 0x7FFFFFFF, 0x00020000};
+  };
+  auto advance_a = [&]() {
+    base_a += step_a;
+    left_a -= LaneA::kStep;
+    aim_a();
+  };
+  auto advance_b = [&]() {
+    base_b += step_b;
+    left_b -= LaneB::kStep;
+    aim_b();
+  };
+  // Behind the loads of a pair: the next segment, or no more of k.
+  auto look = [&]() {
+    if (--until > 0) return;
+    if (remain == 0) {
+      left_a = left_b = 0;
+      until = 0x7FFFFFFF;
+      return;
+    }
+    ++seg;
+    base_a = (uint64_t)(at_a + g.a_off[seg] * 2);
+    base_b = (uint64_t)(at_b + g.b_off[seg] * 2);
+    left_a = (int32_t)g.ka;
+    left_b = (int32_t)g.kb;
+    until = min(g.seg_tiles / 2, remain);
+    remain -= until;
+    aim_a();
+    aim_b();
+    settled(srd_a, srd_b);
+  };
+
+  // Byte offsets: of the pair that is multiplied and of the other, and of the
+  // wave's loads.
+  uint32_t cur_a = 0, cur_b = LaneA::kBytes;
+  uint32_t next_a = LaneA::kPair, next_b = LaneA::kBytes + LaneB::kPair;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)ring +
                         __builtin_amdgcn_readfirstlane(wave) * 1024;
-
-  Srd srd_a, srd_b;
-  uint32_t left_a, left_b, at;
-  auto aim = [&](uint32_t stage) {
-    srd_a = LaneA::srd(pa);
-    srd_b = LaneB::srd(pb);
-    settled(srd_a, srd_b);
-    at = lds0 + stage * kStage;
-    left_a = ahead && g.ka > k ? g.ka - k : 0;
-    left_b = ahead && g.kb > k ? g.kb - k : 0;
-  };
-  auto load = [&](uint32_t j) {
-    if (j < LaneA::kLoads) la.load(j, at, srd_a, left_a);
-    else lb.load(j - LaneA::kLoads, at + LaneA::kBytes, srd_b, left_b);
-  };
-  auto advance = [&]() {
-    ahead -= ahead != 0;
-    k += kTileK;
-    const bool over = k == seg_k;
-    k = over ? 0 : k;
-    seg += over;
-    pa = over ? next_a : pa + step_a;
-    pb = over ? next_b : pb + step_b;
-  };
-  // (outside of the tiles' straight code)
-  auto look_ahead = [&]() {
-    if (seg < known) return;
-    known = min(seg + 1, kMaxSegs - 1);
-    next_a = at_a + g.a_off[known] * 2;
-    next_b = at_b + g.b_off[known] * 2;
+  // load q of those that go out with a tile
+  auto load = [&](auto odd, auto which) {
+    constexpr uint32_t q = decltype(which)::value;
+    constexpr bool is_odd = decltype(odd)::value != 0;
+    constexpr uint32_t of_a = is_odd || !LaneA::kPairs ? LaneA::kLoads : 0;
+    constexpr uint32_t of_b = is_odd || !LaneB::kPairs ? LaneB::kLoads : 0;
+    if constexpr (q < of_a)
+      la.template load<q>(lds0 + (is_odd ? cur_a : next_a + LaneA::kPair / 2), srd_a, left_a);
+    else if constexpr (q < of_a + of_b)
+      lb.template load<q - of_a>(lds0 + (is_odd ? cur_b : next_b + LaneB::kPair / 2), srd_b, left_b);
   };
 
   Acc acc[kSub][kSub];
@@ -308,60 +354,109 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void product(Args g
 #pragma unroll
     for (uint32_t j = 0; j < kSub; ++j) acc[i][j] = Acc{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // A tile's products, row by row of fragments of A; the next tile's fragments
-  // come in behind: B's with the first rows into registers of their own, a row
-  // of A's into its own once that is multiplied.
-  Half8 fa[kSub], fb[2][kSub];
-  auto step = [&](uint32_t stage, uint32_t now) {
-    landed<kLoads>();
-    aim((stage + 3) & 3);
-    const char *s = ring + ((stage + 1) & 3) * kStage;
-#pragma unroll
-    for (uint32_t i = 0; i < kSub; ++i) {
-#pragma unroll
-      for (uint32_t j = 0; j < kSub; ++j) {
-        mfma<T>(fb[now][j], fa[i], acc[i][j]);
-        if (j == 1) load(i);
-      }
-      if (i < kSub / 2) {
-        fb[now ^ 1][2 * i] = lb.fragment(s + LaneA::kBytes, 2 * i);
-        fb[now ^ 1][2 * i + 1] = lb.fragment(s + LaneA::kBytes, 2 * i + 1);
-      }
-      fa[i] = la.fragment(s, i);
+  // A tile's products, row by row of fragments of A, with the next tile's
+  // fragments and loads between them. An even tile's reads are of its own pair,
+  // which loads overwrite next where an operand comes in pairs: they are done
+  // before the last rows then, and waited for.
+  Half8 fa[2][kSub], fb[2][kSub];
+  auto step = [&](auto odd) {
+    constexpr uint32_t now = decltype(odd)::value;
+    if constexpr (now == 1) landed<kEven, kAnyPairs>();
+    else if constexpr (kEven > 0) landed<kOdd, false>();
+    else __builtin_amdgcn_sched_barrier(0);
+    const char *const from_a = ring + (now ? next_a : cur_a), *const from_b = ring + (now ? next_b : cur_b);
+    constexpr uint32_t kOut = now ? kOdd : kEven;
+    constexpr uint32_t kPerRow = (kOut + kSub - 1) / kSub;  // loads
+    constexpr uint32_t kReads = now == 0 && kAnyPairs ? 3 : 2;
+    each<kSub>([&](auto row) {
+      constexpr uint32_t i = decltype(row)::value;
+      each<kReads>([&](auto which) {
+        constexpr uint32_t q = i * kReads + decltype(which)::value;  // B's and A's in turn
+        if constexpr (q < 2 * kSub) {
+          if constexpr (q % 2 == 0)
+            fb[now ^ 1][q / 2] = lb.template fragment<now ^ 1>(from_b, q / 2);
+          else
+            fa[now ^ 1][q / 2] = la.template fragment<now ^ 1>(from_a, q / 2);
+        }
+      });
+      each<kSub>([&](auto column) {
+        constexpr uint32_t j = decltype(column)::value;
+        mfma<T>(fb[now][j], fa[now][i], acc[i][j]);
+        if constexpr (j == kSub / 4 && kPerRow > 0) load(odd, std::integral_constant<uint32_t, i * kPerRow>{});
+        if constexpr (j == 3 * kSub / 4 && kPerRow > 1)
+          load(odd, std::integral_constant<uint32_t, i * kPerRow + 1>{});
+        if constexpr (i == kSub - 1 && j == kSub - 2) {
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (now == 0 || !LaneA::kPairs) advance_a();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (i == kSub - 1 && j == kSub - 1) {
+          if constexpr (now == 0 || !LaneB::kPairs) advance_b();
+          if constexpr (now == 0 || kEven > 0) settled(srd_a, srd_b);
+        }
+      });
       __builtin_amdgcn_sched_barrier(0);
+    });
+    if constexpr (now == 0) {
+      look();
+    } else {
+      const uint32_t a = cur_a, b = cur_b;
+      cur_a = next_a;
+      cur_b = next_b;
+      next_a = a;
+      next_b = b;
     }
-    advance();
   };
+  static_assert(kOdd <= 2 * kSub && kEven <= 2 * kSub, "loads of a row");
 
-  static_assert(kLoads == kSub, "a load per row of fragments");
-#pragma unroll
-  for (uint32_t s = 0; s < 3; ++s) {
-    aim(s);
-#pragma unroll
-    for (uint32_t j = 0; j < kLoads; ++j) load(j);
-    advance();
-    look_ahead();
+  // pairs 0 and 1 along K, tiles 0 to 2 across K
+  const std::integral_constant<uint32_t, 0> even;
+  const std::integral_constant<uint32_t, 1> odd;
+  aim_a();
+  aim_b();
+  settled(srd_a, srd_b);
+  each<kOdd>([&](auto q) { load(odd, q); });  // into the present pair
+  if constexpr (kEven > 0) {
+    if constexpr (!LaneA::kPairs) advance_a();
+    if constexpr (!LaneB::kPairs) advance_b();
+    settled(srd_a, srd_b);
+    next_a = cur_a;  // (tile 1 belongs to the present pair)
+    next_b = cur_b;
+    each<kEven>([&](auto q) { load(even, q); });
+    next_a = LaneA::kPair;
+    next_b = LaneA::kBytes + LaneB::kPair;
   }
-  landed<2 * kLoads>();
+  advance_a();
+  advance_b();
+  settled(srd_a, srd_b);
+  look();
+  cur_a = next_a;
+  cur_b = next_b;
+  each<kOdd>([&](auto q) { load(odd, q); });
+  cur_a = 0;
+  cur_b = LaneA::kBytes;
+  if constexpr (!LaneA::kPairs) advance_a();
+  if constexpr (!LaneB::kPairs) advance_b();
+  settled(srd_a, srd_b);
+  landed<kEven + kOdd, false>();
 #pragma unroll
   for (uint32_t i = 0; i < kSub; ++i) {
-    fa[i] = la.fragment(ring, i);
-    fb[0][i] = lb.fragment(ring + LaneA::kBytes, i);
+    fa[0][i] = la.template fragment<0>(ring + cur_a, i);
+    fb[0][i] = lb.template fragment<0>(ring + cur_b, i);
   }
   // (the compiler's count of reads in flight starts the loop from none)
   __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
   settle();
-  uint32_t stage = 0;
   for (uint32_t t = 0; t < tiles; t += 2) {
-    step(stage, 0);
-    look_ahead();
-    step(stage + 1, 1);
-    stage ^= 2;
+    step(even);
+    step(odd);
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   settle();
-  epi.template run<kTile, kGated>(acc, row0 + wm * (kTile / 2),
-                                  col0 + wn * (kGated ? kTile / 4 : kTile / 2), blockIdx.y);
+  constexpr uint32_t kWide = kGated ? kPart / 2 : kPart;
+  const uint32_t row = row0 + wm * kPart, col = col0 + wn * kWide;
+  const bool whole = row + kPart <= g.m && col + kWide <= g.n;
+  epi.template run<kGated>(acc, row, col, __builtin_amdgcn_readfirstlane(whole) != 0, blockIdx.y);
 }
 
 // --- what becomes of the results ---------------------------------------------
@@ -371,57 +466,79 @@ __device__ __forceinline__ Row8 eight(const Acc &lo, const Acc &hi) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// put(row, col, v) for every 8 results inside of m rows and n columns, or
-// put(row, col, gate, up) for those of a gated product.
+// put<whole>(row, col, v) for every 8 results inside of m rows and n columns, or
+// put<whole>(row, col, gate, up) for those of a gated product. whole: all 8 are.
 template <class Put>
 struct Each {
   Put put;
   uint32_t m, n;
 
-  template <uint32_t kTile, bool kGated, uint32_t kSub>
-  __device__ __forceinline__ void run(const Acc (&acc)[kSub][kSub], uint32_t row0, uint32_t col0,
-                                      uint32_t) const {
+  template <bool kGated, bool kWhole, uint32_t kSubM, uint32_t kSubN>
+  __device__ __forceinline__ void go(const Acc (&acc)[kSubM][kSubN], uint32_t row0,
+                                     uint32_t col0) const {
     const uint32_t lane = lane_id();
 #pragma unroll
-    for (uint32_t i = 0; i < kSub; ++i) {
+    for (uint32_t i = 0; i < kSubM; ++i) {
       const uint32_t row = row0 + outer_of(i, lane & 15);
-      if (row >= m) continue;
+      if (!kWhole && row >= m) continue;
 #pragma unroll
-      for (uint32_t j = 0; j < (kGated ? kSub / 2 : kSub); j += 2) {
+      for (uint32_t j = 0; j < (kGated ? kSubN / 2 : kSubN); j += 2) {
         const uint32_t col = col0 + outer_of(j, (lane / 16) * 4);
-        if (col >= n) continue;
+        if (!kWhole && col >= n) continue;
         if constexpr (kGated)
-          put(row, col, eight(acc[i][j], acc[i][j + 1]),
-              eight(acc[i][j + kSub / 2], acc[i][j + kSub / 2 + 1]));
+          put.template put<kWhole>(row, col, eight(acc[i][j], acc[i][j + 1]),
+                                   eight(acc[i][j + kSubN / 2], acc[i][j + kSubN / 2 + 1]));
         else
-          put(row, col, eight(acc[i][j], acc[i][j + 1]));
+          put.template put<kWhole>(row, col, eight(acc[i][j], acc[i][j + 1]));
       }
     }
+  }
+
+  template <bool kGated, uint32_t kSubM, uint32_t kSubN>
+  __device__ __forceinline__ void run(const Acc (&acc)[kSubM][kSubN], uint32_t row0, uint32_t col0,
+                                      bool whole, uint32_t) const {
+    if (whole) go<kGated, true>(acc, row0, col0);
+    else go<kGated, false>(acc, row0, col0);
   }
 };
 
 // A part of k: f32 sums to rows of `wide` columns (a gated product's up
-// columns behind the gate's), a plane of m rows per part.
+// columns behind the gate's), a plane of m rows per part; `add` to what is
+// there.
 struct Parts {
   float *to;
   uint32_t m, n, wide;
+  bool add;
 
-  template <uint32_t kTile, bool kGated, uint32_t kSub>
-  __device__ __forceinline__ void run(const Acc (&acc)[kSub][kSub], uint32_t row0, uint32_t col0,
-                                      uint32_t part) const {
+  template <bool kGated, uint32_t kSubM, uint32_t kSubN>
+  __device__ __forceinline__ void run(const Acc (&acc)[kSubM][kSubN], uint32_t row0, uint32_t col0,
+                                      bool, uint32_t part) const {
     const uint32_t lane = lane_id();
 #pragma unroll
-    for (uint32_t i = 0; i < kSub; ++i) {
+    for (uint32_t i = 0; i < kSubM; ++i) {
       const uint32_t row = row0 + outer_of(i, lane & 15);
       if (row >= m) continue;
       float *const at = to + ((uint64_t)part * m + row) * wide;
+      Row8 v[kSubN / 2];
+      uint32_t col[kSubN / 2];
 #pragma unroll
-      for (uint32_t j = 0; j < kSub; j += 2) {
-        const bool up = kGated && j >= kSub / 2;
-        const uint32_t col = col0 + outer_of(up ? j - kSub / 2 : j, (lane / 16) * 4);
-        if (col >= n) continue;
-        *reinterpret_cast<Row8 *>(at + (up ? wide / 2 : 0) + col) = eight(acc[i][j], acc[i][j + 1]);
+      for (uint32_t j = 0; j < kSubN; j += 2) {
+        const bool up = kGated && j >= kSubN / 2;
+        const uint32_t c = col0 + outer_of(up ? j - kSubN / 2 : j, (lane / 16) * 4);
+        col[j / 2] = c < n ? c + (up ? wide / 2 : 0) : kOutside;
+        v[j / 2] = eight(acc[i][j], acc[i][j + 1]);
       }
+      if (add) {
+        Row8 old[kSubN / 2];
+#pragma unroll
+        for (uint32_t j = 0; j < kSubN / 2; ++j)  // (all in flight together)
+          old[j] = *reinterpret_cast<const Row8 *>(at + (col[j] == kOutside ? 0 : col[j]));
+#pragma unroll
+        for (uint32_t j = 0; j < kSubN / 2; ++j) v[j] += old[j];
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < kSubN / 2; ++j)
+        if (col[j] != kOutside) *reinterpret_cast<Row8 *>(at + col[j]) = v[j];
     }
   }
 };
@@ -444,8 +561,8 @@ __global__ __launch_bounds__(kThreads) void join_parts(const float *__restrict__
     a += *reinterpret_cast<const Row8 *>(at);
     if (kGated) b += *reinterpret_cast<const Row8 *>(at + wide / 2);
   }
-  if constexpr (kGated) put(row, col, a, b);
-  else put(row, col, a);
+  if constexpr (kGated) put.template put<false>(row, col, a, b);
+  else put.template put<false>(row, col, a);
 }
 
 // --- f32 as three 16-bit numbers ---------------------------------------------
@@ -500,9 +617,12 @@ struct Matrix {
 };
 
 inline uint32_t up8(uint32_t x) { return (x + 7u) & ~7u; }
+// A row of the workspace's matrices starts on a cache line (8192 x 4096 x 16384
+// bf16 780 us, with rows on half lines 930).
+inline uint32_t up64(uint32_t x) { return (x + 63u) & ~63u; }
 inline uint64_t planes_of(uint32_t dtype) { return dtype == 0u ? kPlanes : 1u; }
 inline uint64_t matrix_bytes(uint32_t dtype, uint64_t rows, uint32_t len) {
-  return align_up(rows * up8(len) * 2 * planes_of(dtype), 256);
+  return align_up(rows * up64(len) * 2 * planes_of(dtype), 256);
 }
 
 // Longest row of an operand, and most bytes between the rows of one tile:
@@ -523,7 +643,7 @@ struct PackItem {
   uint64_t from_ld;
   uint16_t *to;
   uint64_t chunks;  // rows * chunks of 8 of a row
-  uint64_t plane;
+  uint64_t to_ld, plane;
   uint32_t row_chunks, len;
 };
 struct Pack3 {
@@ -547,18 +667,19 @@ struct Room {
 inline Matrix operand(const void *p, uint32_t dtype, uint64_t ld, uint32_t rows, uint32_t len,
                       bool stays, Room &room, Pack3 &list) {
   if (stays) return Matrix{static_cast<const uint16_t *>(p), ld, 0};
-  const uint32_t wide = up8(len);
+  const uint32_t wide = up64(len), chunks = up8(len) / 8;
   const uint64_t plane = (uint64_t)rows * wide;
   uint16_t *const to = static_cast<uint16_t *>(room.take(matrix_bytes(dtype, rows, len)));
-  list.item[list.count++] = PackItem{p, ld, to, (uint64_t)rows * (wide / 8), plane, wide / 8, len};
+  list.item[list.count++] = PackItem{p, ld, to, (uint64_t)rows * chunks, wide, plane, chunks, len};
   return Matrix{to, wide, plane};
 }
 
 // How a product of m x n results over `tiles` tiles of k is spread over the
-// card. Times in ns, measured at 8192^3: a step of 32 k of a round of 256 x 256
-// tiles (one a CU) takes 800, of 128 x 128 tiles (two a CU) 590, and of half
-// such a round 350; a round costs about 4000 besides. Parts of k fill the card
-// where tiles are few; their sums are written and read once more.
+// card: the least time by what rounds of blocks take, measured (ns, bf16): of
+// 256 x 256 tiles (one a CU) 8000 + 735 a step of 32 k; of 256 x 128 (two a CU)
+// 7000 + 865, with one a CU 7000 + 630; of 128 x 128 (two) 3500 + 555, with one
+// 5000 + 317. Parts of k fill the card where tiles are few; their sums are
+// written and read once more.
 struct Shape {
   uint32_t tile, parts, per_part;
 };
@@ -632,7 +753,7 @@ hipError_t launch_product(const Args &g, const Shape &s, const Put &put, float *
   if (s.parts == 1)
     return launch_tiles<T, kA, kB, kGated>(g, s, Each<Put>{put, g.m, g.n}, stream);
   const uint32_t wide = up8(g.n) * (kGated ? 2 : 1);
-  hipError_t e = launch_tiles<T, kA, kB, kGated>(g, s, Parts{parts, g.m, g.n, wide}, stream);
+  hipError_t e = launch_tiles<T, kA, kB, kGated>(g, s, Parts{parts, g.m, g.n, wide, false}, stream);
   if (e != hipSuccess) return e;
   const uint64_t chunks = (uint64_t)g.m * div_up(g.n, 8);
   join_parts<kGated, Put><<<div_up(chunks, kThreads), kThreads, 0, stream>>>(parts, s.parts, g.m, g.n,
@@ -641,13 +762,21 @@ hipError_t launch_product(const Args &g, const Shape &s, const Put &put, float *
 }
 
 // Results of type O to the caller's rows (any element-aligned address).
+template <bool kWhole, class O>
+__device__ __forceinline__ void put_row(O *row, uint32_t col, uint32_t n, Row8 v) {
+  const Pack<O, 8> w = __builtin_convertvector(v, Pack<O, 8>);
+  if (kWhole) *reinterpret_cast<Pack<O, 8> *>(row + col) = w;
+  else store_pack_tail<O, 8>(row, col, n, w);
+}
+
 template <class O>
 struct ToRows {
   O *out;
   uint64_t ld;
   uint32_t n;
-  __device__ __forceinline__ void operator()(uint32_t row, uint32_t col, Row8 v) const {
-    store_pack_tail<O, 8>(out + row * ld, col, n, __builtin_convertvector(v, Pack<O, 8>));
+  template <bool kWhole>
+  __device__ __forceinline__ void put(uint32_t row, uint32_t col, Row8 v) const {
+    put_row<kWhole>(out + row * ld, col, n, v);
   }
 };
 

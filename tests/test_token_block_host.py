@@ -79,10 +79,12 @@ QUERIES = [(saa.seacells_gated_ffn_workspace, 4), (saa.seacells_gated_ffn_grad_w
 @pytest.mark.parametrize("query,count", QUERIES)
 def test_workspace_queries(query, count):
     for dtype in (torch.float32, torch.float16, torch.bfloat16):
-        some = query(dtype, *[64] * count)
-        assert some > 0
-        # copies only where rows do not start on 16 bytes, or elements are f32
-        assert (query(dtype, *[64] * count, on_16_bytes=True) == some) == (dtype == torch.float32)
+        for n in (1, 64, 65, 500):
+            some = query(dtype, n, *[64] * (count - 1))
+            there = query(dtype, n, *[64] * (count - 1), on_16_bytes=True)
+            assert 0 < there <= some
+            if n > 64:  # copies only where rows do not start on 16 bytes, or elements are f32
+                assert (there == some) == (dtype == torch.float32)
         assert query(dtype, *[60] * count, on_16_bytes=True) > 0
         assert query(dtype, 0, *[64] * (count - 1)) == 0
         for i in range(1, count):
