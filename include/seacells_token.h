@@ -223,7 +223,7 @@ size_t seacells_linear_logprobs_grad_workspace(uint32_t dtype, uint32_t n, uint3
  * (f16: an h past 65504 is an infinity). f32 products are sums of bf16
  * products of the operands' three parts, to f32's accuracy; where an operand
  * holds an infinity, results that depend on it are NaN or infinite.
- * (f + 256) * (d + 7) is below 2^30 (SEACELLS_E_TOO_LARGE).
+ * (f + 256) * (d + 128) is below 2^30 (SEACELLS_E_TOO_LARGE).
  * workspace: seacells_gated_ffn_workspace bytes, 256-byte aligned.
  */
 int seacells_gated_ffn(const void *x, uint32_t dtype, uint32_t n, uint32_t d, uint64_t x_ld,

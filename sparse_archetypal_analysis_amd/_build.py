@@ -11,8 +11,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libseacells_fw.so")
 SOURCES = ["abi.hip", "fw_a.hip", "fw_b.hip", "sparse_ops.hip", "abi_token.hip", "embed.hip",
-           "layer_norm.hip", "logprobs.hip", "mm.hip", "ffn.hip", "linear_logprobs.hip",
-           "few.hip"]
+           "layer_norm.hip", "logprobs.hip", "mm.hip", "ffn.hip", "ffn_grad.hip",
+           "linear_logprobs.hip", "few.hip"]
 HEADERS = ["common.hpp", "token.hpp", "mm.hpp", "few.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -54,7 +54,7 @@ int check_inner(uint32_t n, uint32_t d, uint64_t ld) {
 bool ffn_sizes(uint32_t dtype, uint32_t act, uint32_t n, uint32_t d, uint32_t f, uint32_t m) {
   return dtype_known(dtype) && act <= SEACELLS_ACT_RELU && n < kTooLarge && d > 0 && f > 0 && m > 0 &&
          d <= kMaxInner && f <= kMaxInner && m <= kMaxInner &&
-         (f + 256ull) * (d + 7ull) < (1ull << 30);
+         (f + 256ull) * (d + 128ull) < (1ull << 30);
 }
 
 int check_ffn(const FfnCall &c) {

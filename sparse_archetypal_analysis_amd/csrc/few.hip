@@ -78,23 +78,25 @@ __device__ __forceinline__ void walk(const T *const (&w)[kW], const T *const (&x
   }
 }
 
-// A block has 16 rows of weights (gated: of gate and up each) and all rows of
-// x; its waves split k and join through the LDS.
-template <class T, uint32_t kX, bool kGated, uint32_t kWaves>
+// A block has kTiles times 16 rows of weights (gated: of gate and up each) and
+// all rows of x; its waves split k and join through the LDS. Two tiles a block
+// halve the reads of x, which are as many as the weights' for 32 rows.
+template <class T, uint32_t kX, bool kGated, uint32_t kWaves, uint32_t kTiles>
 __global__ __launch_bounds__(kWaves * kWave) void few_product(FewProduct g) {
-  constexpr uint32_t kW = kGated ? 2 : 1, kThreads = kWaves * kWave;
+  constexpr uint32_t kKinds = kGated ? 2 : 1, kW = kKinds * kTiles, kThreads = kWaves * kWave;
   __shared__ float part[kWaves][kW][kX][256];
   const uint32_t lane = lane_id(), wave = threadIdx.x / kWave, i = lane & 15;
-  const uint32_t base = blockIdx.x * 16;
+  const uint32_t base = blockIdx.x * 16 * kTiles;
   const T *w[kW], *x[kX];
 #pragma unroll
   for (uint32_t q = 0; q < kW; ++q)
-    w[q] = static_cast<const T *>(g.w) + ((uint64_t)q * g.rows + min(base + i, g.rows - 1)) * g.w_ld;
+    w[q] = static_cast<const T *>(g.w) +
+           ((uint64_t)(q / kTiles) * g.rows + min(base + (q % kTiles) * 16 + i, g.rows - 1)) * g.w_ld;
 #pragma unroll
   for (uint32_t t = 0; t < kX; ++t)
     x[t] = static_cast<const T *>(g.x) + (uint64_t)min(t * 16 + i, g.n - 1) * g.x_ld;
   Acc acc[kW][kX] = {};
-  walk<(kGated || kX > 2 ? 4 : 8)>(w, x, g.k, wave, kWaves, acc);
+  walk<(kW > 1 || kX > 2 ? 4 : 8)>(w, x, g.k, wave, kWaves, acc);
   // a lane has rows 4 (lane / 16) + 0..3 of weights and row lane % 16 of x
 #pragma unroll
   for (uint32_t q = 0; q < kW; ++q)
@@ -102,16 +104,16 @@ __global__ __launch_bounds__(kWaves * kWave) void few_product(FewProduct g) {
     for (uint32_t t = 0; t < kX; ++t)
       *reinterpret_cast<Acc *>(&part[wave][q][t][i * 16 + (lane / 16) * 4]) = acc[q][t];
   __syncthreads();
-  for (uint32_t id = threadIdx.x; id < kX * 256; id += kThreads) {
-    const uint32_t t = id / 256, in = id & 255;
-    const uint32_t token = t * 16 + in / 16, row = base + (in & 15);
+  for (uint32_t id = threadIdx.x; id < kTiles * kX * 256; id += kThreads) {
+    const uint32_t in = id & 255, t = (id / 256) % kX, tile = id / 256 / kX;
+    const uint32_t token = t * 16 + in / 16, row = base + tile * 16 + (in & 15);
     if (token >= g.n || row >= g.rows) continue;
-    float s[kW];
+    float s[kKinds];
 #pragma unroll
-    for (uint32_t q = 0; q < kW; ++q) {
+    for (uint32_t q = 0; q < kKinds; ++q) {
       s[q] = 0.0f;
 #pragma unroll
-      for (uint32_t v = 0; v < kWaves; ++v) s[q] += part[v][q][t][in];
+      for (uint32_t v = 0; v < kWaves; ++v) s[q] += part[v][q * kTiles + tile][t][in];
     }
     T *const out = static_cast<T *>(g.out) + token * g.out_ld + row;
     if constexpr (kGated) {
@@ -213,15 +215,19 @@ hipError_t launch_few_product(const FewProduct &g, bool gated, uint32_t dtype, h
       const uint32_t blocks = div_up(g.rows, 16);
       constexpr uint32_t kX = decltype(x)::value;
       typedef decltype(t) T;
-      // (fewer blocks than CUs: more waves each)
+      // fewer blocks than CUs: more waves each; more than two a CU: two tiles each
       if (gated && blocks < 256)
-        few_product<T, kX, true, 16><<<blocks, 16 * kWave, 0, stream>>>(g);
+        few_product<T, kX, true, 16, 1><<<blocks, 16 * kWave, 0, stream>>>(g);
+      else if (gated && (blocks < 512 || kX == 1))
+        few_product<T, kX, true, 8, 1><<<blocks, 8 * kWave, 0, stream>>>(g);
       else if (gated)
-        few_product<T, kX, true, 8><<<blocks, 8 * kWave, 0, stream>>>(g);
+        few_product<T, kX, true, 8, (kX > 2 ? 1 : 2)>
+            <<<kX > 2 ? blocks : (blocks + 1) / 2, 8 * kWave, 0, stream>>>(g);
       else if (blocks < 512)
-        few_product<T, kX, false, 16><<<blocks, 16 * kWave, 0, stream>>>(g);
+        few_product<T, kX, false, 16, 1><<<blocks, 16 * kWave, 0, stream>>>(g);
       else
-        few_product<T, kX, false, 8><<<blocks, 8 * kWave, 0, stream>>>(g);
+        few_product<T, kX, false, 8, (kX > 2 ? 1 : 2)>
+            <<<kX > 2 ? blocks : (blocks + 1) / 2, 8 * kWave, 0, stream>>>(g);
       return hipGetLastError();
     });
   });

@@ -7,13 +7,14 @@
 
 namespace seacells {
 
+constexpr float kInf = __builtin_huge_valf();
+constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
+
 // --- activations ---------------------------------------------------------------
 
-// 1 / (1 + e^-g), from e^-|g| so that neither end overflows.
+// 1 / (1 + e^-g): 0 and 1 at the ends, where e^-g is infinite or 0.
 __device__ __forceinline__ float sigmoid(float g) {
-  const float e = exp_neg(-fabsf(g));
-  const float r = __builtin_amdgcn_rcpf(1.0f + e);
-  return g >= 0.0f ? r : e * r;
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -kLog2E));
 }
 
 // The normal distribution's integral and density (times sqrt(2 pi)) at g:
@@ -57,7 +58,6 @@ __device__ __forceinline__ void act_both(float g, float *a, float *da) {
 
 // --- figures of a row of log probabilities ------------------------------------
 
-constexpr float kInf = __builtin_huge_valf();
 
 // What a row's figures are made of: maximum, sum e^(z - m), sum (z - m) e^(z - m).
 struct Sums {
@@ -81,14 +81,24 @@ __device__ __forceinline__ Sums joined(Sums a, Sums b) {
   return Sums{m, a.s + b.s, a.u + b.u};
 }
 
-// e^-200 is 0: a difference below that, -inf among them, is as good as that
+// e^-200 (and 2^-200) is 0: a difference below that, -inf among them, is as good as that
 // one, and finite. (NaN becomes that too; a row's maximum tells of NaN.)
 __device__ __forceinline__ float not_below(float t) { return fmaxf(t, -200.0f); }
 
 // --- few rows ------------------------------------------------------------------
 
-// Most rows that the kernels for few rows take.
-constexpr uint32_t kFewRows = 64;
+// Whether n rows against weights of `elements` elements in all go to these
+// kernels (at most 64 rows). They read 16 rows of x with 16 of weights, so more
+// rows cost as much as the weights; tiles cost some launches, and f32 a copy of
+// the weights. Weights from memory, us here and by tiles: block of 4096 x 8192
+// bf16 16 rows 54 and 66, 32 rows 65 and 67; 2048 x 16384 32 rows 87 and 67;
+// 1024 x 4096 32 rows 20 and 25, 64 rows 30 and 26; f32 64 rows 57 and 70, 206
+// and 445. Log probabilities of 512 x 50001 bf16 16 rows 22 and 20, 32 rows 30
+// and 20; 100 x 1300 64 rows 12 and 14; f32 64 rows 81 and 96, 14 and 19.
+inline bool few_rows(uint32_t dtype, uint32_t n, uint64_t elements, bool block) {
+  if (n <= 16 || (n <= 64 && dtype == 0u)) return true;
+  return block ? n <= 32 && elements <= (1u << 24) : n <= 64 && elements <= (1u << 18);
+}
 
 // out[n, rows] = x[n, k] w[rows, k]^T, or gated: w has 2 rows, pre [n, 2 rows]
 // (or nullptr) and out = act(gate) * up.

@@ -1,0 +1,214 @@
+// Gradient of the gated feed-forward block (ffn.hip) on gfx950. With g, u the
+// halves of pre and dh = dy W_out:
+//   d_pre = [dh u act'(g), dh act(g)],  dx = d_pre W_in,
+//   dW_in = d_pre^T x,  dW_out = dy^T h,  h = act(g) u.
+// Four products on the matrix cores (mm.hpp); the one that gives dh reads pre
+// and leaves d_pre and h, in x's 16-bit type (f32: three bf16), one rounding of
+// half a step beside the output's own; sums are f32.
+#include <type_traits>
+
+#include "few.hpp"
+#include "mm.hpp"
+
+namespace seacells {
+namespace {
+
+using namespace mm;
+
+// dh to d_pre (its up columns `half` behind the gate's) and h.
+template <class O, Act kAct>
+struct PutPre {
+  const O *pre;
+  uint64_t pre_ld;
+  uint16_t *d_pre, *h;
+  uint64_t d_ld, h_ld, d_plane, h_plane;
+  uint32_t f, half;
+  struct Ahead {
+    Pack<O, 8> g, u;
+  };
+  template <bool kWhole>
+  __device__ __forceinline__ Ahead ahead(uint32_t row, uint32_t col) const {
+    const O *const at = pre + row * pre_ld;
+    Ahead p;
+    if (kWhole || col + 8 <= f) {
+      p.g = *reinterpret_cast<const Pack<O, 8> *>(at + col);
+      p.u = *reinterpret_cast<const Pack<O, 8> *>(at + f + col);
+    } else {
+#pragma unroll
+      for (uint32_t e = 0; e < 8; ++e) {
+        const uint32_t c = min(col + e, f - 1);
+        p.g[e] = at[c];
+        p.u[e] = at[f + c];
+      }
+    }
+    return p;
+  }
+
+  template <bool kWhole>
+  __device__ __forceinline__ void put(uint32_t row, uint32_t col, Row8 dh, const Ahead &p) const {
+    const bool whole = kWhole || col + 8 <= f;
+    const Row8 g = __builtin_convertvector(p.g, Row8), u = __builtin_convertvector(p.u, Row8);
+    Row8 dg, du, v;
+#pragma unroll
+    for (uint32_t e = 0; e < 8; ++e) {
+      float a, da;
+      act_both<kAct>(g[e], &a, &da);
+      const bool in = whole || col + e < f;
+      dg[e] = in ? dh[e] * u[e] * da : 0.0f;
+      du[e] = in ? dh[e] * a : 0.0f;
+      v[e] = in ? a * u[e] : 0.0f;
+    }
+    uint16_t *const to = d_pre + row * d_ld + col;
+    put_operand<O>(to, d_plane, dg);
+    put_operand<O>(to + half, d_plane, du);
+    put_operand<O>(h + row * h_ld + col, h_plane, v);
+  }
+};
+
+// Rows of [gate columns, up columns] of d_pre (`apart` each) to W_in's rows.
+template <class O>
+struct ToGatedRows {
+  typedef void Ahead;
+  O *out;
+  uint64_t ld;
+  uint32_t n, f, apart;
+  template <bool kWhole>
+  __device__ __forceinline__ void put(uint32_t row, uint32_t col, Row8 v) const {
+    const bool up = row >= apart;
+    const uint32_t in = up ? row - apart : row;
+    if (in < f) put_row<kWhole>(out + (uint64_t)(up ? f + in : in) * ld, col, n, v);
+  }
+};
+
+template <class F>
+hipError_t with_act(Act a, F &&f) {
+  switch (a) {
+    case Act::silu:
+      return f(std::integral_constant<Act, Act::silu>{});
+    case Act::gelu:
+      return f(std::integral_constant<Act, Act::gelu>{});
+    default:
+      return f(std::integral_constant<Act, Act::relu>{});
+  }
+}
+
+struct GradRoom {
+  Matrix x, d_out, w_in, w_out;
+  uint16_t *h, *d_pre;
+  float *parts;
+  Pack3 list = {};
+  Shape dh, dx, d_in, d_out_w;
+  size_t bytes;
+};
+
+GradRoom lay_out_grad(const FfnGradCall &c, const bool stays[4], void *ws) {
+  GradRoom r;
+  Room room{static_cast<char *>(ws)};
+  const uint32_t f8 = up8(c.f), half = up64(c.f);
+  r.x = operand(c.x, c.dtype, c.x_ld, c.n, c.d, stays[0], room, r.list);
+  r.d_out = operand(c.d_out, c.dtype, c.d_out_ld, c.n, c.m, stays[1], room, r.list);
+  r.w_in = operand(c.w_in, c.dtype, c.w_in_ld, 2 * c.f, c.d, stays[2], room, r.list);
+  r.w_out = operand(c.w_out, c.dtype, c.w_out_ld, c.m, c.f, stays[3], room, r.list);
+  r.h = static_cast<uint16_t *>(room.take(matrix_bytes(c.dtype, c.n, c.f)));
+  r.d_pre = static_cast<uint16_t *>(room.take(matrix_bytes(c.dtype, c.n, 2 * half)));
+  r.dh = plan_shape(c.n, c.f, tiles_of(c.dtype, 1, up8(c.m)), c.n > 512);
+  r.dx = plan_shape(c.n, c.d, tiles_of(c.dtype, 2, f8));
+  r.d_in = plan_shape(2ull * half, c.d, tiles_of(c.dtype, 1, c.n));
+  r.d_out_w = plan_shape(c.m, c.f, tiles_of(c.dtype, 1, c.n));
+  size_t most = parts_bytes(r.dh, c.n, f8);
+  const size_t more[3] = {parts_bytes(r.dx, c.n, up8(c.d)), parts_bytes(r.d_in, 2ull * half, up8(c.d)),
+                          parts_bytes(r.d_out_w, c.m, f8)};
+  for (size_t b : more) most = b > most ? b : most;
+  r.parts = static_cast<float *>(room.take(most));
+  r.bytes = room.used;
+  return r;
+}
+
+// A matrix of zero rows by d: what a weight's gradient is without rows.
+template <class O>
+__global__ __launch_bounds__(kThreads) void zero_rows(O *out, uint64_t ld, uint64_t rows, uint32_t d) {
+  for (uint64_t id = (uint64_t)blockIdx.x * kThreads + threadIdx.x; id < rows * d;
+       id += (uint64_t)gridDim.x * kThreads) {
+    const uint64_t row = id / d;
+    out[row * ld + (id - row * d)] = (O)0.0f;
+  }
+}
+
+}  // namespace
+
+size_t ffn_grad_workspace(const FfnGradCall &c, bool aligned) {
+  if (c.n == 0) return 0;
+  const bool s = aligned && c.dtype != 0u;
+  const bool stays[4] = {s && c.d % 8 == 0, s && c.m % 8 == 0, s && c.d % 8 == 0, s && c.f % 8 == 0};
+  return lay_out_grad(c, stays, nullptr).bytes;
+}
+
+static void stay(const FfnGradCall &c, bool stays[4]) {
+  stays[0] = in_place(c.x, c.dtype, c.x_ld, c.d);
+  stays[1] = in_place(c.d_out, c.dtype, c.d_out_ld, c.m);
+  stays[2] = in_place(c.w_in, c.dtype, c.w_in_ld, c.d, c.f);
+  stays[3] = in_place(c.w_out, c.dtype, c.w_out_ld, c.f);
+}
+
+size_t ffn_grad_need(const FfnGradCall &c) {
+  if (c.n == 0) return 0;
+  bool stays[4];
+  stay(c, stays);
+  return lay_out_grad(c, stays, nullptr).bytes;
+}
+
+hipError_t launch_ffn_grad(const FfnGradCall &c, void *d_x, uint64_t d_x_ld, void *d_w_in,
+                           uint64_t d_w_in_ld, void *d_w_out, uint64_t d_w_out_ld, void *ws,
+                           hipStream_t stream) {
+  const uint32_t f8 = up8(c.f), m8 = up8(c.m), half = up64(c.f);
+  const uint32_t h_ld = apart64(c.f), d_ld = apart64(2 * half);
+  if (c.n == 0)
+    return with_type(c.dtype, [&](auto o) {
+      typedef decltype(o) O;
+      if (d_w_in != nullptr)
+        zero_rows<O><<<1024, kThreads, 0, stream>>>(static_cast<O *>(d_w_in), d_w_in_ld, 2ull * c.f, c.d);
+      if (d_w_out != nullptr)
+        zero_rows<O><<<1024, kThreads, 0, stream>>>(static_cast<O *>(d_w_out), d_w_out_ld, c.m, c.f);
+      return hipGetLastError();
+    });
+  bool stays[4];
+  stay(c, stays);
+  const GradRoom r = lay_out_grad(c, stays, ws);
+  hipError_t e = launch_pack(r.list, c.dtype, stream);
+  if (e != hipSuccess) return e;
+  const uint64_t h_plane = (uint64_t)c.n * h_ld, d_plane = (uint64_t)c.n * d_ld;
+  const Matrix h = {r.h, h_ld, h_plane}, d_pre = {r.d_pre, d_ld, d_plane};
+  return with_types(c.dtype, [&](auto o, auto t) {
+    typedef decltype(o) O;
+    typedef decltype(t) T;
+    hipError_t rc = with_act(c.act, [&](auto a) {
+      const Args g = make_args(c.dtype, r.d_out, r.w_out, c.n, c.f, m8, c.m, 1, nullptr, nullptr,
+                               r.dh, c.f);
+      const PutPre<O, decltype(a)::value> put = {static_cast<const O *>(c.pre), c.pre_ld, r.d_pre, r.h,
+                                                 d_ld, h_ld, d_plane, h_plane, c.f, half};
+      return launch_product<T, kAlongK, kAcrossK, false>(g, r.dh, put, r.parts, stream);
+    });
+    if (rc == hipSuccess && d_x != nullptr) {
+      const uint64_t a_base[2] = {0, half}, b_base[2] = {0, (uint64_t)c.f * r.w_in.ld};
+      const Args g = make_args(c.dtype, d_pre, r.w_in, c.n, c.d, f8, c.f, 2, a_base, b_base, r.dx, c.d);
+      rc = launch_product<T, kAlongK, kAcrossK, false>(
+          g, r.dx, ToRows<O>{static_cast<O *>(d_x), d_x_ld, c.d}, r.parts, stream);
+    }
+    if (rc == hipSuccess && d_w_in != nullptr) {
+      const Args g = make_args(c.dtype, d_pre, r.x, 2 * half, c.d, c.n, c.n, 1, nullptr, nullptr, r.d_in,
+                               c.d);
+      rc = launch_product<T, kAcrossK, kAcrossK, false>(
+          g, r.d_in, ToGatedRows<O>{static_cast<O *>(d_w_in), d_w_in_ld, c.d, c.f, half}, r.parts,
+          stream);
+    }
+    if (rc == hipSuccess && d_w_out != nullptr) {
+      const Args g = make_args(c.dtype, r.d_out, h, c.m, c.f, c.n, c.n, 1, nullptr, nullptr, r.d_out_w,
+                               c.f);
+      rc = launch_product<T, kAcrossK, kAcrossK, false>(
+          g, r.d_out_w, ToRows<O>{static_cast<O *>(d_w_out), d_w_out_ld, c.f}, r.parts, stream);
+    }
+    return rc;
+  });
+}
+
+}  // namespace seacells

@@ -39,8 +39,8 @@ struct Logits {
     }
   }
   __device__ __forceinline__ float of(const Acc &acc, uint32_t j, uint32_t e) const {
-    if (kPlain) return acc[e];
-    return bias[j][e] == -kInf ? -kInf : acc[e] + bias[j][e];
+    const float z = result(acc, e);
+    return kPlain ? z : bias[j][e] == -kInf ? -kInf : z + bias[j][e];
   }
 };
 
@@ -52,25 +52,25 @@ struct RowSums {
   float *at_target;        // [rows]
   uint32_t rows, n;
 
-  template <bool kPlain, uint32_t kSubM, uint32_t kSubN>
-  __device__ __forceinline__ void go(const Acc (&acc)[kSubM][kSubN], uint32_t row0,
+  template <bool kPlain, uint32_t kSub>
+  __device__ __forceinline__ void go(const Acc (&acc)[kSub][kSub], uint32_t row0,
                                      uint32_t col0) const {
     const uint32_t lane = lane_id();
-    Logits<kPlain, kSubN> logits;
+    Logits<kPlain, kSub> logits;
     logits.load(bias, col0, n);
-    float *const out = sums + (uint64_t)(col0 / (kSubN * 16)) * 3 * rows;
-    uint32_t in[kSubM];  // the target's place among the wave's columns
+    float *const out = sums + (uint64_t)(col0 / (kSub * 16)) * 3 * rows;
+    uint32_t in[kSub];  // the target's place among the wave's columns
 #pragma unroll
-    for (uint32_t i = 0; i < kSubM; ++i) {
+    for (uint32_t i = 0; i < kSub; ++i) {
       const uint32_t row = row0 + outer_of(i, lane & 15);
       in[i] = targets != nullptr ? (uint32_t)targets[min(row, rows - 1)] - col0 : ~0u;
     }
 #pragma unroll
-    for (uint32_t i = 0; i < kSubM; ++i) {
+    for (uint32_t i = 0; i < kSub; ++i) {
       const uint32_t row = row0 + outer_of(i, lane & 15);
-      float z[kSubN][4], m = -kInf;
+      float z[kSub][4], m = -kInf;
 #pragma unroll
-      for (uint32_t j = 0; j < kSubN; ++j)
+      for (uint32_t j = 0; j < kSub; ++j)
 #pragma unroll
         for (uint32_t e = 0; e < 4; ++e) {
           z[j][e] = logits.of(acc[i][j], j, e);
@@ -81,15 +81,16 @@ struct RowSums {
       const float base = m == -kInf ? 0.0f : m;
       float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (uint32_t j = 0; j < kSubN; ++j)
+      for (uint32_t j = 0; j < kSub; ++j)
 #pragma unroll
         for (uint32_t e = 0; e < 4; ++e) {
-          const float t = not_below(z[j][e] - base);
-          const float x = exp_neg(t);
+          // (in powers of 2; the difference first, so that any z of f32 will do)
+          const float t = not_below((z[j][e] - base) * kLog2E);
+          const float x = __builtin_amdgcn_exp2f(t);
           s[e] += x;
           u[e] = fmaf(t, x, u[e]);
         }
-      float s1 = (s[0] + s[1]) + (s[2] + s[3]), u1 = (u[0] + u[1]) + (u[2] + u[3]);
+      float s1 = (s[0] + s[1]) + (s[2] + s[3]), u1 = ((u[0] + u[1]) + (u[2] + u[3])) * kLn2;
       s1 += __shfl_xor(s1, 16, kWave);
       u1 += __shfl_xor(u1, 16, kWave);
       s1 += __shfl_xor(s1, 32, kWave);
@@ -99,9 +100,9 @@ struct RowSums {
         out[(uint64_t)rows + row] = s1;
         out[2ull * rows + row] = u1;
       }
-      if (in[i] < kSubN * 16 && row < rows && col0 + in[i] < n) {
+      if (in[i] < kSub * 16 && row < rows && col0 + in[i] < n) {
 #pragma unroll
-        for (uint32_t j = 0; j < kSubN; ++j)
+        for (uint32_t j = 0; j < kSub; ++j)
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e)
             if (in[i] == outer_of(j, (lane / 16) * 4) + e) at_target[row] = z[j][e];
@@ -109,8 +110,8 @@ struct RowSums {
     }
   }
 
-  template <bool kGated, uint32_t kSubM, uint32_t kSubN>
-  __device__ __forceinline__ void run(const Acc (&acc)[kSubM][kSubN], uint32_t row0, uint32_t col0,
+  template <bool kGated, uint32_t kSub>
+  __device__ __forceinline__ void run(const Acc (&acc)[kSub][kSub], uint32_t row0, uint32_t col0,
                                       bool whole, uint32_t) const {
     if (whole && bias == nullptr) go<true>(acc, row0, col0);
     else go<false>(acc, row0, col0);
@@ -216,23 +217,23 @@ struct PutDz {
   float *column_sums;  // [half tiles of rows][ld], or nullptr
   uint32_t rows, n, first, classes;
 
-  template <bool kPlain, uint32_t kSubM, uint32_t kSubN>
-  __device__ __forceinline__ void go(const Acc (&acc)[kSubM][kSubN], uint32_t row0,
+  template <bool kPlain, uint32_t kSub>
+  __device__ __forceinline__ void go(const Acc (&acc)[kSub][kSub], uint32_t row0,
                                      uint32_t col0) const {
     const uint32_t lane = lane_id();
-    Logits<kPlain, kSubN> logits;
+    Logits<kPlain, kSub> logits;
     logits.load(bias, col0, n);
-    float sum[kSubN][4];
+    float sum[kSub][4];
 #pragma unroll
-    for (uint32_t j = 0; j < kSubN; ++j)
+    for (uint32_t j = 0; j < kSub; ++j)
 #pragma unroll
       for (uint32_t e = 0; e < 4; ++e) sum[j][e] = 0.0f;
     const float by = scale != nullptr ? scale[0] : 1.0f;
     // the rows' figures, all in flight together
-    float m[kSubM], ls[kSubM], g[kSubM], h[kSubM], gh[kSubM];
-    uint32_t hit[kSubM];
+    float m[kSub], ls[kSub], g[kSub], h[kSub], gh[kSub];
+    uint32_t hit[kSub];
 #pragma unroll
-    for (uint32_t i = 0; i < kSubM; ++i) {
+    for (uint32_t i = 0; i < kSub; ++i) {
       const uint32_t r = min(row0 + outer_of(i, lane & 15), rows - 1);
       m[i] = stats[2ull * r];
       ls[i] = stats[2ull * r + 1];
@@ -242,40 +243,42 @@ struct PutDz {
       gh[i] = d_entropy != nullptr ? entropy[r] : 0.0f;
     }
 #pragma unroll
-    for (uint32_t i = 0; i < kSubM; ++i) {
+    for (uint32_t i = 0; i < kSub; ++i) {
       g[i] = hit[i] < classes ? g[i] : 0.0f;
       gh[i] = m[i] == m[i] ? fmaf(h[i], gh[i], g[i]) : m[i];  // no distribution: NaN
+      ls[i] *= kLog2E;  // (log p in powers of 2)
+      h[i] *= kLn2;
       hit[i] -= first;
       if (bias != nullptr && hit[i] < n && bias[hit[i]] == -kInf) hit[i] = ~0u;  // masked
       hit[i] = hit[i] < n ? hit[i] - col0 : ~0u;
     }
 #pragma unroll
-    for (uint32_t i = 0; i < kSubM; ++i) {
+    for (uint32_t i = 0; i < kSub; ++i) {
       const uint32_t row = row0 + outer_of(i, lane & 15);
       const bool in_row = row < rows;
-      float d[kSubN][4];
+      float d[kSub][4];
 #pragma unroll
-      for (uint32_t j = 0; j < kSubN; ++j)
+      for (uint32_t j = 0; j < kSub; ++j)
 #pragma unroll
         for (uint32_t e = 0; e < 4; ++e) {
-          const float lp = not_below(logits.of(acc[i][j], j, e) - m[i] - ls[i]);
-          d[j][e] = -exp_neg(lp) * fmaf(h[i], lp, gh[i]);
+          const float lp = not_below(fmaf(logits.of(acc[i][j], j, e) - m[i], kLog2E, -ls[i]));
+          d[j][e] = -__builtin_amdgcn_exp2f(lp) * fmaf(h[i], lp, gh[i]);
         }
-      if (hit[i] < kSubN * 16) {
+      if (hit[i] < kSub * 16) {
 #pragma unroll
-        for (uint32_t j = 0; j < kSubN; ++j)
+        for (uint32_t j = 0; j < kSub; ++j)
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e)
             if (hit[i] == outer_of(j, (lane / 16) * 4) + e) d[j][e] += g[i];
       }
       if (column_sums != nullptr && in_row) {
 #pragma unroll
-        for (uint32_t j = 0; j < kSubN; ++j)
+        for (uint32_t j = 0; j < kSub; ++j)
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e) sum[j][e] += d[j][e];
       }
 #pragma unroll
-      for (uint32_t j = 0; j < kSubN; j += 2) {
+      for (uint32_t j = 0; j < kSub; j += 2) {
         const uint32_t col = col0 + outer_of(j, (lane / 16) * 4);
         Row8 v;
 #pragma unroll
@@ -284,9 +287,9 @@ struct PutDz {
       }
     }
     if (column_sums == nullptr) return;
-    float *const to = column_sums + (uint64_t)(row0 / (kSubM * 16)) * ld;
+    float *const to = column_sums + (uint64_t)(row0 / (kSub * 16)) * ld;
 #pragma unroll
-    for (uint32_t j = 0; j < kSubN; ++j) {
+    for (uint32_t j = 0; j < kSub; ++j) {
       Acc s;
 #pragma unroll
       for (uint32_t e = 0; e < 4; ++e) s[e] = group_sum<16>(sum[j][e]);
@@ -295,8 +298,8 @@ struct PutDz {
     }
   }
 
-  template <bool kGated, uint32_t kSubM, uint32_t kSubN>
-  __device__ __forceinline__ void run(const Acc (&acc)[kSubM][kSubN], uint32_t row0, uint32_t col0,
+  template <bool kGated, uint32_t kSub>
+  __device__ __forceinline__ void run(const Acc (&acc)[kSub][kSub], uint32_t row0, uint32_t col0,
                                       bool whole, uint32_t) const {
     if (whole && bias == nullptr) go<true>(acc, row0, col0);
     else go<false>(acc, row0, col0);
@@ -306,6 +309,7 @@ struct PutDz {
 // Results of d_z times its scale to the caller's rows.
 template <class O>
 struct ToScaledRows {
+  typedef void Ahead;
   O *out;
   uint64_t ld;
   uint32_t n;
@@ -352,10 +356,12 @@ struct LossRoom {
   size_t bytes;
 };
 
+bool few(const LossCall &c) { return few_rows(c.dtype, c.n, (uint64_t)c.d * c.v, false); }
+
 LossRoom lay_out(const LossCall &c, bool x_stays, bool table_stays, void *ws) {
   LossRoom r;
   Room room{static_cast<char *>(ws)};
-  if (c.n <= kFewRows) {
+  if (few(c)) {
     r.rows = c.n;
     r.sums = static_cast<float *>(room.take((size_t)c.n * 12 * few_slices(c.v)));
     r.at_target = static_cast<float *>(room.take((size_t)c.n * 4));
@@ -368,8 +374,7 @@ LossRoom lay_out(const LossCall &c, bool x_stays, bool table_stays, void *ws) {
   uint64_t rows = kSumsBytes / a_row / 256 * 256;
   if (rows < 4096) rows = 4096;
   r.rows = rows < c.n ? (uint32_t)rows : c.n;
-  r.shape = plan_shape(r.rows, c.v, tiles_of(c.dtype, 1, up8(c.d)));
-  if (r.shape.parts > 1) r.shape = Shape{128, 1, tiles_of(c.dtype, 1, up8(c.d))};
+  r.shape = plan_shape(r.rows, c.v, tiles_of(c.dtype, 1, up8(c.d)), true);
   r.sums = static_cast<float *>(
       room.take((size_t)r.rows * 12 * 2 * div_up(c.v, r.shape.tile)));
   r.at_target = static_cast<float *>(room.take((size_t)r.rows * 4));
@@ -404,11 +409,10 @@ LossGradRoom lay_out_grad(const LossGradCall &c, bool x_stays, bool table_stays,
   // pieces of equal size
   piece = (div_up(c.v, count) + 255) / 256 * 256;
   r.piece = piece < c.v ? (uint32_t)piece : c.v;
-  r.dz_ld = up64(r.piece);
+  r.dz_ld = apart64(r.piece);
   r.dz = static_cast<uint16_t *>(room.take(matrix_bytes(c.dtype, c.n, r.piece)));
   const uint32_t tiles = tiles_of(c.dtype, 1, up8(c.d));
-  r.z = plan_shape(c.n, r.piece, tiles);
-  if (r.z.parts > 1) r.z = Shape{128, 1, tiles};
+  r.z = plan_shape(c.n, r.piece, tiles, true);
   r.dx = plan_shape(c.n, c.d, tiles_of(c.dtype, 1, up8(r.piece)));
   r.dt = plan_shape(r.piece, c.d, tiles_of(c.dtype, 1, c.n));
   const size_t a = d_x ? (size_t)r.dx.parts * c.n * up8(c.d) * 4 : 0;
@@ -451,10 +455,9 @@ hipError_t launch_loss(const LossCall &c, float *logp, float *entropy, float *st
   const uint32_t d8 = up8(c.d);
   for (uint64_t i = 0; e == hipSuccess && (i < c.n || i == 0); i += r.rows) {
     const uint32_t rows = (uint32_t)(c.n - i < r.rows ? c.n - i : r.rows);
-    const bool few = c.n <= kFewRows;
-    const uint32_t slices = few ? few_slices(c.v) : 2 * div_up(c.v, r.shape.tile);
+    const uint32_t slices = few(c) ? few_slices(c.v) : 2 * div_up(c.v, r.shape.tile);
     const int32_t *const targets = c.targets == nullptr ? nullptr : c.targets + i;
-    if (few && rows > 0) {
+    if (few(c) && rows > 0) {
       const FewSums sums = {c.x, c.table, c.bias, targets, r.sums, r.at_target, c.x_ld, c.table_ld,
                             rows, c.d, c.v};
       if ((e = launch_few_sums(sums, c.dtype, stream)) != hipSuccess) break;

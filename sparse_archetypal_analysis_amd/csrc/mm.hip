@@ -45,7 +45,7 @@ hipError_t launch_pack(const Pack3 &list, uint32_t dtype, hipStream_t stream) {
   });
 }
 
-Shape plan_shape(uint64_t m, uint64_t n, uint32_t tiles) {
+Shape plan_shape(uint64_t m, uint64_t n, uint32_t tiles, bool heavy) {
   Shape best = {256, 1, tiles};
   double least = 0.0;
   for (uint32_t tile = 256; tile >= 128; tile /= 2) {
@@ -54,17 +54,15 @@ Shape plan_shape(uint64_t m, uint64_t n, uint32_t tiles) {
       uint32_t per = (tiles + parts - 1) / parts;
       per += per & 1;  // (a block goes by two tiles)
       const uint32_t real = (tiles + per - 1) / per;
-      if (parts > 1 && per < 16) break;
+      if (parts > 1 && (per < 16 || heavy)) break;
       const uint64_t blocks = count * real;
       double t;
-      if (tile == 256) {
-        t = (double)((blocks + 255) / 256) * (8000.0 + 735.0 * per);
-      } else {
-        const uint64_t full = blocks / 512, rest = blocks % 512;
-        t = (double)full * (3500.0 + 555.0 * per);
-        if (rest > 256) t += 6000.0 + 555.0 * per;
-        else if (rest > 0) t += 5000.0 + 317.0 * per;
-      }
+      if (tile == 256)
+        t = (double)((blocks + 255) / 256) * ((heavy ? 18000.0 : 8000.0) + 690.0 * per);
+      else if (blocks > 256)
+        t = ((double)blocks / 512 + (blocks > 512 ? 0.25 : 0.5)) * ((heavy ? 8500.0 : 3500.0) + 440.0 * per);
+      else
+        t = (heavy ? 10000.0 : 5000.0) + 300.0 * per;
       if (real > 1) t += 3000.0 + (double)(m * n) * 4.0 * (2.0 * real) / 3500.0;
       if (least == 0.0 || t < least) {
         least = t;

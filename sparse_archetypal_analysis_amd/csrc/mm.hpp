@@ -461,41 +461,79 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void product(Args g
 
 // --- what becomes of the results ---------------------------------------------
 
-// A lane's results of a tile of fragments: row, and 8 neighbouring columns.
+// One result. Read where it is used: left to itself the compiler moves all 256
+// out of the accumulation registers first, and has none left to work with.
+__device__ __forceinline__ float result(const Acc &acc, uint32_t e) {
+  float x;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(x) : "a"(acc[e]));
+  return x;
+}
+
+// A lane's results of two neighbouring tiles: 8 columns of a row.
 __device__ __forceinline__ Row8 eight(const Acc &lo, const Acc &hi) {
-  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  Row8 v;
+#pragma unroll
+  for (uint32_t e = 0; e < 8; ++e) v[e] = result(e < 4 ? lo : hi, e & 3);
+  return v;
 }
 
 // put<whole>(row, col, v) for every 8 results inside of m rows and n columns, or
 // put<whole>(row, col, gate, up) for those of a gated product. whole: all 8 are.
+// A Put that reads (Put::Ahead is not void) has ahead<whole>(row, col) called a
+// row of fragments before, and its result given to put. (dh of 16384 x 8192 x
+// 2048 bf16: 490 us without what it reads and writes, 750 with 1.34 GB of it at
+// 5 TB/s; four rows ahead 770.)
 template <class Put>
 struct Each {
   Put put;
   uint32_t m, n;
 
-  template <bool kGated, bool kWhole, uint32_t kSubM, uint32_t kSubN>
-  __device__ __forceinline__ void go(const Acc (&acc)[kSubM][kSubN], uint32_t row0,
+  template <bool kGated, bool kWhole, uint32_t kSub>
+  __device__ __forceinline__ void go(const Acc (&acc)[kSub][kSub], uint32_t row0,
                                      uint32_t col0) const {
+    constexpr uint32_t kChunks = kGated ? kSub / 4 : kSub / 2;
+    constexpr bool kReads = !std::is_void<typename Put::Ahead>::value;
+    typedef typename std::conditional<kReads, typename Put::Ahead, int>::type Ahead;
     const uint32_t lane = lane_id();
+    auto row_of = [&](uint32_t i) { return row0 + outer_of(i, lane & 15); };
+    auto col_of = [&](uint32_t q) { return col0 + outer_of(2 * q, (lane / 16) * 4); };
+    Ahead next[kChunks];
+    auto look = [&](uint32_t i) {
+      if constexpr (kReads) {
 #pragma unroll
-    for (uint32_t i = 0; i < kSubM; ++i) {
-      const uint32_t row = row0 + outer_of(i, lane & 15);
-      if (!kWhole && row >= m) continue;
-#pragma unroll
-      for (uint32_t j = 0; j < (kGated ? kSubN / 2 : kSubN); j += 2) {
-        const uint32_t col = col0 + outer_of(j, (lane / 16) * 4);
-        if (!kWhole && col >= n) continue;
-        if constexpr (kGated)
-          put.template put<kWhole>(row, col, eight(acc[i][j], acc[i][j + 1]),
-                                   eight(acc[i][j + kSubN / 2], acc[i][j + kSubN / 2 + 1]));
-        else
-          put.template put<kWhole>(row, col, eight(acc[i][j], acc[i][j + 1]));
+        for (uint32_t q = 0; q < kChunks; ++q)
+          next[q] = put.template ahead<kWhole>(kWhole ? row_of(i) : min(row_of(i), m - 1), col_of(q));
       }
-    }
+    };
+    look(0);
+    each<kSub>([&](auto index) {
+      constexpr uint32_t i = decltype(index)::value;
+      Ahead now[kChunks];
+      if constexpr (kReads) {
+#pragma unroll
+        for (uint32_t q = 0; q < kChunks; ++q) now[q] = next[q];
+        if constexpr (i + 1 < kSub) look(i + 1);
+      }
+      const uint32_t row = row_of(i);
+      if (!kWhole && row >= m) return;
+#pragma unroll
+      for (uint32_t q = 0; q < kChunks; ++q) {
+        const uint32_t col = col_of(q);
+        if (!kWhole && col >= n) continue;
+        const Row8 v = eight(acc[i][2 * q], acc[i][2 * q + 1]);
+        if constexpr (kGated)
+          put.template put<kWhole>(row, col, v,
+                                   eight(acc[i][2 * q + kSub / 2], acc[i][2 * q + 1 + kSub / 2]));
+        else if constexpr (kReads)
+          put.template put<kWhole>(row, col, v, now[q]);
+        else
+          put.template put<kWhole>(row, col, v);
+      }
+    });
   }
 
-  template <bool kGated, uint32_t kSubM, uint32_t kSubN>
-  __device__ __forceinline__ void run(const Acc (&acc)[kSubM][kSubN], uint32_t row0, uint32_t col0,
+  template <bool kGated, uint32_t kSub>
+  __device__ __forceinline__ void run(const Acc (&acc)[kSub][kSub], uint32_t row0, uint32_t col0,
                                       bool whole, uint32_t) const {
     if (whole) go<kGated, true>(acc, row0, col0);
     else go<kGated, false>(acc, row0, col0);
@@ -561,8 +599,12 @@ __global__ __launch_bounds__(kThreads) void join_parts(const float *__restrict__
     a += *reinterpret_cast<const Row8 *>(at);
     if (kGated) b += *reinterpret_cast<const Row8 *>(at + wide / 2);
   }
-  if constexpr (kGated) put.template put<false>(row, col, a, b);
-  else put.template put<false>(row, col, a);
+  if constexpr (kGated)
+    put.template put<false>(row, col, a, b);
+  else if constexpr (!std::is_void<typename Put::Ahead>::value)
+    put.template put<false>(row, col, a, put.template ahead<false>(row, col));
+  else
+    put.template put<false>(row, col, a);
 }
 
 // --- f32 as three 16-bit numbers ---------------------------------------------
@@ -620,9 +662,12 @@ inline uint32_t up8(uint32_t x) { return (x + 7u) & ~7u; }
 // A row of the workspace's matrices starts on a cache line (8192 x 4096 x 16384
 // bf16 780 us, with rows on half lines 930).
 inline uint32_t up64(uint32_t x) { return (x + 63u) & ~63u; }
+// One that only products here read: and not all rows on the same memory channels
+// (8192 x 4096 x 16384 803 us with rows 32 KB apart, 784 with 128 bytes more).
+inline uint32_t apart64(uint32_t x) { return up64(x) + (up64(x) % 2048 == 0 ? 64u : 0u); }
 inline uint64_t planes_of(uint32_t dtype) { return dtype == 0u ? kPlanes : 1u; }
 inline uint64_t matrix_bytes(uint32_t dtype, uint64_t rows, uint32_t len) {
-  return align_up(rows * up64(len) * 2 * planes_of(dtype), 256);
+  return align_up(rows * apart64(len) * 2 * planes_of(dtype), 256);
 }
 
 // Longest row of an operand, and most bytes between the rows of one tile:
@@ -667,7 +712,7 @@ struct Room {
 inline Matrix operand(const void *p, uint32_t dtype, uint64_t ld, uint32_t rows, uint32_t len,
                       bool stays, Room &room, Pack3 &list) {
   if (stays) return Matrix{static_cast<const uint16_t *>(p), ld, 0};
-  const uint32_t wide = up64(len), chunks = up8(len) / 8;
+  const uint32_t wide = apart64(len), chunks = up8(len) / 8;
   const uint64_t plane = (uint64_t)rows * wide;
   uint16_t *const to = static_cast<uint16_t *>(room.take(matrix_bytes(dtype, rows, len)));
   list.item[list.count++] = PackItem{p, ld, to, (uint64_t)rows * chunks, wide, plane, chunks, len};
@@ -676,14 +721,14 @@ inline Matrix operand(const void *p, uint32_t dtype, uint64_t ld, uint32_t rows,
 
 // How a product of m x n results over `tiles` tiles of k is spread over the
 // card: the least time by what rounds of blocks take, measured (ns, bf16): of
-// 256 x 256 tiles (one a CU) 8000 + 735 a step of 32 k; of 256 x 128 (two a CU)
-// 7000 + 865, with one a CU 7000 + 630; of 128 x 128 (two) 3500 + 555, with one
-// 5000 + 317. Parts of k fill the card where tiles are few; their sums are
-// written and read once more.
+// 256 x 256 tiles (one a CU) 8000 + 690 a step of 32 k; of 128 x 128 (two a CU)
+// 3500 + 440, with one a CU 5000 + 300. Parts of k fill the card where tiles
+// are few; their sums are written and read once more. heavy: the results are
+// worked on (10000 and 5000 a round more), in one part of k.
 struct Shape {
   uint32_t tile, parts, per_part;
 };
-Shape plan_shape(uint64_t m, uint64_t n, uint32_t tiles);
+Shape plan_shape(uint64_t m, uint64_t n, uint32_t tiles, bool heavy = false);
 
 inline size_t parts_bytes(const Shape &s, uint64_t m, uint64_t wide) {
   return s.parts > 1 ? s.parts * m * wide * 4 : 0;
@@ -771,6 +816,7 @@ __device__ __forceinline__ void put_row(O *row, uint32_t col, uint32_t n, Row8 v
 
 template <class O>
 struct ToRows {
+  typedef void Ahead;
   O *out;
   uint64_t ld;
   uint32_t n;

@@ -313,6 +313,32 @@ def test_every_class_masked(dtype):
     assert not dx.any() and not dt.any() and not db.any()
 
 
+@pytest.mark.parametrize("n", [3, 200])
+@pytest.mark.parametrize("level", [-3.4028234e38, -1e30, 3e38])
+def test_biases_of_the_types_ends(n, level):
+    """Every class shifted as far as f32 goes: the classes are equally likely,
+    whatever their z was, as where logits are masked by the lowest value."""
+    rng = np.random.default_rng(6)
+    x, table, b = head(rng, n, 40, 300, "bf16", "plain")
+    b.fill_(level)
+    tgt = classes(rng, n, 300)
+    logp, H, stats = check_loss(x, table, b, tgt, "bf16")
+    assert bool((H - math.log(300)).abs().max() < 1e-5)
+    one = torch.ones(n, device="cuda")
+    got = saa.seacells_linear_logprobs_grad(x, table, tgt, stats, H, one, one, b)
+    want, bounds = R.loss_grad(exact(x), exact(table), exact(b), exact(tgt), exact(stats), exact(H),
+                               np.ones(n), np.ones(n), "bf16")
+    for what, g in zip(("d_x", "d_table", "d_bias"), got):
+        assert bool(g.isfinite().all()), what
+    # p is 1 / 300 to its rounding: z and m are the same number
+    p = np.full((n, 300), 1.0 / 300)
+    dz = -p
+    t = exact(tgt)
+    dz[t < 0] = 0.0
+    dz[np.nonzero(t >= 0)[0], t[t >= 0]] += 1.0
+    assert np.abs(exact(got[2]) - dz.sum(axis=0)).max() < 1e-4 * n
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_masked_classes_have_no_part(dtype):
     """What a masked class' row holds reaches no output but its own d_table;
