@@ -175,7 +175,8 @@ __global__ __launch_bounds__(kThreads) void join_rows(const float *__restrict__ 
 // f16 holds 2^-24 to 2^15; d_z of a mean over rows is far below that. It is
 // kept times a power of two that takes its bound, max |d_logp| + 17 |d_entropy|
 // (p |log p + H| <= 0.4 + log v), to below 2^15. Also reports targets past the
-// classes. One block.
+// classes (without a scale the first product's first block does, where targets
+// are few enough to hide beside the others' work). One block.
 constexpr uint32_t kPrepare = 1024;
 __global__ __launch_bounds__(kPrepare) void prepare_rows(const int32_t *__restrict__ targets,
                                                          const float *__restrict__ d_logp,
@@ -216,6 +217,7 @@ struct PutDz {
   uint64_t ld, plane;
   float *column_sums;  // [half tiles of rows][ld], or nullptr
   uint32_t rows, n, first, classes;
+  uint32_t *status;  // or nullptr: not reported here
 
   template <bool kPlain, uint32_t kSub>
   __device__ __forceinline__ void go(const Acc (&acc)[kSub][kSub], uint32_t row0,
@@ -303,6 +305,7 @@ struct PutDz {
                                       bool whole, uint32_t) const {
     if (whole && bias == nullptr) go<true>(acc, row0, col0);
     else go<false>(acc, row0, col0);
+    if (status != nullptr && blockIdx.x == 0) report_ids<kThreads>(targets, rows, classes, status);
   }
 };
 
@@ -321,15 +324,23 @@ struct ToScaledRows {
   }
 };
 
-// d_bias of a piece: the tiles' column sums, in order.
+// d_bias of a piece: the tiles' column sums, 16 columns and 16 parts of the
+// tiles a block, then the parts in order.
 __global__ __launch_bounds__(kThreads) void join_columns(const float *__restrict__ sums,
                                                          uint32_t slices, uint64_t ld, uint32_t n,
                                                          float *__restrict__ out) {
-  const uint32_t col = blockIdx.x * kThreads + threadIdx.x;
-  if (col >= n) return;
+  __shared__ float part[16][17];
+  const uint32_t in = threadIdx.x & 15, lane = threadIdx.x / 16, col = blockIdx.x * 16 + in;
+  const uint32_t each = (slices + 15) / 16;
   float a = 0.0f;
-#pragma unroll 8
-  for (uint32_t k = 0; k < slices; ++k) a += sums[k * ld + col];
+  if (col < n) {
+#pragma unroll 4
+    for (uint32_t k = lane * each; k < min(slices, (lane + 1) * each); ++k) a += sums[k * ld + col];
+  }
+  part[lane][in] = a;
+  __syncthreads();
+  if (lane > 0 || col >= n) return;
+  for (uint32_t k = 1; k < 16; ++k) a += part[k][in];
   out[col] = a;
 }
 
@@ -513,8 +524,11 @@ hipError_t launch_loss_grad(const LossGradCall &c, void *d_x, uint64_t d_x_ld, v
   if (e != hipSuccess) return e;
   const bool scaled = static_cast<Dtype>(c.dtype) == Dtype::f16;
   float *const scale = scaled ? r.scale : nullptr;
-  prepare_rows<<<1, kPrepare, 0, stream>>>(c.targets, c.d_logp, c.d_entropy, c.n, c.v, scale, status);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const bool apart = scaled || c.targets == nullptr || c.n > 32768;
+  if (apart) {
+    prepare_rows<<<1, kPrepare, 0, stream>>>(c.targets, c.d_logp, c.d_entropy, c.n, c.v, scale, status);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   const uint64_t plane = (uint64_t)c.n * r.dz_ld;
   const Matrix dz = {r.dz, r.dz_ld, plane};
   const uint32_t d8 = up8(c.d);
@@ -542,12 +556,13 @@ hipError_t launch_loss_grad(const LossGradCall &c, void *d_x, uint64_t d_x_ld, v
                               c.n,
                               n,
                               first,
-                              c.v};
+                              c.v,
+                              apart || first > 0 ? nullptr : status};
         rc = launch_tiles<T, kAlongK, kAlongK, false>(g, r.z, put, stream);
         if (rc != hipSuccess) break;
         if (d_bias != nullptr) {
           const uint32_t slices = 2 * div_up(c.n, r.z.tile);
-          join_columns<<<div_up(n, kThreads), kThreads, 0, stream>>>(r.columns, slices, r.dz_ld, n,
+          join_columns<<<div_up(n, 16), kThreads, 0, stream>>>(r.columns, slices, r.dz_ld, n,
                                                                      d_bias + first);
           if ((rc = hipGetLastError()) != hipSuccess) break;
         }
@@ -566,12 +581,8 @@ hipError_t launch_loss_grad(const LossGradCall &c, void *d_x, uint64_t d_x_ld, v
         } else {
           rc = launch_tiles<T, kAlongK, kAcrossK, false>(
               g, s, Parts{r.parts, c.n, c.d, d8, first > 0}, stream);
-          if (rc == hipSuccess && first + n == c.v) {
-            const uint64_t chunks = (uint64_t)c.n * div_up(c.d, 8);
-            join_parts<false><<<div_up(chunks, kThreads), kThreads, 0, stream>>>(
-                r.parts, r.dx.parts, c.n, c.d, d8, to);
-            rc = hipGetLastError();
-          }
+          if (rc == hipSuccess && first + n == c.v)
+            rc = launch_join<false>(r.parts, r.dx.parts, c.n, c.d, d8, to, stream);
         }
         if (rc != hipSuccess) break;
       }

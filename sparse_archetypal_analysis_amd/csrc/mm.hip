@@ -59,8 +59,10 @@ Shape plan_shape(uint64_t m, uint64_t n, uint32_t tiles, bool heavy) {
       double t;
       if (tile == 256)
         t = (double)((blocks + 255) / 256) * ((heavy ? 18000.0 : 8000.0) + 690.0 * per);
+      else if (blocks > 512)
+        t = ((double)blocks / 512 + 0.25) * ((heavy ? 8500.0 : 3500.0) + 440.0 * per);
       else if (blocks > 256)
-        t = ((double)blocks / 512 + (blocks > 512 ? 0.25 : 0.5)) * ((heavy ? 8500.0 : 3500.0) + 440.0 * per);
+        t = (heavy ? 12000.0 : 7000.0) + 440.0 * per;
       else
         t = (heavy ? 10000.0 : 5000.0) + 300.0 * per;
       if (real > 1) t += 3000.0 + (double)(m * n) * 4.0 * (2.0 * real) / 3500.0;

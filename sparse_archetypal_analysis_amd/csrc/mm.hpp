@@ -581,30 +581,55 @@ struct Parts {
   }
 };
 
-// The parts' sums, in their order, to put.
-template <bool kGated, class Put>
+// The parts' sums, in a fixed order, to put: kLanes threads for every 8 results,
+// each with every kLanes-th part (1300 x 64 in 32 parts: one thread each 10.7
+// us, eight 4.8; 2048 x 256 in 16 6.8 and 10.1).
+template <bool kGated, uint32_t kLanes, class Put>
 __global__ __launch_bounds__(kThreads) void join_parts(const float *__restrict__ parts,
                                                        uint32_t count, uint32_t m, uint32_t n,
                                                        uint32_t wide, Put put) {
-  const uint32_t chunks = (n + 7) / 8;
-  const uint64_t id = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (id >= (uint64_t)m * chunks) return;
-  const uint32_t row = (uint32_t)(id / chunks), col = (uint32_t)(id - (uint64_t)row * chunks) * 8;
-  const float *at = parts + (uint64_t)row * wide + col;
-  Row8 a = *reinterpret_cast<const Row8 *>(at);
-  Row8 b = a;
-  if (kGated) b = *reinterpret_cast<const Row8 *>(at + wide / 2);
-  for (uint32_t s = 1; s < count; ++s) {
-    at += (uint64_t)m * wide;
+  const uint32_t chunks = (n + 7) / 8, lane = threadIdx.x % kLanes;
+  const uint64_t id = (uint64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+  const bool in = id < (uint64_t)m * chunks;
+  const uint32_t row = in ? (uint32_t)(id / chunks) : 0;
+  const uint32_t col = in ? (uint32_t)(id - (uint64_t)row * chunks) * 8 : 0;
+  const float *at = parts + ((uint64_t)lane * m + row) * wide + col;
+  Row8 a = 0.0f, b = 0.0f;
+#pragma unroll 4
+  for (uint32_t s = lane; s < count; s += kLanes) {
     a += *reinterpret_cast<const Row8 *>(at);
     if (kGated) b += *reinterpret_cast<const Row8 *>(at + wide / 2);
+    at += (uint64_t)kLanes * m * wide;
   }
+  if constexpr (kLanes > 1) {
+#pragma unroll
+    for (uint32_t step = 1; step < kLanes; step *= 2)
+#pragma unroll
+      for (uint32_t e = 0; e < 8; ++e) {
+        a[e] += __shfl_xor(a[e], step, kWave);
+        if (kGated) b[e] += __shfl_xor(b[e], step, kWave);
+      }
+  }
+  if (!in || lane > 0) return;
   if constexpr (kGated)
     put.template put<false>(row, col, a, b);
   else if constexpr (!std::is_void<typename Put::Ahead>::value)
     put.template put<false>(row, col, a, put.template ahead<false>(row, col));
   else
     put.template put<false>(row, col, a);
+}
+
+template <bool kGated, class Put>
+hipError_t launch_join(const float *parts, uint32_t count, uint32_t m, uint32_t n, uint32_t wide,
+                       const Put &put, hipStream_t stream) {
+  const uint64_t chunks = (uint64_t)m * ((n + 7) / 8);
+  if (count >= 8 && chunks < (1u << 15))
+    join_parts<kGated, 8><<<(uint32_t)((chunks + kThreads / 8 - 1) / (kThreads / 8)), kThreads, 0, stream>>>(
+        parts, count, m, n, wide, put);
+  else
+    join_parts<kGated, 1><<<(uint32_t)((chunks + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
+        parts, count, m, n, wide, put);
+  return hipGetLastError();
 }
 
 // --- f32 as three 16-bit numbers ---------------------------------------------
@@ -722,7 +747,7 @@ inline Matrix operand(const void *p, uint32_t dtype, uint64_t ld, uint32_t rows,
 // How a product of m x n results over `tiles` tiles of k is spread over the
 // card: the least time by what rounds of blocks take, measured (ns, bf16): of
 // 256 x 256 tiles (one a CU) 8000 + 690 a step of 32 k; of 128 x 128 (two a CU)
-// 3500 + 440, with one a CU 5000 + 300. Parts of k fill the card where tiles
+// 3500 + 440, alone 7000 + 440, with one a CU 5000 + 300. Parts of k fill the card where tiles
 // are few; their sums are written and read once more. heavy: the results are
 // worked on (10000 and 5000 a round more), in one part of k.
 struct Shape {
@@ -800,10 +825,7 @@ hipError_t launch_product(const Args &g, const Shape &s, const Put &put, float *
   const uint32_t wide = up8(g.n) * (kGated ? 2 : 1);
   hipError_t e = launch_tiles<T, kA, kB, kGated>(g, s, Parts{parts, g.m, g.n, wide, false}, stream);
   if (e != hipSuccess) return e;
-  const uint64_t chunks = (uint64_t)g.m * div_up(g.n, 8);
-  join_parts<kGated, Put><<<div_up(chunks, kThreads), kThreads, 0, stream>>>(parts, s.parts, g.m, g.n,
-                                                                           wide, put);
-  return hipGetLastError();
+  return launch_join<kGated>(parts, s.parts, g.m, g.n, wide, put, stream);
 }
 
 // Results of type O to the caller's rows (any element-aligned address).
