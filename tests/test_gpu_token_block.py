@@ -450,6 +450,162 @@ def test_loss_rows_beyond_4_gib():
         assert (p is None and q is None) or torch.equal(p, q)
 
 
+# --- sizes of large tiles, strides, workspaces ---------------------------------------
+
+def some(rng, n, count=48):
+    """Indexes at both ends and between."""
+    at = np.unique(np.concatenate([[0, 1, n - 1], rng.integers(0, n, count)]))
+    return at, torch.from_numpy(at).cuda()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_blocks_of_results(dtype):
+    """Enough rows and columns that tiles of 256 are taken, with ragged ends, on
+    a few of the rows and columns."""
+    rng = np.random.default_rng(4)
+    n, d, f, m = 4103, 1040, 8200, 4104
+    x, w_in, w_out = block(rng, n, d, f, m, dtype)
+    y, pre = saa.seacells_gated_ffn(x, w_in, w_out, "silu")
+    at, dev = some(rng, n)
+    want, bounds = R.ffn(exact(x[dev]), exact(w_in), exact(w_out), "silu", dtype)
+    within(y[dev], want[0], bounds[0], "out")
+    within(pre[dev], want[1], bounds[1], "pre")
+    dy = rows(rng, n, m, dtype)
+    dx, di, do = saa.seacells_gated_ffn_grad(dy, x, pre, w_in, w_out, "silu")
+    want, bounds = R.ffn_grad(exact(dy[dev]), exact(x[dev]), exact(pre[dev]), exact(w_in), exact(w_out),
+                              "silu", dtype)
+    within(dx[dev], want[0], bounds[0], "d_x")
+    cols, dcols = some(rng, f)
+    both = torch.cat([dcols, dcols + f])
+    want, bounds = R.ffn_grad(exact(dy), exact(x), exact(pre[:, both]), exact(w_in[both]),
+                              exact(w_out[:, dcols]), "silu", dtype)
+    within(di[both], want[1], bounds[1], "d_w_in")
+    within(do[:, dcols], want[2], bounds[2], "d_w_out")
+
+
+@pytest.mark.parametrize("bias", [None, "plain"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_blocks_of_logits(dtype, bias):
+    rng = np.random.default_rng(4)
+    n, d, v = 4103, 1040, 8199
+    x, table, b = head(rng, n, d, v, dtype, bias)
+    at, dev = some(rng, n)
+    cls, dcls = some(rng, v)
+    local = rng.integers(0, cls.size, n)
+    tgt = torch.from_numpy(cls[local].astype(np.int32)).cuda()
+    logp, H, stats, _ = saa.seacells_linear_logprobs(x, table, tgt, b)
+    want, bounds = R.loss(exact(x[dev]), exact(table), None if b is None else exact(b), exact(tgt[dev]), dtype)
+    for what, g, w, e in zip(("logp", "entropy", "stats"), (logp, H, stats), want, bounds):
+        within(g[dev], w, e, what)
+    gl, ge = vector(rng, n, 1.0 / n), vector(rng, n, 0.1 / n)
+    dx, dt, db, _ = saa.seacells_linear_logprobs_grad(x, table, tgt, stats, H, gl, ge, b)
+    pick = lambda t: exact(t[dev])  # noqa: E731
+    bx = None if b is None else exact(b)
+    want, bounds = R.loss_grad(pick(x), exact(table), bx, pick(tgt), pick(stats), pick(H), pick(gl), pick(ge),
+                               dtype)
+    if dtype == "f16":  # (the scale goes by all rows' gradients)
+        most = float((gl.abs() + 17 * ge.abs()).max())
+        bounds = (bounds[0] + 2.0 ** -38 * most * np.abs(exact(table)).sum(axis=0), *bounds[1:])
+    within(dx[dev], want[0], bounds[0], "d_x")
+    want, bounds = R.loss_grad(exact(x), exact(table[dcls]), None if b is None else bx[cls], local,
+                               exact(stats), exact(H), exact(gl), exact(ge), dtype)
+    within(dt[dcls], want[1], bounds[1], "d_table")
+    if b is not None:
+        within(db[dcls], want[2], bounds[2], "d_bias")
+
+
+def test_rows_in_several_launches():
+    """More rows than the sums of one launch's slices are kept for, checked on
+    rows on both sides of the cut (at a multiple of 256 below 22000) and at the
+    ends."""
+    rng = np.random.default_rng(4)
+    n, d, v = 23000, 8, 131072
+    x, table, b = head(rng, n, d, v, "bf16", "plain")
+    tgt = classes(rng, n, v)
+    tgt[n - 2] = v
+    got = saa.seacells_linear_logprobs(x, table, tgt, b)
+    assert flags(got[3]) == ["BAD_INDEX"] and got[0][n - 2] == 0
+    at = np.unique(np.concatenate([[0, 1, n - 2, n - 1], np.arange(20480, 22017, 256),
+                                   np.arange(20480, 22017, 256) - 1]))
+    dev = torch.from_numpy(at).cuda()
+    want, bounds = R.loss(exact(x[dev]), exact(table), exact(b), exact(tgt[dev]), "bf16")
+    for what, g, w, e in zip(("logp", "entropy", "stats"), got, want, bounds):
+        within(g[dev], w, e, what)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("gap,start", [(0, 1), (5, 0), (8, 8), (3, 7), (2 ** 22, 0)])
+def test_even_widths_at_any_stride_and_start(dtype, gap, start):
+    """Widths of whole chunks in rows that start anywhere: the same bits as in
+    plain matrices."""
+    rng = np.random.default_rng(11)
+    n, d, f, m, v = 70, 64, 128, 72, 200
+
+    def moved(t):
+        base = torch.full((start + t.shape[0] * (t.shape[1] + gap) + 8,), float("nan"), dtype=t.dtype,
+                          device="cuda")
+        out = base[start:start + t.shape[0] * (t.shape[1] + gap)].view(t.shape[0], -1)[:, :t.shape[1]]
+        return out.copy_(t)
+
+    x, w_in, w_out = block(rng, n, d, f, m, dtype)
+    if gap > 100:  # (one operand with rows 2^22 apart is enough memory)
+        a = saa.seacells_gated_ffn(x, w_in, w_out)
+        b = saa.seacells_gated_ffn(moved(x[:65].contiguous()), w_in, w_out)
+        assert torch.equal(a[0][:65], b[0]) and torch.equal(a[1][:65], b[1])
+        return
+    a = saa.seacells_gated_ffn(x, w_in, w_out)
+    b = saa.seacells_gated_ffn(moved(x), moved(w_in), moved(w_out))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    dy = rows(rng, n, m, dtype)
+    for p, q in zip(saa.seacells_gated_ffn_grad(dy, x, a[1], w_in, w_out),
+                    saa.seacells_gated_ffn_grad(moved(dy), moved(x), moved(a[1]), moved(w_in),
+                                                moved(w_out))):
+        assert torch.equal(p, q)
+    table, tgt = rows(rng, v, d, dtype), classes(rng, n, v)
+    a = saa.seacells_linear_logprobs(x, table, tgt)
+    b = saa.seacells_linear_logprobs(moved(x), moved(table), tgt)
+    one = torch.ones(n, device="cuda")
+    g = saa.seacells_linear_logprobs_grad(x, table, tgt, a[2], a[1], one, one)
+    h = saa.seacells_linear_logprobs_grad(moved(x), moved(table), tgt, b[2], b[1], one, one)
+    for p, q in zip(a[:3] + g[:2], b[:3] + h[:2]):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,d", [(5, 24), (5, 23), (150, 24), (150, 23)])
+def test_workspaces_are_as_large_as_the_queries_say(n, d, dtype):
+    """Calls with exactly the bytes of the queries, between marks that stay; one
+    byte less is refused."""
+    rng = np.random.default_rng(n + d)
+    f, m, v, dt = 40, d, 70, DT[dtype]
+    x, w_in, w_out = block(rng, n, d, f, m, dtype)
+    table, tgt, dy = rows(rng, v, d, dtype), classes(rng, n, v), rows(rng, n, m, dtype)
+    b, one = vector(rng, v), torch.ones(n, device="cuda")
+    y, pre = saa.seacells_gated_ffn(x, w_in, w_out)
+    _, H, stats, _ = saa.seacells_linear_logprobs(x, table, tgt, b)
+    for query, sizes, go in (
+            (saa.seacells_gated_ffn_workspace, (n, d, f, m),
+             lambda ws: saa.seacells_gated_ffn(x, w_in, w_out, workspace=ws)),
+            (saa.seacells_gated_ffn_grad_workspace, (n, d, f, m),
+             lambda ws: saa.seacells_gated_ffn_grad(dy, x, pre, w_in, w_out, workspace=ws)),
+            (saa.seacells_linear_logprobs_workspace, (n, d, v),
+             lambda ws: saa.seacells_linear_logprobs(x, table, tgt, b, workspace=ws)),
+            (saa.seacells_linear_logprobs_grad_workspace, (n, d, v),
+             lambda ws: saa.seacells_linear_logprobs_grad(x, table, tgt, stats, H, one, one, b,
+                                                          workspace=ws))):
+        want = [t for t in go(None) if t is not None]
+        for on_16 in ((True, False) if d % 8 == 0 else (False,)):
+            size = query(dt, *sizes, on_16_bytes=on_16)
+            base = torch.full((size + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+            got = [t for t in go(base[256:256 + size]) if t is not None]
+            assert all(torch.equal(p, q) for p, q in zip(want, got))
+            assert bool((base[:256] == 0x5A).all()) and bool((base[256 + size:] == 0x5A).all())
+        # (these operands start on 16 bytes; those whose rows do not are copied either way)
+        least = query(dt, *sizes, on_16_bytes=True)
+        with pytest.raises(saa.SeacellsError):
+            go(torch.empty(least - 1, dtype=torch.uint8, device="cuda"))
+
+
 # --- together, streams, graphs, refusals -------------------------------------------
 
 def model_step(s):
@@ -536,6 +692,47 @@ def test_block_and_loss_in_a_graph(n, dtype):
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert torch.equal(a, b)
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace, over the same weights."""
+    s = model_state(900, "bf16")
+    s2 = dict(model_state(900, "bf16", seed=5), **{k: s[k] for k in ("w_in", "w_out", "head", "bias")})
+    want, want2 = model_step(s), model_step(s2)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(4):
+        with torch.cuda.stream(a):
+            outs.append((model_step(s), want))
+        with torch.cuda.stream(b):
+            outs.append((model_step(s2), want2))
+    torch.cuda.synchronize()
+    for got, ref in outs:
+        for p, q in zip(got, ref):
+            assert torch.equal(p, q)
+
+
+def test_two_graphs_of_one_workspace():
+    """Graphs that share a workspace and run one after the other."""
+    rng = np.random.default_rng(2)
+    x, w_in, w_out = block(rng, 300, 96, 200, 64, "bf16")
+    x2 = rows(rng, 40, 96, "bf16")
+    ws = torch.empty(saa.seacells_gated_ffn_workspace(torch.bfloat16, 300, 96, 200, 64), dtype=torch.uint8,
+                     device="cuda")
+    want = [saa.seacells_gated_ffn(t, w_in, w_out)[0] for t in (x, x2)]
+    graphs, outs = [], []
+    for t in (x, x2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(saa.seacells_gated_ffn(t, w_in, w_out, workspace=ws)[0])
+        graphs.append(g)
+    for _ in range(3):
+        for g, o, w in zip(graphs, outs, want):
+            o.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, w)
 
 
 def test_the_same_call_gives_the_same_bits():
