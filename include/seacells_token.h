@@ -239,7 +239,9 @@ int seacells_gated_ffn(const void *x, uint32_t dtype, uint32_t n, uint32_t d, ui
  *   d_x = d_pre w_in [n, d];  d_w_in = d_pre^T x [2f, d];
  *   d_w_out = d_out^T h [m, f], h = act(g) u
  * All of dtype; each of the three may be NULL (not computed). d_pre and h are
- * held in dtype between the products. n = 0 gives zero weight gradients.
+ * held in dtype between the products. A pre that is infinite (f16: past 65504)
+ * has no gradient: what depends on it is NaN or infinite. n = 0 gives zero
+ * weight gradients.
  * workspace: seacells_gated_ffn_grad_workspace bytes, 256-byte aligned.
  */
 int seacells_gated_ffn_grad(const void *d_out, uint64_t d_out_ld, const void *x, uint32_t dtype,
@@ -283,9 +285,10 @@ int seacells_linear_logprobs(const void *x, uint32_t dtype, uint32_t n, uint32_t
  * d_x, d_table             of dtype, d_bias f32; each may be NULL.
  * d_z is computed anew in pieces of the classes and held in dtype between the
  * products (f16: times a power of two); d_bias sums it before that rounding.
- * Masked classes and rows with nothing left have d_z 0 (a masked class' row of
- * the table and every row of x still have to be finite for d_x and d_table to
- * be); a row without a distribution has NaN. n = 0 gives zero d_table, d_bias.
+ * Masked classes and rows with nothing left have d_z 0, whatever d_logp and
+ * d_entropy hold there (a masked class' row of the table and every row of x
+ * still have to be finite for d_x and d_table to be); a row without a
+ * distribution has NaN. n = 0 gives zero d_table, d_bias.
  * workspace: seacells_linear_logprobs_grad_workspace bytes, 256-byte aligned.
  */
 int seacells_linear_logprobs_grad(const void *x, uint32_t dtype, uint32_t n, uint32_t d,

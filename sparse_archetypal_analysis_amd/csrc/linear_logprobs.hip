@@ -247,6 +247,7 @@ struct PutDz {
 #pragma unroll
     for (uint32_t i = 0; i < kSub; ++i) {
       g[i] = hit[i] < classes ? g[i] : 0.0f;
+      if (m[i] == -kInf) g[i] = h[i] = 0.0f;  // nothing left: 0, whatever they hold
       gh[i] = m[i] == m[i] ? fmaf(h[i], gh[i], g[i]) : m[i];  // no distribution: NaN
       ls[i] *= kLog2E;  // (log p in powers of 2)
       h[i] *= kLn2;
@@ -272,6 +273,14 @@ struct PutDz {
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e)
             if (hit[i] == outer_of(j, (lane / 16) * 4) + e) d[j][e] += g[i];
+      }
+      // 0 times a gradient that is not finite: masked classes stay at 0
+      if (!kPlain && __any(!(fabsf(gh[i]) < kInf && fabsf(h[i]) < kInf))) {
+#pragma unroll
+        for (uint32_t j = 0; j < kSub; ++j)
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e)
+            if (logits.bias[j][e] == -kInf && m[i] == m[i]) d[j][e] = 0.0f;
       }
       if (column_sums != nullptr && in_row) {
 #pragma unroll

@@ -361,6 +361,45 @@ def test_masked_classes_have_no_part(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("bad", [INF, -INF, float("nan")])
+def test_masked_places_under_gradients_that_are_not_finite(dtype, bad):
+    """Masked classes get nothing from a row whose incoming gradients are not
+    finite, and a row with nothing left gets and gives nothing."""
+    rng = np.random.default_rng(11)
+    x, table, b = head(rng, 300, 48, 700, dtype, "plain")
+    b[100:500] = -INF
+    tgt = classes(rng, 300, 700)
+    tgt[7], tgt[8], tgt[9] = 20, 250, -1
+    _, H, stats, _ = saa.seacells_linear_logprobs(x, table, tgt, b)
+    for which in ("logp", "entropy"):
+        g, h = torch.ones(300, device="cuda"), torch.ones(300, device="cuda")
+        (g if which == "logp" else h)[7:10] = bad
+        dx, dt, db, _ = saa.seacells_linear_logprobs_grad(x, table, tgt, stats, H, g, h, b)
+        assert not dt[100:500].any() and not db[100:500].any()
+        assert bool(dx[10:].isfinite().all()) and bool(dx[:7].isfinite().all())
+    b[:] = -INF
+    _, H, stats, _ = saa.seacells_linear_logprobs(x, table, tgt, b)
+    g, h = torch.full((300,), bad, device="cuda"), torch.full((300,), bad, device="cuda")
+    dx, dt, db, _ = saa.seacells_linear_logprobs_grad(x, table, tgt, stats, H, g, h, b)
+    assert not dx.any() and not dt.any() and not db.any()
+
+
+@pytest.mark.parametrize("dtype", ("f16", "bf16"))
+def test_rows_with_nothing_left_without_a_bias(dtype):
+    """Every z is -inf from the operands: no gradient either."""
+    x = torch.ones(5, 8, device="cuda").to(DT[dtype])
+    table = torch.full((12, 8), -INF, device="cuda").to(DT[dtype])
+    tgt = torch.tensor([0, 11, 3, -1, 4], dtype=torch.int32, device="cuda")
+    logp, H, stats, _ = saa.seacells_linear_logprobs(x, table, tgt)
+    assert bool((stats[:, 0] == -INF).all()) and not stats[:, 1].any() and not H.any()
+    assert torch.equal(logp.cpu(), torch.tensor([-INF, -INF, -INF, 0.0, -INF]))
+    g = torch.full((5,), 2.0, device="cuda")
+    _, dt, db, _ = saa.seacells_linear_logprobs_grad(
+        x, table, tgt, stats, H, g, g, d_x=False, d_bias=torch.empty(12, device="cuda"))
+    assert not dt.any() and not db.any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_rows_without_a_distribution(dtype):
     rng = np.random.default_rng(7)
     x, table, b = head(rng, 30, 48, 900, dtype, "plain")
