@@ -637,17 +637,15 @@ hipError_t launch_join(const float *parts, uint32_t count, uint32_t m, uint32_t 
 // f32 operands are multiplied as sums of three bf16 numbers (8 bits each, so
 // x = x0 + x1 + x2 to 2^-25 of x), with the six products whose size is above
 // 2^-24 of the whole; sums are f32. The matrix cores multiply bf16 at 16 times
-// f32's rate. An infinity or NaN stays in x0.
+// f32's rate. An infinity or NaN goes on to x1 and x2, where it is NaN.
 constexpr uint32_t kPlanes = 3, kPairs = 6;
 constexpr uint8_t kPairA[kPairs] = {0, 2, 1, 0, 1, 0}, kPairB[kPairs] = {2, 0, 1, 1, 0, 0};
 
 __device__ __forceinline__ void split(float x, __bf16 out[kPlanes]) {
-  __bf16 a = (__bf16)x;
   // (a finite x next to the type's end is not rounded up to infinity)
-  if (!__builtin_isfinite((float)a) && __builtin_isfinite(x))
-    a = __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(x) >> 16));
-  const float r = __builtin_isfinite(x) ? x - (float)a : 0.0f;
-  out[0] = a;
+  constexpr float kMost = 0x1.fep127f;  // bf16's largest
+  out[0] = (__bf16)__builtin_amdgcn_fmed3f(x, -kMost, kMost);
+  const float r = x - (float)out[0];
   out[1] = (__bf16)r;
   out[2] = (__bf16)(r - (float)out[1]);
 }
