@@ -11,9 +11,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libseacells_fw.so")
 SOURCES = ["abi.hip", "fw_a.hip", "fw_b.hip", "sparse_ops.hip", "abi_token.hip", "embed.hip",
-           "layer_norm.hip", "logprobs.hip", "mm.hip", "ffn.hip", "ffn_grad.hip",
-           "linear_logprobs.hip", "few.hip"]
-HEADERS = ["common.hpp", "token.hpp", "mm.hpp", "few.hpp"]
+           "layer_norm.hip", "logprobs.hip", "mm.hip", "ffn.hip", "ffn_d_pre.hip",
+           "ffn_grad.hip", "linear_logprobs.hip", "few.hip"]
+HEADERS = ["common.hpp", "token.hpp", "mm.hpp", "few.hpp", "ffn_grad.hpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

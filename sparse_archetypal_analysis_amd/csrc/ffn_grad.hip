@@ -3,71 +3,14 @@
 //   d_pre = [dh u act'(g), dh act(g)],  dx = d_pre W_in,
 //   dW_in = d_pre^T x,  dW_out = dy^T h,  h = act(g) u.
 // Four products on the matrix cores (mm.hpp); the one that gives dh reads pre
-// and leaves d_pre and h, in x's 16-bit type (f32: three bf16), one rounding of
-// half a step beside the output's own; sums are f32.
-#include <type_traits>
-
-#include "few.hpp"
-#include "mm.hpp"
+// and leaves d_pre and h (ffn_d_pre.hip), in x's 16-bit type (f32: three bf16),
+// one rounding of half a step beside the output's own; sums are f32.
+#include "ffn_grad.hpp"
 
 namespace seacells {
 namespace {
 
 using namespace mm;
-
-// dh to d_pre (its up columns `half` behind the gate's) and h.
-template <class O, Act kAct>
-struct PutPre {
-  const O *pre;
-  uint64_t pre_ld;
-  uint16_t *d_pre, *h;
-  uint64_t d_ld, h_ld, d_plane, h_plane;
-  uint32_t f, half;
-  struct Ahead {
-    Pack<O, 8> g, u;
-  };
-  template <bool kWhole>
-  __device__ __forceinline__ Ahead ahead(uint32_t row, uint32_t col) const {
-    const O *const at = pre + row * pre_ld;
-    Ahead p;
-    if (kWhole || col + 8 <= f) {
-      // (read once: lines that the L2 gives up first leave it to the product's
-      // operands, 16384 x 8192 x 2048 bf16 746 -> 713 us; f32's 81 -> 88)
-      const Pack<O, 8> *const g = reinterpret_cast<const Pack<O, 8> *>(at + col);
-      const Pack<O, 8> *const u = reinterpret_cast<const Pack<O, 8> *>(at + f + col);
-      p.g = sizeof(O) == 2 ? __builtin_nontemporal_load(g) : *g;
-      p.u = sizeof(O) == 2 ? __builtin_nontemporal_load(u) : *u;
-    } else {
-#pragma unroll
-      for (uint32_t e = 0; e < 8; ++e) {
-        const uint32_t c = min(col + e, f - 1);
-        p.g[e] = at[c];
-        p.u[e] = at[f + c];
-      }
-    }
-    return p;
-  }
-
-  template <bool kWhole>
-  __device__ __forceinline__ void put(uint32_t row, uint32_t col, Row8 dh, const Ahead &p) const {
-    const bool whole = kWhole || col + 8 <= f;
-    const Row8 g = __builtin_convertvector(p.g, Row8), u = __builtin_convertvector(p.u, Row8);
-    Row8 dg, du, v;
-#pragma unroll
-    for (uint32_t e = 0; e < 8; ++e) {
-      float a, da;
-      act_both<kAct>(g[e], &a, &da);
-      const bool in = whole || col + e < f;
-      dg[e] = in ? dh[e] * u[e] * da : 0.0f;
-      du[e] = in ? dh[e] * a : 0.0f;
-      v[e] = in ? a * u[e] : 0.0f;
-    }
-    uint16_t *const to = d_pre + row * d_ld + col;
-    put_operand<O>(to, d_plane, dg);
-    put_operand<O>(to + half, d_plane, du);
-    put_operand<O>(h + row * h_ld + col, h_plane, v);
-  }
-};
 
 // Rows of [gate columns, up columns] of d_pre (`apart` each) to W_in's rows.
 template <class O>
@@ -83,18 +26,6 @@ struct ToGatedRows {
     if (in < f) put_row<kWhole>(out + (uint64_t)(up ? f + in : in) * ld, col, n, v);
   }
 };
-
-template <class F>
-hipError_t with_act(Act a, F &&f) {
-  switch (a) {
-    case Act::silu:
-      return f(std::integral_constant<Act, Act::silu>{});
-    case Act::gelu:
-      return f(std::integral_constant<Act, Act::gelu>{});
-    default:
-      return f(std::integral_constant<Act, Act::relu>{});
-  }
-}
 
 struct GradRoom {
   Matrix x, d_out, w_in, w_out;
@@ -182,16 +113,14 @@ hipError_t launch_ffn_grad(const FfnGradCall &c, void *d_x, uint64_t d_x_ld, voi
   if (e != hipSuccess) return e;
   const uint64_t h_plane = (uint64_t)c.n * h_ld, d_plane = (uint64_t)c.n * d_ld;
   const Matrix h = {r.h, h_ld, h_plane}, d_pre = {r.d_pre, d_ld, d_plane};
+  const DPre d = {c.dtype, c.act, make_args(c.dtype, r.d_out, r.w_out, c.n, c.f, m8, c.m, 1, nullptr, nullptr,
+                                            r.dh, c.f),
+                  r.dh, c.pre, c.pre_ld, r.d_pre, r.h, d_ld, h_ld, d_plane, h_plane, c.f, half, r.parts};
+  if ((e = launch_d_pre(d, stream)) != hipSuccess) return e;
   return with_types(c.dtype, [&](auto o, auto t) {
     typedef decltype(o) O;
     typedef decltype(t) T;
-    hipError_t rc = with_act(c.act, [&](auto a) {
-      const Args g = make_args(c.dtype, r.d_out, r.w_out, c.n, c.f, m8, c.m, 1, nullptr, nullptr,
-                               r.dh, c.f);
-      const PutPre<O, decltype(a)::value> put = {static_cast<const O *>(c.pre), c.pre_ld, r.d_pre, r.h,
-                                                 d_ld, h_ld, d_plane, h_plane, c.f, half};
-      return launch_product<T, kAlongK, kAcrossK, false>(g, r.dh, put, r.parts, stream);
-    });
+    hipError_t rc = hipSuccess;
     if (rc == hipSuccess && d_x != nullptr) {
       const uint64_t a_base[2] = {0, half}, b_base[2] = {0, (uint64_t)c.f * r.w_in.ld};
       const Args g = make_args(c.dtype, d_pre, r.w_in, c.n, c.d, f8, c.f, 2, a_base, b_base, r.dx, c.d);
