@@ -58,16 +58,20 @@ __device__ __forceinline__ void act_both(float g, float *a, float *da) {
 
 // --- figures of a row of log probabilities ------------------------------------
 
+// e^-200 (and 2^-200) is 0: a difference below that, -inf among them, is as good as that
+// one, and finite. (NaN becomes that too; a row's maximum tells of NaN.)
+__device__ __forceinline__ float not_below(float t) { return fmaxf(t, -200.0f); }
 
 // What a row's figures are made of: maximum, sum e^(z - m), sum (z - m) e^(z - m).
 struct Sums {
   float m, s, u;
 };
 
-// The same for the maximum m (not below own.m); nothing: (-inf, 0, 0).
+// The same for the maximum m (not below own.m); nothing: (-inf, 0, 0). Classes
+// of a bias at f32's low end are 1e38 below others: t s would be infinite, and e 0.
 __device__ __forceinline__ void rescale(Sums &a, float m) {
   const bool none = a.m == -kInf;
-  const float t = none ? 0.0f : a.m - m;
+  const float t = none ? 0.0f : not_below(a.m - m);
   const float e = none ? 0.0f : exp_neg(t);
   a.u = none ? 0.0f : e * (a.u + t * a.s);
   a.s *= e;
@@ -80,10 +84,6 @@ __device__ __forceinline__ Sums joined(Sums a, Sums b) {
   rescale(b, m);
   return Sums{m, a.s + b.s, a.u + b.u};
 }
-
-// e^-200 (and 2^-200) is 0: a difference below that, -inf among them, is as good as that
-// one, and finite. (NaN becomes that too; a row's maximum tells of NaN.)
-__device__ __forceinline__ float not_below(float t) { return fmaxf(t, -200.0f); }
 
 // --- few rows ------------------------------------------------------------------
 
