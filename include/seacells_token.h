@@ -284,7 +284,8 @@ int seacells_linear_logprobs(const void *x, uint32_t dtype, uint32_t n, uint32_t
  * d_logp, d_entropy        device [n] f32; either may be NULL (0).
  * d_x, d_table             of dtype, d_bias f32; each may be NULL.
  * d_z is computed anew in pieces of the classes and held in dtype between the
- * products (f16: times a power of two); d_bias sums it before that rounding.
+ * products (f16: times a power of two, by the largest d_logp and d_entropy of
+ * the rows that have a d_z of their own); d_bias sums it before that rounding.
  * Masked classes and rows with nothing left have d_z 0, whatever d_logp and
  * d_entropy hold there (a masked class' row of the table and every row of x
  * still have to be finite for d_x and d_table to be); a row without a
