@@ -187,7 +187,8 @@ __global__ __launch_bounds__(kPrepare) void report_targets(const int32_t *__rest
 // (p |log p + H| <= 0.4 + log v), to below 2^15. Values that d_z does not
 // depend on choose nothing: d_logp of ignored targets, both of rows with nothing
 // left or without a distribution. Targets past the classes are reported in the
-// same pass. One block up to kOneBlock rows, more blocks in two launches (gradient
+// same pass. The maximum is of 1/32 of the bound, so that it is finite for any
+// finite gradients. One block up to kOneBlock rows, more blocks in two launches (gradient
 // of 64 x 1300, us in one and two: 3001 rows 45.2 and 46.4, 8192 rows 57.2 and
 // 54.4, 131072 rows 498 and 387).
 constexpr uint32_t kOneBlock = 4096, kScaleBlocks = 128;
@@ -200,9 +201,9 @@ struct Looked {
 __device__ __forceinline__ void put_scale(Looked all, float *__restrict__ scale,
                                           uint32_t *__restrict__ status) {
   *status = all.bad ? kFlagBadIndex : 0u;
-  // most < 2^(e + 1); powers between 2^-100 and 2^100 keep both factors normal
-  int e = (int)((__float_as_uint(all.most) >> 23) & 255u) - 127;
-  e = all.most > 0.0f ? min(max(14 - e, -100), 100) : 0;
+  // 32 most < 2^(e + 1), e <= 132; powers from 2^-118 to 2^100 keep both factors normal
+  int e = (int)((__float_as_uint(all.most) >> 23) & 255u) - 122;
+  e = all.most > 0.0f ? min(14 - e, 100) : 0;
   scale[0] = __uint_as_float((uint32_t)(e + 127) << 23);
   scale[1] = __uint_as_float((uint32_t)(127 - e) << 23);
 }
@@ -221,8 +222,8 @@ __global__ __launch_bounds__(kPrepare) void scale_rows(const int32_t *__restrict
   for (uint64_t i = blockIdx.x * kPrepare + threadIdx.x; i < n; i += gridDim.x * kPrepare) {
     const bool left = stats[2 * i] > -kInf;  // (false for NaN)
     const int32_t target = targets != nullptr ? targets[i] : -1;
-    const float g = d_logp != nullptr ? fabsf(d_logp[i]) : 0.0f;
-    const float h = d_entropy != nullptr ? 17.0f * fabsf(d_entropy[i]) : 0.0f;
+    const float g = d_logp != nullptr ? fabsf(d_logp[i]) / 32.0f : 0.0f;
+    const float h = d_entropy != nullptr ? fabsf(d_entropy[i]) * (17.0f / 32.0f) : 0.0f;
     const float x = ((uint32_t)target < v ? g : 0.0f) + h;
     most = left && x < kInf ? fmaxf(most, x) : most;
     bad |= target >= (int32_t)v;

@@ -71,3 +71,29 @@ def test_rows_with_nothing_left_have_no_part(lost, dtype):
     keep[7:9] = False
     assert torch.equal(want[keep], got[keep])
     assert not got[7:9].any() if lost == -INF else bool(got[7:9].isnan().all())
+
+
+@pytest.mark.parametrize("which", ["logp", "entropy"])
+@pytest.mark.parametrize("n", [5, 300])
+def test_incoming_gradients_at_f32s_end(n, which):
+    """Gradients as large as f32 goes (for entropy: as 17 times them does not
+    go) stay numbers: where x or the table is 0 their products are 0, elsewhere
+    they are past f16, to the side that the formula says."""
+    rng = np.random.default_rng(9)
+    x, table, b = head(rng, n, 64, 800, "f16", "plain")
+    x *= 0.25  # (log p stays above -15: with entropies' gradients it is a number)
+    x[:, 3] = 0.0
+    table[:, 5] = 0.0
+    tgt = classes(rng, n, 800)
+    tgt[0] = 7
+    _, H, stats, _ = saa.seacells_linear_logprobs(x, table, None, b)
+    sign = torch.where(vector(rng, n) > 0, 1.0, -1.0)
+    zero = torch.zeros(n, device="cuda")
+    gl, ge = (3e38 * sign, zero) if which == "logp" else (zero, 2.1e37 * sign)
+    dx, dt, _, _ = saa.seacells_linear_logprobs_grad(x, table, tgt, stats, H, gl, ge, b)
+    assert not dx[:, 5].any() and not dt[:, 3].any()
+    want, bounds = R.loss_grad(exact(x), exact(table), exact(b), exact(tgt), exact(stats), exact(H),
+                               exact(gl), exact(ge), "f16")
+    sure = np.abs(want[0]) > bounds[0] + 1e6
+    assert sure.mean() > 0.5
+    assert np.array_equal(exact(dx)[sure], np.sign(want[0][sure]) * INF)
