@@ -281,7 +281,9 @@ int seacells_linear_logprobs(const void *x, uint32_t dtype, uint32_t n, uint32_t
  * x, table, bias, targets  as the forward call's (targets NULL: all ignored).
  * stats, entropy           as it wrote them; entropy may be NULL with d_entropy
  *                          NULL.
- * d_logp, d_entropy        device [n] f32; either may be NULL (0).
+ * d_logp, d_entropy        device [n] f32; either may be NULL (0). A finite
+ *                          d_entropy is below 2^120 in size (past that a class
+ *                          that has no probability without being masked is NaN).
  * d_x, d_table             of dtype, d_bias f32; each may be NULL.
  * d_z is computed anew in pieces of the classes and held in dtype between the
  * products (f16: times a power of two, by the largest d_logp and d_entropy of

@@ -265,6 +265,7 @@ hipError_t launch_scale(const LossGradCall &c, Looked *parts, float *scale, uint
 
 // Epilogue of the backward's first product: d_z of a piece of the classes.
 // With lp = log p: d_z = g [target] - p (g + h H + h lp).
+constexpr float kLarge = 0x1p120f;
 template <class O>
 struct PutDz {
   const float *bias;  // of the piece
@@ -331,8 +332,8 @@ struct PutDz {
           for (uint32_t e = 0; e < 4; ++e)
             if (hit[i] == outer_of(j, (lane / 16) * 4) + e) d[j][e] += g[i];
       }
-      // 0 times a gradient that is not finite: masked classes stay at 0
-      if (!kPlain && __any(!(fabsf(gh[i]) < kInf && fabsf(h[i]) < kInf))) {
+      // 0 times what is not finite (200 |h| may be past f32): masked classes stay at 0
+      if (!kPlain && __any(!(fabsf(gh[i]) < kLarge && fabsf(h[i]) < kLarge))) {
 #pragma unroll
         for (uint32_t j = 0; j < kSub; ++j)
 #pragma unroll

@@ -93,3 +93,29 @@ def test_gradients_where_every_class_has_the_types_end(n, level, dtype):
     for what, g, w, e, t in zip(("d_x", "d_table", "d_bias"), got, (dz @ tt, dz.T @ tx, dz.sum(axis=0)),
                                 (e_x, e_t, e_b), (dtype, dtype, "f32")):
         within(g, w, R.rounded(w, e, t), what)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [5, 300])
+def test_masked_classes_under_large_finite_gradients(n, dtype):
+    """A finite gradient whose product with a masked class' log p is past f32
+    gives it nothing."""
+    rng = np.random.default_rng(10)
+    v = 512
+    x, table, b = head(rng, n, 64, v, dtype, "plain")
+    b[256:] = -INF
+    tgt = torch.from_numpy(rng.integers(-1, v, n).astype(np.int32)).cuda()
+    tgt[1], tgt[2] = 7, 300
+    _, H, stats, _ = saa.seacells_linear_logprobs(x, table, None, b)
+    gl, ge = torch.ones(n, device="cuda"), torch.zeros(n, device="cuda")
+    ge[::2], ge[1::4] = 1e37, -1e37
+    got = saa.seacells_linear_logprobs_grad(x, table, tgt, stats, H, gl, ge, b)
+    want, bounds = R.loss_grad(exact(x), exact(table), exact(b), exact(tgt), exact(stats), exact(H),
+                               exact(gl), exact(ge), dtype)
+    assert not got[1][256:].any() and not got[2][256:].any()
+    within(got[2], want[2], bounds[2], "d_bias")
+    if dtype == "f16":  # (most of the others are past its range)
+        assert not got[0].isnan().any() and not got[1].isnan().any()
+        return
+    within(got[0], want[0], bounds[0], "d_x")
+    within(got[1], want[1], bounds[1], "d_table")
