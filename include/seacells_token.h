@@ -239,9 +239,10 @@ int seacells_gated_ffn(const void *x, uint32_t dtype, uint32_t n, uint32_t d, ui
  *   d_x = d_pre w_in [n, d];  d_w_in = d_pre^T x [2f, d];
  *   d_w_out = d_out^T h [m, f], h = act(g) u
  * All of dtype; each of the three may be NULL (not computed). d_pre and h are
- * held in dtype between the products. A pre that is infinite (f16: past 65504)
- * has no gradient: what depends on it is NaN or infinite. n = 0 gives zero
- * weight gradients.
+ * held in dtype between the products (f16: d_pre times a power of two, by the
+ * largest of d_out, where that keeps it below 65520). A pre that is infinite
+ * (f16: past 65504) has no gradient: what depends on it is NaN or infinite.
+ * n = 0 gives zero weight gradients.
  * workspace: seacells_gated_ffn_grad_workspace bytes, 256-byte aligned.
  */
 int seacells_gated_ffn_grad(const void *d_out, uint64_t d_out_ld, const void *x, uint32_t dtype,

@@ -20,13 +20,18 @@ struct PutPre {
   uint16_t *d_pre, *h;
   uint64_t d_ld, h_ld, d_plane, h_plane;
   uint32_t f, half;
+  Scale *scale;  // f16, or nullptr
+  static constexpr bool kScaled = std::is_same<O, _Float16>::value;
+  static constexpr float kEnd = 65520.0f;  // what f16 rounds to infinity
   struct Ahead {
     Pack<O, 8> g, u;
+    float by;  // the scale's
   };
   template <bool kWhole>
   __device__ __forceinline__ Ahead ahead(uint32_t row, uint32_t col) const {
     const O *const at = pre + row * pre_ld;
     Ahead p;
+    p.by = kScaled && scale != nullptr ? scale->by : 1.0f;
     if (kWhole || col + 8 <= f) {
       // (read once: lines that the L2 gives up first leave it to the product's
       // operands, 16384 x 8192 x 2048 bf16 746 -> 713 us; f32's 81 -> 88)
@@ -50,6 +55,7 @@ struct PutPre {
     const bool whole = kWhole || col + 8 <= f;
     const Row8 g = __builtin_convertvector(p.g, Row8), u = __builtin_convertvector(p.u, Row8);
     Row8 dg, du, v;
+    if (kScaled) dh *= p.by;
 #pragma unroll
     for (uint32_t e = 0; e < 8; ++e) {
       float a, da;
@@ -58,6 +64,23 @@ struct PutPre {
       dg[e] = in ? dh[e] * u[e] * da : 0.0f;
       du[e] = in ? dh[e] * a : 0.0f;
       v[e] = in ? a * u[e] : 0.0f;
+    }
+    if (kScaled && scale != nullptr) {
+      float most = 0.0f;  // (NaN loses)
+#pragma unroll
+      for (uint32_t e = 0; e < 8; ++e) most = fmaxf(most, fmaxf(fabsf(dg[e]), fabsf(du[e])));
+      if (most >= kEnd) {
+        const float end = kEnd * p.by;
+        bool past = false;
+#pragma unroll
+        for (uint32_t e = 0; e < 8; ++e)
+          past = past || (fabsf(dg[e]) >= kEnd && fabsf(dg[e]) < end) ||
+                 (fabsf(du[e]) >= kEnd && fabsf(du[e]) < end);
+        if (past) {  // (every thread that does writes the same)
+          scale->back = 1.0f;
+          scale->past = 1u;
+        }
+      }
     }
     uint16_t *const to = d_pre + row * d_ld + col;
     put_operand<O>(to, d_plane, dg);
@@ -85,9 +108,14 @@ hipError_t launch_d_pre(const DPre &d, hipStream_t stream) {
     typedef decltype(o) O;
     typedef decltype(t) T;
     return with_act(d.act, [&](auto a) {
-      const PutPre<O, decltype(a)::value> put = {static_cast<const O *>(d.pre), d.pre_ld, d.d_pre, d.h,
-                                                 d.d_ld, d.h_ld, d.d_plane, d.h_plane, d.f, d.half};
-      return launch_product<T, kAlongK, kAcrossK, false>(d.product, d.shape, put, d.parts, stream);
+      PutPre<O, decltype(a)::value> put = {static_cast<const O *>(d.pre), d.pre_ld, d.d_pre, d.h, d.d_ld,
+                                           d.h_ld, d.d_plane, d.h_plane, d.f, d.half, d.scale};
+      hipError_t e = launch_product<T, kAlongK, kAcrossK, false>(d.product, d.shape, put, d.parts, stream);
+      if (e != hipSuccess || d.scale == nullptr) return e;
+      Args again = d.product;
+      again.only = &d.scale->past;
+      put.scale = nullptr;
+      return launch_product<T, kAlongK, kAcrossK, false>(again, d.shape, put, d.parts, stream);
     });
   });
 }

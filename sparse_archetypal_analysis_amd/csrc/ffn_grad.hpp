@@ -8,6 +8,8 @@ namespace seacells {
 
 // dh = d_out w_out (product, shape) turned into d_pre and h. (A source of its
 // own: its kernels take longer to compile than all the others of the gradient.)
+// With a scale d_pre is held times it; where that takes a number past f16 that
+// f16 holds without, all of d_pre is done again without and the scale is 1.
 struct DPre {
   uint32_t dtype;
   Act act;
@@ -19,6 +21,7 @@ struct DPre {
   uint64_t d_ld, h_ld, d_plane, h_plane;
   uint32_t f, half;
   float *parts;
+  mm::Scale *scale;  // f16, or nullptr
 };
 hipError_t launch_d_pre(const DPre &d, hipStream_t stream);
 

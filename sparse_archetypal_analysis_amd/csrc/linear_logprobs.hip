@@ -198,14 +198,14 @@ struct Looked {
 };
 
 // By one thread, from the maximum over all rows.
-__device__ __forceinline__ void put_scale(Looked all, float *__restrict__ scale,
+__device__ __forceinline__ void put_scale(Looked all, Scale *__restrict__ scale,
                                           uint32_t *__restrict__ status) {
   *status = all.bad ? kFlagBadIndex : 0u;
   // 32 most < 2^(e + 1), e <= 132; powers from 2^-118 to 2^100 keep both factors normal
   int e = (int)((__float_as_uint(all.most) >> 23) & 255u) - 122;
   e = all.most > 0.0f ? min(14 - e, 100) : 0;
-  scale[0] = __uint_as_float((uint32_t)(e + 127) << 23);
-  scale[1] = __uint_as_float((uint32_t)(127 - e) << 23);
+  scale->by = __uint_as_float((uint32_t)(e + 127) << 23);
+  scale->back = __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
 __global__ __launch_bounds__(kPrepare) void scale_rows(const int32_t *__restrict__ targets,
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(kPrepare) void scale_rows(const int32_t *__restrict
                                                        const float *__restrict__ d_entropy,
                                                        uint32_t n, uint32_t v,
                                                        Looked *__restrict__ parts,
-                                                       float *__restrict__ scale,
+                                                       Scale *__restrict__ scale,
                                                        uint32_t *__restrict__ status) {
   float most = 0.0f;
   bool bad = false;
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(kPrepare) void scale_rows(const int32_t *__restrict
 }
 
 __global__ __launch_bounds__(kWave) void join_scale(const Looked *__restrict__ parts, uint32_t count,
-                                                    float *__restrict__ scale,
+                                                    Scale *__restrict__ scale,
                                                     uint32_t *__restrict__ status) {
   float most = 0.0f;
   bool bad = false;
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(kWave) void join_scale(const Looked *__restrict__ p
   if (threadIdx.x == 0) put_scale(Looked{most, any}, scale, status);
 }
 
-hipError_t launch_scale(const LossGradCall &c, Looked *parts, float *scale, uint32_t *status,
+hipError_t launch_scale(const LossGradCall &c, Looked *parts, Scale *scale, uint32_t *status,
                         hipStream_t stream) {
   const uint32_t blocks = c.n <= kOneBlock ? 1 : min(div_up(c.n, kPrepare), kScaleBlocks);
   scale_rows<<<blocks, kPrepare, 0, stream>>>(c.targets, c.stats, c.d_logp, c.d_entropy, c.n, c.v, parts,
@@ -270,7 +270,8 @@ template <class O>
 struct PutDz {
   const float *bias;  // of the piece
   const int32_t *targets;
-  const float *stats, *entropy, *d_logp, *d_entropy, *scale;
+  const float *stats, *entropy, *d_logp, *d_entropy;
+  const Scale *scale;  // or nullptr
   uint16_t *dz;
   uint64_t ld, plane;
   float *column_sums;  // [half tiles of rows][ld], or nullptr
@@ -288,7 +289,7 @@ struct PutDz {
     for (uint32_t j = 0; j < kSub; ++j)
 #pragma unroll
       for (uint32_t e = 0; e < 4; ++e) sum[j][e] = 0.0f;
-    const float by = scale != nullptr ? scale[0] : 1.0f;
+    const float by = scale != nullptr ? scale->by : 1.0f;
     // the rows' figures, all in flight together
     float m[kSub], ls[kSub], g[kSub], h[kSub], gh[kSub];
     uint32_t hit[kSub];
@@ -376,21 +377,6 @@ struct PutDz {
   }
 };
 
-// Results of d_z times its scale to the caller's rows.
-template <class O>
-struct ToScaledRows {
-  typedef void Ahead;
-  O *out;
-  uint64_t ld;
-  uint32_t n;
-  const float *scale;  // or nullptr
-  template <bool kWhole>
-  __device__ __forceinline__ void put(uint32_t row, uint32_t col, Row8 v) const {
-    if (scale != nullptr) v *= scale[1];
-    put_row<kWhole>(out + row * ld, col, n, v);
-  }
-};
-
 // d_bias of a piece: the tiles' column sums, 16 columns and 16 parts of the
 // tiles a block, then the parts in order.
 __global__ __launch_bounds__(kThreads) void join_columns(const float *__restrict__ sums,
@@ -468,7 +454,8 @@ struct LossGradRoom {
   Matrix x, table;
   uint16_t *dz;
   uint64_t dz_ld;
-  float *parts, *columns, *scale;  // (f16's scale)
+  float *parts, *columns;
+  Scale *scale;  // (f16)
   Looked *looked;
   Pack3 list = {};
   Shape z, dx, dt;
@@ -504,9 +491,9 @@ LossGradRoom lay_out_grad(const LossGradCall &c, bool x_stays, bool table_stays,
     room.used -= align_up(b, 256);
     r.columns = static_cast<float *>(room.take(s));
   }
-  r.scale = static_cast<float *>(room.take(8));
+  r.scale = static_cast<Scale *>(room.take(sizeof(Scale)));
   r.looked = static_cast<Looked *>(
-      room.take(static_cast<Dtype>(c.dtype) == Dtype::f16 ? kScaleBlocks * sizeof(Looked) : 0));
+      room.take(is_f16(c.dtype) ? kScaleBlocks * sizeof(Looked) : 0));
   r.bytes = room.used;
   return r;
 }
@@ -592,8 +579,8 @@ hipError_t launch_loss_grad(const LossGradCall &c, void *d_x, uint64_t d_x_ld, v
                                       d_bias != nullptr, ws);
   hipError_t e = launch_pack(r.list, c.dtype, stream);
   if (e != hipSuccess) return e;
-  const bool scaled = static_cast<Dtype>(c.dtype) == Dtype::f16;
-  float *const scale = scaled ? r.scale : nullptr;
+  const bool scaled = is_f16(c.dtype);
+  Scale *const scale = scaled ? r.scale : nullptr;
   const bool apart = scaled || c.targets == nullptr || c.n > 32768;
   if (scaled) {
     e = launch_scale(c, r.looked, scale, status, stream);

@@ -33,7 +33,13 @@ struct Args {
   uint32_t per_split;         // tiles of a part of k (tiles: one part)
   uint32_t tiles_m, tiles_n;
   uint64_t a_off[kMaxSegs], b_off[kMaxSegs];
+  const uint32_t *only;  // or nullptr: left out where this is 0 (products that may_skip)
 };
+
+// The products whose launch the device may leave out: f16's of dh (the check at
+// the start of all of them cost bf16's gradients 0.5 to 2 %).
+template <class T, Side kA, Side kB>
+constexpr bool may_skip = std::is_same<T, _Float16>::value && kA == kAlongK && kB == kAcrossK;
 
 // f(0), f(1), ... as constants.
 template <class F, uint32_t... kI>
@@ -261,6 +267,9 @@ __global__ __launch_bounds__(kThreads, kTile == 256 ? 1 : 2) void product(Args g
   constexpr uint32_t kOdd = LaneA::kLoads + LaneB::kLoads;
   constexpr bool kAnyPairs = LaneA::kPairs || LaneB::kPairs;
   __shared__ __attribute__((aligned(1024))) char ring[LaneA::kBytes + LaneB::kBytes];
+  if constexpr (may_skip<T, kA, kB>) {
+    if (g.only != nullptr && *g.only == 0) return;
+  }
 
   const uint32_t wave = threadIdx.x / kWave;
   const uint32_t wm = wave & 1, wn = wave >> 1;
@@ -587,7 +596,9 @@ struct Parts {
 template <bool kGated, uint32_t kLanes, class Put>
 __global__ __launch_bounds__(kThreads) void join_parts(const float *__restrict__ parts,
                                                        uint32_t count, uint32_t m, uint32_t n,
-                                                       uint32_t wide, Put put) {
+                                                       uint32_t wide, Put put,
+                                                       const uint32_t *__restrict__ only) {
+  if (only != nullptr && *only == 0) return;
   const uint32_t chunks = (n + 7) / 8, lane = threadIdx.x % kLanes;
   const uint64_t id = (uint64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
   const bool in = id < (uint64_t)m * chunks;
@@ -621,14 +632,14 @@ __global__ __launch_bounds__(kThreads) void join_parts(const float *__restrict__
 
 template <bool kGated, class Put>
 hipError_t launch_join(const float *parts, uint32_t count, uint32_t m, uint32_t n, uint32_t wide,
-                       const Put &put, hipStream_t stream) {
+                       const Put &put, hipStream_t stream, const uint32_t *only = nullptr) {
   const uint64_t chunks = (uint64_t)m * ((n + 7) / 8);
   if (count >= 8 && chunks < (1u << 15))
     join_parts<kGated, 8><<<(uint32_t)((chunks + kThreads / 8 - 1) / (kThreads / 8)), kThreads, 0, stream>>>(
-        parts, count, m, n, wide, put);
+        parts, count, m, n, wide, put, only);
   else
     join_parts<kGated, 1><<<(uint32_t)((chunks + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
-        parts, count, m, n, wide, put);
+        parts, count, m, n, wide, put, only);
   return hipGetLastError();
 }
 
@@ -823,7 +834,7 @@ hipError_t launch_product(const Args &g, const Shape &s, const Put &put, float *
   const uint32_t wide = up8(g.n) * (kGated ? 2 : 1);
   hipError_t e = launch_tiles<T, kA, kB, kGated>(g, s, Parts{parts, g.m, g.n, wide, false}, stream);
   if (e != hipSuccess) return e;
-  return launch_join<kGated>(parts, s.parts, g.m, g.n, wide, put, stream);
+  return launch_join<kGated>(parts, s.parts, g.m, g.n, wide, put, stream, g.only);
 }
 
 // Results of type O to the caller's rows (any element-aligned address).
@@ -842,6 +853,30 @@ struct ToRows {
   uint32_t n;
   template <bool kWhole>
   __device__ __forceinline__ void put(uint32_t row, uint32_t col, Row8 v) const {
+    put_row<kWhole>(out + row * ld, col, n, v);
+  }
+};
+
+// f16's range is narrow: what it holds between two products is times a power of
+// two, here with its inverse (on the device).
+struct Scale {
+  float by, back;
+  uint32_t past;  // something got past f16 by it (the block's gradient)
+};
+
+inline bool is_f16(uint32_t dtype) { return static_cast<Dtype>(dtype) == Dtype::f16; }
+
+// Products of one to the caller's rows.
+template <class O>
+struct ToScaledRows {
+  typedef void Ahead;
+  O *out;
+  uint64_t ld;
+  uint32_t n;
+  const Scale *scale;  // or nullptr
+  template <bool kWhole>
+  __device__ __forceinline__ void put(uint32_t row, uint32_t col, Row8 v) const {
+    if (scale != nullptr) v *= scale->back;
     put_row<kWhole>(out + row * ld, col, n, v);
   }
 };
