@@ -5,8 +5,9 @@ training pairs, and the archetype of the neighbour is the class to predict.
     loss   = mean over pairs of -log p[archetype] - beta * entropy
 
 It runs the token operators (include/seacells_token.h) as a training step does,
-forward and backward, and as a serving step does, with the top alternatives of
-a few cells. The matrix products are torch's.
+forward and backward, with the loss straight from the hidden rows (no logits in
+memory), and as a serving step does, with the top alternatives of a few cells
+(their logits are torch's product).
 
     python -m examples.archetype_tokens [--config c1] [--width 64] [--steps 200]
 """
@@ -37,34 +38,33 @@ class Model:
 
 
 def forward(model, cells):
-    """(embedded rows, normalised rows, mean, rstd, logits, status) of int32 cells."""
+    """(embedded rows, normalised rows, mean, rstd, status) of int32 cells."""
     x, status = saa.seacells_embed(model.table, cells, model.scale)
     h, mean, rstd = saa.seacells_layer_norm(x, model.weight, model.bias)
-    return x, h, mean, rstd, h @ model.head.t(), status
+    return x, h, mean, rstd, status
 
 
 def training_step(model, cells, archetypes, beta=0.0):
     """Loss (on the device), gradients by parameter and the step's status words.
     A negative archetype leaves its pair out of the loss' first term."""
-    x, h, mean, rstd, logits, s0 = forward(model, cells)
-    logp, entropy, stats, _, _, s1 = saa.seacells_logprobs(logits, archetypes)
+    x, h, mean, rstd, s0 = forward(model, cells)
+    logp, entropy, stats, s1 = saa.seacells_linear_logprobs(h, model.head, archetypes)
     kept = (archetypes >= 0).sum().clamp(min=1).float()
     loss = -logp.sum() / kept - beta * entropy.mean()
     d_logp = (-1.0 / kept).expand(cells.numel()).contiguous()
     d_entropy = torch.full_like(d_logp, -beta / max(cells.numel(), 1))
-    d_logits, s2 = saa.seacells_logprobs_grad(logits, archetypes, stats, entropy, d_logp, d_entropy,
-                                              d_logits=logits)
-    d_x, d_weight, d_bias = saa.seacells_layer_norm_grad(d_logits @ model.head, x, mean, rstd,
-                                                         model.weight)
+    d_h, d_head, _, s2 = saa.seacells_linear_logprobs_grad(h, model.head, archetypes, stats, entropy,
+                                                           d_logp, d_entropy)
+    d_x, d_weight, d_bias = saa.seacells_layer_norm_grad(d_h, x, mean, rstd, model.weight)
     d_table, s3 = saa.seacells_embed_grad(cells, d_x, model.table.shape[0], model.scale)
-    grads = {"table": d_table, "weight": d_weight, "bias": d_bias, "head": d_logits.t() @ h}
+    grads = {"table": d_table, "weight": d_weight, "bias": d_bias, "head": d_head}
     return loss, grads, (s0, s1, s2, s3)
 
 
 def answer(model, cells, top_k=5):
     """The top_k likeliest archetypes of a few cells and their log probabilities."""
-    _, _, _, _, logits, status = forward(model, cells)
-    _, _, _, top, logp, s1 = saa.seacells_logprobs(logits, None, top_k)
+    _, h, _, _, status = forward(model, cells)
+    _, _, _, top, logp, s1 = saa.seacells_logprobs(h @ model.head.t(), None, top_k)
     return top, logp, (status, s1)
 
 
