@@ -3,6 +3,8 @@
 // internal interface of those for few rows. Nothing here is exported.
 #pragma once
 
+#include <type_traits>
+
 #include "token.hpp"
 
 namespace seacells {
@@ -19,7 +21,8 @@ __device__ __forceinline__ float sigmoid(float g) {
 
 // The normal distribution's integral and density (times sqrt(2 pi)) at g:
 // erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2), t = 1 / (1 + p x), to 1.5e-7
-// (Abramowitz and Stegun, 7.1.26), mirrored for g > 0.
+// (Abramowitz and Stegun, 7.1.26), mirrored for g > 0. (act(g) in f32 is off by
+// up to 2.1e-7, about twice what an erf rounded to f32 gives.)
 __device__ __forceinline__ float normal(float g, float *density) {
   const float x = fabsf(g) * 0.70710678118654752440f;
   const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
@@ -53,6 +56,19 @@ __device__ __forceinline__ void act_both(float g, float *a, float *da) {
   } else {
     *a = act<Act::relu>(g);
     *da = g > 0.0f ? 1.0f : (g <= 0.0f ? 0.0f : g);
+  }
+}
+
+// Calls f with the activation as a constant.
+template <class F>
+hipError_t with_act(Act a, F &&f) {
+  switch (a) {
+    case Act::silu:
+      return f(std::integral_constant<Act, Act::silu>{});
+    case Act::gelu:
+      return f(std::integral_constant<Act, Act::gelu>{});
+    default:
+      return f(std::integral_constant<Act, Act::relu>{});
   }
 }
 
@@ -94,7 +110,9 @@ __device__ __forceinline__ Sums joined(Sums a, Sums b) {
 // bf16 16 rows 54 and 66, 32 rows 65 and 67; 2048 x 16384 32 rows 87 and 67;
 // 1024 x 4096 32 rows 20 and 25, 64 rows 30 and 26; f32 64 rows 57 and 70, 206
 // and 445. Log probabilities of 512 x 50001 bf16 16 rows 22 and 20, 32 rows 30
-// and 20; 100 x 1300 64 rows 12 and 14; f32 64 rows 81 and 96, 14 and 19.
+// and 20; 100 x 1300 64 rows 12 and 14; f32 64 rows 81 and 96, 14 and 19. f32
+// with few results and a long k, which one block walks alone, loses by the rule:
+// 512 x 16384 64 rows 179, by tiles 65 rows 104.
 inline bool few_rows(uint32_t dtype, uint32_t n, uint64_t elements, bool block) {
   if (n <= 16 || (n <= 64 && dtype == 0u)) return true;
   return block ? n <= 32 && elements <= (1u << 24) : n <= 64 && elements <= (1u << 18);

@@ -43,23 +43,11 @@ struct PutGated {
   }
 };
 
-template <class F>
-hipError_t with_act(Act a, F &&f) {
-  switch (a) {
-    case Act::silu:
-      return f(std::integral_constant<Act, Act::silu>{});
-    case Act::gelu:
-      return f(std::integral_constant<Act, Act::gelu>{});
-    default:
-      return f(std::integral_constant<Act, Act::relu>{});
-  }
-}
-
 struct FfnRoom {
   Matrix x, w_in, w_out;
   uint16_t *h;
   float *parts;
-  Pack3 list = {};
+  PackList list = {};
   Shape in, out;
   size_t bytes;
 };

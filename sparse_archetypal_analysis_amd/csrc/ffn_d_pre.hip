@@ -89,18 +89,6 @@ struct PutPre {
   }
 };
 
-template <class F>
-hipError_t with_act(Act a, F &&f) {
-  switch (a) {
-    case Act::silu:
-      return f(std::integral_constant<Act, Act::silu>{});
-    case Act::gelu:
-      return f(std::integral_constant<Act, Act::gelu>{});
-    default:
-      return f(std::integral_constant<Act, Act::relu>{});
-  }
-}
-
 }  // namespace
 
 hipError_t launch_d_pre(const DPre &d, hipStream_t stream) {

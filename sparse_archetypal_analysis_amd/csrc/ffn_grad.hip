@@ -105,7 +105,7 @@ struct GradRoom {
   uint16_t *h, *d_pre;
   float *parts, *most;
   Scale *scale;  // (f16)
-  Pack3 list = {};
+  PackList list = {};
   Shape dh, dx, d_in, d_out_w;
   size_t bytes;
 };

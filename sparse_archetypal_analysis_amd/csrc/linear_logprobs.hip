@@ -408,13 +408,14 @@ __global__ __launch_bounds__(kThreads) void zero_table(O *out, uint64_t ld, uint
   }
 }
 
-// Rows of one launch of the forward product: its slices' sums stay below this.
+// Rows of one launch of the forward product: its slices' sums stay below this, or
+// are those of 4096 rows where that is more (above 700k classes; 3.2 GB at 2^23).
 constexpr uint64_t kSumsBytes = 512ull << 20;
 
 struct LossRoom {
   Matrix x, table;
   float *sums, *at_target;
-  Pack3 list = {};
+  PackList list = {};
   Shape shape;
   uint32_t rows;  // of a launch
   size_t bytes;
@@ -446,8 +447,8 @@ LossRoom lay_out(const LossCall &c, bool x_stays, bool table_stays, void *ws) {
   return r;
 }
 
-// Classes of a piece: d_z of one stays below this (and the rows' whole length
-// below that where they are few).
+// Classes of a piece: d_z of one stays below this, or has 256 classes where that
+// is more (from 2^19 16-bit rows on, a third of that in f32).
 constexpr uint64_t kPieceBytes = 256ull << 20;
 
 struct LossGradRoom {
@@ -457,7 +458,7 @@ struct LossGradRoom {
   float *parts, *columns;
   Scale *scale;  // (f16)
   Looked *looked;
-  Pack3 list = {};
+  PackList list = {};
   Shape z, dx, dt;
   uint32_t piece;  // classes
   size_t bytes;

@@ -9,7 +9,7 @@ namespace {
 // 8 elements a thread: rows of any stride and alignment to rows on 16 bytes
 // with zeros behind them (f32: to planes). Bound by memory.
 template <class O>
-__global__ __launch_bounds__(kThreads) void pack_rows(Pack3 list) {
+__global__ __launch_bounds__(kThreads) void pack_rows(PackList list) {
   const PackItem &it = list.item[blockIdx.y];
   for (uint64_t id = (uint64_t)blockIdx.x * kThreads + threadIdx.x; id < it.chunks;
        id += (uint64_t)gridDim.x * kThreads) {
@@ -32,7 +32,7 @@ __global__ __launch_bounds__(kThreads) void pack_rows(Pack3 list) {
 
 }  // namespace
 
-hipError_t launch_pack(const Pack3 &list, uint32_t dtype, hipStream_t stream) {
+hipError_t launch_pack(const PackList &list, uint32_t dtype, hipStream_t stream) {
   uint64_t most = 0;
   for (uint32_t i = 0; i < list.count; ++i)
     if (list.item[i].chunks > most) most = list.item[i].chunks;

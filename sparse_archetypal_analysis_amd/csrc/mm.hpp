@@ -725,11 +725,11 @@ struct PackItem {
   uint64_t to_ld, plane;
   uint32_t row_chunks, len;
 };
-struct Pack3 {
+struct PackList {
   PackItem item[4];
   uint32_t count;
 };
-hipError_t launch_pack(const Pack3 &items, uint32_t dtype, hipStream_t stream);
+hipError_t launch_pack(const PackList &items, uint32_t dtype, hipStream_t stream);
 
 // Takes the next free piece of a workspace (or only counts).
 struct Room {
@@ -744,7 +744,7 @@ struct Room {
 
 // The caller's matrix, or room for its copy (added to the list).
 inline Matrix operand(const void *p, uint32_t dtype, uint64_t ld, uint32_t rows, uint32_t len,
-                      bool stays, Room &room, Pack3 &list) {
+                      bool stays, Room &room, PackList &list) {
   if (stays) return Matrix{static_cast<const uint16_t *>(p), ld, 0};
   const uint32_t wide = apart64(len), chunks = up8(len) / 8;
   const uint64_t plane = (uint64_t)rows * wide;
