@@ -188,9 +188,9 @@ __global__ __launch_bounds__(kPrepare) void report_targets(const int32_t *__rest
 // depend on choose nothing: d_logp of ignored targets, both of rows with nothing
 // left or without a distribution. Targets past the classes are reported in the
 // same pass. The maximum is of 1/32 of the bound, so that it is finite for any
-// finite gradients. One block up to kOneBlock rows, more blocks in two launches (gradient
-// of 64 x 1300, us in one and two: 3001 rows 45.2 and 46.4, 8192 rows 57.2 and
-// 54.4, 131072 rows 498 and 387).
+// finite gradients. One block up to kOneBlock rows, more blocks in two launches
+// (gradient of 64 x 1300, us in one and two: 3001 rows 45.2 and 46.4, 8192 rows
+// 57.2 and 54.4, 131072 rows 498 and 387).
 constexpr uint32_t kOneBlock = 4096, kScaleBlocks = 128;
 struct Looked {
   float most;
